@@ -54,6 +54,8 @@ extern "C" {
 #define TV_DEV_TIMEOUT 16       /* a pipeline wait in a kernel exceeded 2 s     */
 #define TV_DEV_BAD_BLOCK 32     /* a block-table entry a prefix position uses is outside
                                    [0, num_blocks): those keys and values read as zeros */
+#define TV_DEV_BAD_OFFSETS 64   /* token offsets that decrease or leave [0, T]: that
+                                   request gets no tokens                        */
 
 /* ---- element types ------------------------------------------------------ */
 #define TV_F32 0
@@ -528,6 +530,53 @@ int tv_kv_commit(void* k_cache, void* v_cache, int64_t num_blocks, int32_t block
                  const int32_t* path, int32_t path_cols, const int32_t* n_out, int32_t B,
                  int32_t N, int32_t Hkv, int32_t head_dim, int32_t dtype, int32_t* status,
                  void* stream);
+
+/*
+ * tv_kv_append -- device, asynchronous.  Puts new tokens' keys and values into
+ * the paged cache -- a batch of prompts or of single tokens -- with the keys
+ * and, when given, the queries rotated at their positions on the way.  Token j
+ * of request b sits at position L_b + j: its K row R(L_b + j) k and V row v, every
+ * KV head, go to block block_table[b, (L_b + j) / block_size], slot
+ * (L_b + j) % block_size, in the bits tv_rope_apply would give ("Tree
+ * Verification", "The Cost Side": the cached prefix keys are stored rotated).
+ * No page defines the call: it is what fills the prefix that
+ * tv_tree_attn_verify and tv_decode_attn read.
+ *
+ * q         device [T, Hq, head_dim] (dtype), nullable; q_stride elements
+ *           between tokens (heads of a token contiguous).  Left as it is.
+ * q_out     device [T, Hq, head_dim] (dtype) out, q_out_stride elements between
+ *           tokens: the rotated queries.  May be q itself (with the same
+ *           stride); a partial overlap is undefined.  Needs cos_sin.
+ * k_new,    device [T, Hkv, head_dim] (dtype), k_stride / v_stride elements
+ * v_new     between tokens (>= 0): slices of one projection's rows fit.
+ * cu_new    device int32 [B + 1] (nullable): request b's tokens are the packed
+ *           rows cu_new[b] .. cu_new[b + 1] - 1 (non-decreasing, within [0, T]; a
+ *           request may have none; rows of no request are not read, and their
+ *           q_out rows are left as they are).  NULL: T / B rows each, in order.
+ * k_cache, v_cache, block_table: as in tv_kv_commit; the caller has placed
+ *           blocks for the new positions.  Distinct tokens go to distinct slots.
+ * seq_lens  device int32 [B]: L_b before the call (read).
+ * new_seq_lens device int32 [B] out (nullable, must not alias seq_lens): L_b +
+ *           the request's tokens, or L_b + j when token j is the first that
+ *           cannot be placed (below).
+ * cos_sin   device float32 [max_pos, 2, head_dim/2] from tv_rope_table (nullable:
+ *           keys are stored as given).
+ * A request with bad offsets (TV_DEV_BAD_OFFSETS) or L_b < 0
+ * (TV_DEV_BAD_POSITION) gets no tokens.  A token whose position is outside the
+ * rotary table (TV_DEV_BAD_POSITION) or has no valid block in the table
+ * (TV_DEV_OUT_OVERFLOW) is not stored and ends the returned length there;
+ * a later token whose own block is valid may be stored past that length.
+ * q_out rows are written for every token whose position is in the rotary table.
+ * head_dim in {16, 32, 64, 128, 256}; every buffer and token stride a multiple
+ * of 16 bytes (else TV_ERR_INVALID_ARG).
+ */
+int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t Hq,
+                 const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                 const int32_t* cu_new, int32_t T, void* k_cache, void* v_cache,
+                 int64_t num_blocks, int32_t block_size, const int32_t* block_table,
+                 int32_t max_blocks, const int32_t* seq_lens, int32_t* new_seq_lens,
+                 const float* cos_sin, int32_t max_pos, int32_t B, int32_t Hkv,
+                 int32_t head_dim, int32_t dtype, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

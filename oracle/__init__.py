@@ -18,7 +18,7 @@ Everything is written as the plain definition the pages give, in float64
                      page, the tree walk with sibling residual updates, and
                      the fixed-point inverse-CDF sampler they share.
 * ``kvcache``     -- commit of the accepted path's tree K/V into the paged
-                     cache.
+                     cache, and appending of new tokens' K/V to it.
 
 Every function is pinned by ``tests/test_oracle_*.py`` (``-m "not gpu"``)
 against facts the pages print or mathematics fixes; no function here is

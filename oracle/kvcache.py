@@ -1,5 +1,5 @@
-"""Oracle: commit of the accepted path's tree K/V to the paged cache (test
-infrastructure).
+"""Oracle: commit of the accepted path's tree K/V to the paged cache, and
+appending of new tokens' K/V (test infrastructure).
 
 Definition followed
 -------------------
@@ -32,6 +32,8 @@ from __future__ import annotations
 
 import numpy as np
 
+from .attention import rope
+
 
 def commit_path(k_cache, v_cache, block_table, seq_lens, k_tree, v_tree, path, n_out, stop_at_bad=False):
     """Returns (k_cache', v_cache', seq_lens') with the accepted rows copied in.
@@ -63,3 +65,41 @@ def commit_path(k_cache, v_cache, block_table, seq_lens, k_tree, v_tree, path, n
             vc[blk, :, t % bs, :] = v_tree[b, node]
         lens[b] = L + done
     return kc, vc, lens
+
+
+def append_tokens(k_cache, v_cache, block_table, seq_lens, k_new, v_new, counts, q=None, rope_base=None,
+                  max_pos=None):
+    """New tokens' K/V appended to the paged cache: request b takes the next
+    ``counts[b]`` rows of k_new / v_new [T, Hkv, D], row j at position
+    ``L_b + j``, keys (and queries q [T, Hq, D]) rotated there when
+    ``rope_base`` is given.  Returns (k_cache', v_cache', seq_lens', q').
+
+    A token whose position is outside the rotary table (``max_pos`` rows) or
+    without a valid block is not stored and ends the returned length; later
+    tokens with a valid block are stored (their slots lie past the length).
+    Queries past the table, and rows behind the last request, stay as given.
+    """
+    kc = np.array(k_cache, dtype=np.float64)
+    vc = np.array(v_cache, dtype=np.float64)
+    qo = None if q is None else np.array(q, dtype=np.float64)
+    lens = np.array(seq_lens, dtype=np.int64, copy=True)
+    bs = kc.shape[2]
+    t = 0
+    for b in range(lens.size):
+        L, done = int(seq_lens[b]), None
+        for j in range(int(counts[b])):
+            pos = L + j
+            ok = 0 <= L and (max_pos is None or pos < max_pos)
+            if ok and qo is not None:
+                qo[t] = rope(q[t], np.full(qo.shape[1], pos), rope_base)
+            ok = ok and pos // bs < block_table.shape[1] and 0 <= int(block_table[b, pos // bs]) < kc.shape[0]
+            if ok:
+                blk = int(block_table[b, pos // bs])
+                k = k_new[t] if rope_base is None else rope(k_new[t], np.full(kc.shape[1], pos), rope_base)
+                kc[blk, :, pos % bs, :] = k
+                vc[blk, :, pos % bs, :] = v_new[t]
+            elif done is None:
+                done = j
+            t += 1
+        lens[b] = L + (int(counts[b]) if done is None else done)
+    return kc, vc, lens, qo

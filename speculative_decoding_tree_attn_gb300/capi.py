@@ -28,6 +28,7 @@ TV_ATTN_WORKSPACE_ZEROED = 32
 TV_SAMPLE_AUTO, TV_SAMPLE_CLUSTER, TV_SAMPLE_SINGLE_CTA, TV_SAMPLE_STREAM, TV_SAMPLE_GRID = 0, 1, 2, 3, 4
 TV_DEV_BAD_TOPOLOGY, TV_DEV_BAD_TOKEN, TV_DEV_OUT_OVERFLOW, TV_DEV_BAD_POSITION, TV_DEV_TIMEOUT = 1, 2, 4, 8, 16
 TV_DEV_BAD_BLOCK = 32
+TV_DEV_BAD_OFFSETS = 64
 STATUS_NAMES = {0: "TV_OK", -1: "TV_ERR_INVALID_ARG", -2: "TV_ERR_MISSING_PARENT", -3: "TV_ERR_TOO_MANY_NODES",
                 -4: "TV_ERR_UNSUPPORTED", -5: "TV_ERR_WORKSPACE", -6: "TV_ERR_CUDA"}
 
@@ -60,6 +61,8 @@ SIGNATURES = {
                                               _P, _P]),
     "tv_kv_commit": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32,
                                     _I32, _I32, _P, _P]),
+    "tv_kv_append": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _I64, _I32, _P,
+                                    _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
 }
 
 
@@ -116,6 +119,44 @@ def _dev(t, name, dtypes):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+def _dev_rows(t, name, dtype, tail):
+    """A CUDA tensor [T, *tail] of dtype whose rows are contiguous (any stride between them)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != 3 or t.shape[1:] != tail:
+        raise ValueError(f"{name} must be {dtype} [T, {tail[0]}, {tail[1]}], got {t.dtype} {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 and tail[1] > 1 or t.stride(1) != tail[1] and tail[0] > 1):
+        raise ValueError(f"{name} must have contiguous rows")
+    return t
+
+
+def _dev_shaped(t, name, dtype, shape):
+    """A contiguous CUDA tensor of exactly this dtype and shape."""
+    _dev(t, name, (dtype,))
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _one_device(*tensors):
+    """Every tensor lives on the current device (whose stream the call uses)."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"tensor on {t.device}, current device is cuda:{cur}")
+
+
+def _dev_cache(k_cache, v_cache, block_table, B):
+    """Checks a paged cache [num_blocks, Hkv, block_size, D] and its block table [B, max_blocks]."""
+    _dev(k_cache, "k_cache", (torch.float32, torch.bfloat16))
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [num_blocks, Hkv, block_size, D], got {tuple(k_cache.shape)}")
+    _dev_shaped(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
+    _dev(block_table, "block_table", (torch.int32,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
 
 
 def _code(dtype):
@@ -473,3 +514,51 @@ def tv_kv_commit(k_cache, v_cache, block_table, seq_lens, k_tree, v_tree, path, 
                               path.shape[1], _ptr(n_out), B, N, Hkv, D, _code(k_cache.dtype), _ptr(status),
                               _stream(stream)))
     return new_seq_lens
+
+
+def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_sin=None, q=None, q_out=None,
+                 cu_new=None, new_seq_lens=None, status=None, stream=None):
+    """Put new tokens' K/V rows [T, Hkv, D] into the paged cache (in place), keys
+    rotated with cos_sin (None: stored as given) at the positions that follow
+    seq_lens; q [T, Hq, D] is rotated into q_out (may be q).  Rows of k_new, v_new,
+    q and q_out may be strided.  cu_new int32 [B + 1]: packed offsets; None: T / B
+    tokens each.  Returns (q_out, new_seq_lens int32 [B])."""
+    _dev(seq_lens, "seq_lens", (torch.int32,))
+    B = seq_lens.numel()
+    _dev_cache(k_cache, v_cache, block_table, B)
+    num_blocks, Hkv, bs, D = k_cache.shape
+    dt = k_cache.dtype
+    _dev_rows(k_new, "k_new", dt, (Hkv, D))
+    _dev_rows(v_new, "v_new", dt, (Hkv, D))
+    T = k_new.shape[0]
+    Hq = max_pos = q_stride = out_stride = 0
+    if v_new.shape[0] != T:
+        raise ValueError(f"v_new has {v_new.shape[0]} rows, k_new {T}")
+    if cos_sin is not None:
+        max_pos = cos_sin.shape[0]
+        _dev_shaped(cos_sin, "cos_sin", torch.float32, (max_pos, 2, D // 2))
+    if q is not None:
+        Hq = q.shape[1]
+        _dev_rows(q, "q", dt, (Hq, D))
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device)
+        else:
+            _dev_rows(q_out, "q_out", dt, (Hq, D))
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError(f"q and q_out must have k_new's {T} rows")
+        q_stride, out_stride = q.stride(0), q_out.stride(0)
+    if cu_new is not None:
+        _dev_shaped(cu_new, "cu_new", torch.int32, (B + 1,))
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty_like(seq_lens)
+    else:
+        _dev_shaped(new_seq_lens, "new_seq_lens", torch.int32, seq_lens.shape)
+    if status is not None:
+        _dev(status, "status", (torch.int32,))
+    _one_device(k_cache, v_cache, block_table, seq_lens, k_new, v_new, q, q_out, cos_sin, cu_new, new_seq_lens, status)
+    _check("tv_kv_append",
+           lib().tv_kv_append(_ptr(q), q_stride, _ptr(q_out), out_stride, Hq, _ptr(k_new), k_new.stride(0),
+                              _ptr(v_new), v_new.stride(0), _ptr(cu_new), T, _ptr(k_cache), _ptr(v_cache), num_blocks,
+                              bs, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(new_seq_lens),
+                              _ptr(cos_sin), max_pos, B, Hkv, D, _code(dt), _ptr(status), _stream(stream)))
+    return q_out, new_seq_lens

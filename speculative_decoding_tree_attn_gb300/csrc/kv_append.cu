@@ -1,0 +1,293 @@
+// Appending new tokens' keys and values to the paged cache, keys (and
+// queries) rotated at their positions on the way.
+//
+// Token j of request b (packed row t = cu_new[b] + j) sits at position
+// p = L_b + j: its keys R(p) k and values v go to block
+// block_table[b, p / block_size], slot p % block_size, its queries R(p) q to
+// q_out, with the rotation of rope_math.cuh (the bits of tv_rope_apply).
+// "Tree Verification", "The Cost Side": the cached prefix keys are stored
+// rotated, so the tree and one-token attention read them as they are.
+//
+// Pure movement: (Hq + 2 Hkv) D elements a token read once and written once;
+// the rotation is 3 flops an element.  Bound by HBM for a prompt, by latency
+// for a step's tokens.
+#include <algorithm>
+#include <climits>
+
+#include <cuda_bf16.h>
+
+#include "common.h"
+#include "rope_math.cuh"
+
+namespace {
+
+struct AppendParams {
+  const char* q;  // nullable
+  char* q_out;
+  const char* k;
+  const char* v;
+  int64_t q_stride, q_out_stride, k_stride, v_stride;  // bytes between tokens
+  char* k_cache;
+  char* v_cache;
+  int64_t num_blocks;
+  int block_size;
+  const int32_t* table;
+  int max_blocks;
+  const int32_t* cu;  // nullable: T / B tokens each
+  const int32_t* seq_lens;
+  int32_t* new_lens;  // nullable
+  const float* cs;    // nullable: nothing is rotated
+  int max_pos;        // rows of cs; without it the largest length an int32 holds
+  int B, T, Hq, Hkv;
+  int slices;  // warps per token
+  int32_t* status;
+};
+
+// Request and index within it of packed row t (every lane the same); false
+// for a row of no request.  Largest b with cu[b] <= t, 32 probes a round.
+__device__ __forceinline__ bool find_request(const AppendParams& p, int t, int lane, int& b, int& j) {
+  if (!p.cu) {
+    const int per = p.T / p.B;
+    b = t / per;
+    j = t - b * per;
+    return true;
+  }
+  int lo = 0, hi = p.B;  // the answer is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int64_t i = (int64_t)lo + (int64_t)step * lane;
+    const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldg(p.cu + i) <= t);
+    lo += step * (le ? 31 - __clz(le) : 0);
+    hi = min(hi, lo + step);
+  }
+  b = lo;
+  const int s0 = __ldg(p.cu + b), s1 = __ldg(p.cu + b + 1);
+  j = t - s0;
+  return s0 >= 0 && s0 <= t && t < s1 && s1 <= p.T;
+}
+
+// New length of request b: the tokens before the first that cannot be placed.
+__device__ void count_request(const AppendParams& p, int b, int lane) {
+  const int L = p.seq_lens[b];
+  int n, bad = 0;
+  if (p.cu) {
+    const int s0 = p.cu[b], s1 = p.cu[b + 1];
+    n = s1 - s0;
+    if (s0 < 0 || s1 < s0 || s1 > p.T) {
+      n = 0;
+      bad = TV_DEV_BAD_OFFSETS;
+    }
+  } else {
+    n = p.T / p.B;
+  }
+  if (L < 0) {
+    n = 0;
+    bad |= TV_DEV_BAD_POSITION;
+  }
+  if ((int64_t)L + n > p.max_pos) {
+    n = max(0, p.max_pos - L);
+    bad |= TV_DEV_BAD_POSITION;
+  }
+  if (n > 0) {
+    const int64_t c1 = ((int64_t)L + n - 1) / p.block_size;
+    for (int64_t c0 = L / p.block_size; c0 <= c1; c0 += 32) {
+      const int64_t c = c0 + lane;
+      bool miss = false;
+      if (c <= c1) {
+        const int64_t blk = c < p.max_blocks ? p.table[(int64_t)b * p.max_blocks + c] : -1;
+        miss = blk < 0 || blk >= p.num_blocks;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, miss);
+      if (m) {
+        n = (int)max((int64_t)0, (c0 + __ffs(m) - 1) * p.block_size - L);
+        bad = TV_DEV_OUT_OVERFLOW;  // reached before any position past the table
+        break;
+      }
+    }
+  }
+  if (lane == 0) {
+    if (p.new_lens) p.new_lens[b] = L + n;
+    if (bad && p.status) atomicOr(p.status, bad);
+  }
+}
+
+template <int N>
+struct Raw {
+  uint4 v[N];
+};
+
+// One warp per (token, slice of its heads): a lane keeps one chunk of 8
+// frequency pairs (elements 8c.. and 8c + D/2..), so its cos/sin entries are
+// read once for all heads.  The warps behind the tokens' take a request each
+// and count its new length.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
+  constexpr int kChunks = D / 16;
+  constexpr int kHeads = 32 / kChunks;             // heads a warp covers at once
+  constexpr int kVec = 8 * (int)sizeof(T) / 16;    // 16-byte vectors per 8 elements
+  constexpr int kRow = D * (int)sizeof(T);         // bytes of a head's row
+  constexpr int kUnroll = 4;
+  const int lane = threadIdx.x % 32;
+  const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const int64_t token_warps = (int64_t)p.T * p.slices;
+  if (w >= token_warps) {
+    if (w - token_warps < p.B) count_request(p, (int)(w - token_warps), lane);
+    return;
+  }
+  const int t = (int)(w / p.slices);
+  const int s = (int)(w - (int64_t)t * p.slices);
+  int b, j;
+  if (!find_request(p, t, lane, b, j)) return;
+  const int L = __ldg(p.seq_lens + b);
+  const int64_t pos = (int64_t)L + j;
+  if (L < 0 || pos >= p.max_pos) return;
+  const int64_t col = pos / p.block_size;
+  const int64_t slot = pos - col * p.block_size;
+  const int64_t blk = col < p.max_blocks ? __ldg(p.table + (int64_t)b * p.max_blocks + col) : -1;
+  const bool placed = blk >= 0 && blk < p.num_blocks;
+
+  const int c = lane % kChunks;
+  float co[8], si[8];
+  if (p.cs) {
+    const float* row = p.cs + pos * D + c * 8;
+    Vec8<float>::load(row, co);
+    Vec8<float>::load(row + D / 2, si);
+  }
+  const int Hq = p.q ? p.Hq : 0;
+  const int H = Hq + 2 * p.Hkv;
+  const int rounds = (H + kHeads - 1) / kHeads;
+  const int per = (rounds + p.slices - 1) / p.slices * kHeads;
+  const int h_end = min(H, (s + 1) * per);
+  const int64_t lo = c * 8 * sizeof(T), hi = lo + kRow / 2;
+  for (int h0 = s * per + lane / kChunks; h0 < h_end; h0 += kHeads * kUnroll) {
+    Raw<kVec> x1[kUnroll], x2[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u * kHeads;
+      if (h >= h_end) break;
+      const char* src = h < Hq ? p.q + t * p.q_stride + (int64_t)h * kRow
+                      : h < Hq + p.Hkv ? p.k + t * p.k_stride + (int64_t)(h - Hq) * kRow
+                                       : p.v + t * p.v_stride + (int64_t)(h - Hq - p.Hkv) * kRow;
+      x1[u] = *reinterpret_cast<const Raw<kVec>*>(src + lo);
+      x2[u] = *reinterpret_cast<const Raw<kVec>*>(src + hi);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u * kHeads;
+      if (h >= h_end) break;
+      char* dst;
+      if (h < Hq) {
+        dst = p.q_out + t * p.q_out_stride + (int64_t)h * kRow;
+      } else {
+        if (!placed) continue;
+        const bool is_k = h < Hq + p.Hkv;
+        const int kh = h - Hq - (is_k ? 0 : p.Hkv);
+        dst = (is_k ? p.k_cache : p.v_cache) + ((blk * p.Hkv + kh) * p.block_size + slot) * kRow;
+      }
+      if (p.cs && h < Hq + p.Hkv) {
+        float a[8], d[8], y1[8], y2[8];
+        Vec8<T>::load(reinterpret_cast<const T*>(&x1[u]), a);
+        Vec8<T>::load(reinterpret_cast<const T*>(&x2[u]), d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rope_pair(a[e], d[e], co[e], si[e], y1[e], y2[e]);
+        Vec8<T>::store(reinterpret_cast<T*>(dst + lo), y1);
+        Vec8<T>::store(reinterpret_cast<T*>(dst + hi), y2);
+      } else {
+        *reinterpret_cast<Raw<kVec>*>(dst + lo) = x1[u];
+        *reinterpret_cast<Raw<kVec>*>(dst + hi) = x2[u];
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+void launch_append(AppendParams p, int sm_count, cudaStream_t stream) {
+  constexpr int kHeads = 32 / (D / 16);
+  const int rounds = ((p.q ? p.Hq : 0) + 2 * p.Hkv + kHeads - 1) / kHeads;
+  // few tokens: several warps share one, so that a step's tokens reach every SM
+  const int64_t want = (int64_t)sm_count * 16;
+  p.slices = (int)std::max<int64_t>(1, std::min<int64_t>(rounds, want / std::max(1, p.T)));
+  const int64_t warps = (int64_t)p.T * p.slices + p.B;
+  kv_append_kernel<T, D><<<(unsigned)tv::ceil_div(warps, 8), 256, 0, stream>>>(p);
+}
+
+template <typename T>
+int dispatch_append(const AppendParams& p, int D, int sm_count, cudaStream_t stream) {
+  switch (D) {
+    case 16: launch_append<T, 16>(p, sm_count, stream); break;
+    case 32: launch_append<T, 32>(p, sm_count, stream); break;
+    case 64: launch_append<T, 64>(p, sm_count, stream); break;
+    case 128: launch_append<T, 128>(p, sm_count, stream); break;
+    case 256: launch_append<T, 256>(p, sm_count, stream); break;
+    default: return tv::fail(TV_ERR_UNSUPPORTED, "tv_kv_append: head_dim %d not in {16, 32, 64, 128, 256}", D);
+  }
+  TV_LAUNCH_CHECK("kv_append_kernel");
+  return TV_OK;
+}
+
+}  // namespace
+
+extern "C" int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t Hq,
+                            const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                            const int32_t* cu_new, int32_t T, void* k_cache, void* v_cache, int64_t num_blocks,
+                            int32_t block_size, const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* seq_lens, int32_t* new_seq_lens, const float* cos_sin, int32_t max_pos,
+                            int32_t B, int32_t Hkv, int32_t head_dim, int32_t dtype, int32_t* status, void* stream) {
+  tv::clear_error();
+  if (B < 0 || T < 0 || Hkv < 1 || head_dim < 1 || block_size < 1 || max_blocks < 1 || num_blocks < 1 ||
+      (q && Hq < 1) || (cos_sin && max_pos < 1))
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: bad sizes");
+  if (dtype != TV_F32 && dtype != TV_BF16) return tv::fail(TV_ERR_UNSUPPORTED, "tv_kv_append: dtype %d", dtype);
+  if (head_dim != 16 && head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return tv::fail(TV_ERR_UNSUPPORTED, "tv_kv_append: head_dim %d not in {16, 32, 64, 128, 256}", head_dim);
+  if (B == 0) return TV_OK;
+  if (!cu_new && T % B)
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: without offsets T (%d) must be a multiple of B (%d)", T, B);
+  if (!k_cache || !v_cache || !block_table || !seq_lens || (T > 0 && (!k_new || !v_new)))
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: null pointer");
+  if (q && (!cos_sin || !q_out))
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: q needs cos_sin and q_out");
+  if (new_seq_lens && new_seq_lens == seq_lens)
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: new_seq_lens must not alias seq_lens");
+  const int64_t e = dtype == TV_F32 ? 4 : 2;
+  const int64_t kv_row = (int64_t)Hkv * head_dim, q_row = (int64_t)Hq * head_dim;
+  if (k_stride < 0 || v_stride < 0 || (q && (q_stride < 0 || (T > 1 && q_out_stride < q_row))))
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: bad token stride");
+  if ((k_stride * e) % 16 || (v_stride * e) % 16 || (q && ((q_stride * e) % 16 || (q_out_stride * e) % 16)) ||
+      ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
+        reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) | reinterpret_cast<uintptr_t>(q) |
+        reinterpret_cast<uintptr_t>(q ? q_out : nullptr) | reinterpret_cast<uintptr_t>(cos_sin)) & 15))
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: buffers and token strides must be multiples of 16 bytes");
+  if (kv_row >= INT32_MAX / 4 || (q && q_row >= INT32_MAX / 4))
+    return tv::fail(TV_ERR_UNSUPPORTED, "tv_kv_append: a token's heads exceed 2^29 elements");
+  tv::DeviceInfo dev;
+  if (int rc = tv::current_device_info(&dev)) return rc;
+  AppendParams p{};
+  p.q = static_cast<const char*>(q);
+  p.q_out = static_cast<char*>(q_out);
+  p.k = static_cast<const char*>(k_new);
+  p.v = static_cast<const char*>(v_new);
+  p.q_stride = q_stride * e;
+  p.q_out_stride = q_out_stride * e;
+  p.k_stride = k_stride * e;
+  p.v_stride = v_stride * e;
+  p.k_cache = static_cast<char*>(k_cache);
+  p.v_cache = static_cast<char*>(v_cache);
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.table = block_table;
+  p.max_blocks = max_blocks;
+  p.cu = cu_new;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_seq_lens;
+  p.cs = cos_sin;
+  p.max_pos = cos_sin ? max_pos : INT32_MAX;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.status = status;
+  cudaStream_t s = (cudaStream_t)stream;
+  return dtype == TV_BF16 ? dispatch_append<__nv_bfloat16>(p, head_dim, dev.sm_count, s)
+                          : dispatch_append<float>(p, head_dim, dev.sm_count, s);
+}

@@ -1,0 +1,77 @@
+"""Checks of the serving operators (append, one-token attention, token log
+probabilities) that need no GPU: argument errors are reported before anything
+is launched, and the oracle's definitions agree with independent ones."""
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as OA
+from oracle import kvcache as OK
+from speculative_decoding_tree_attn_gb300 import build as B
+from speculative_decoding_tree_attn_gb300 import capi
+
+FAKE = ctypes.c_void_p(4096)  # stands for a device buffer; never touched
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    if not os.path.exists(capi.LIB_PATH):
+        B.build()
+    return capi.lib()
+
+
+def _call(name, args, **change):
+    """Status of the entry point with the named arguments changed."""
+    return getattr(capi.lib(), name)(*{**args, **change}.values())
+
+
+APPEND = dict(q=FAKE, q_stride=256, q_out=FAKE, q_out_stride=256, Hq=4, k_new=FAKE, k_stride=64, v_new=FAKE,
+              v_stride=64, cu_new=None, T=6, k_cache=FAKE, v_cache=FAKE, num_blocks=9, block_size=16, table=FAKE,
+              max_blocks=4, seq_lens=FAKE, new_lens=ctypes.c_void_p(8192), cos_sin=FAKE, max_pos=100, B=3, Hkv=1,
+              head_dim=64, dtype=1, status=None, stream=None)
+
+
+@pytest.mark.parametrize("change,code,text", [
+    (dict(B=-1), -1, b"bad sizes"), (dict(T=-1), -1, b"bad sizes"), (dict(Hkv=0), -1, b"bad sizes"),
+    (dict(Hq=0), -1, b"bad sizes"), (dict(max_pos=0), -1, b"bad sizes"), (dict(num_blocks=0), -1, b"bad sizes"),
+    (dict(dtype=2), -4, b"dtype"), (dict(head_dim=48), -4, b"head_dim 48"), (dict(T=7), -1, b"multiple of B"),
+    (dict(k_cache=None), -1, b"null"), (dict(v_new=None), -1, b"null"), (dict(seq_lens=None), -1, b"null"),
+    (dict(cos_sin=None), -1, b"cos_sin"), (dict(q_out=None), -1, b"cos_sin"),
+    (dict(new_lens=FAKE), -1, b"alias"), (dict(k_stride=-64), -1, b"stride"), (dict(q_out_stride=128), -1, b"stride"),
+    (dict(k_stride=65), -1, b"16 bytes"), (dict(k_new=ctypes.c_void_p(4098)), -1, b"16 bytes"),
+])
+def test_append_refuses_on_the_host(change, code, text):
+    assert _call("tv_kv_append", APPEND, **change) == code
+    assert text in capi.lib().tv_last_error()
+
+
+def test_append_of_an_empty_batch_does_nothing():
+    assert _call("tv_kv_append", APPEND, B=0, T=0) == 0
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    t = torch.zeros(2, 1, 64)
+    cache, table, lens = torch.zeros(3, 1, 16, 64), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        capi.tv_kv_append(t, t, cache, cache, table, lens)
+
+
+def test_append_oracle_is_the_commit_of_a_chain():
+    """Appending a chain's rotated rows is committing the path 0, 1, .. of a tree holding those rows rotated."""
+    rng = np.random.default_rng(3)
+    Bn, N, Hkv, D, bs = 3, 5, 2, 32, 4
+    lens, counts = np.array([0, 3, 9]), np.array([5, 1, 4])
+    table = rng.permutation(15).reshape(3, 5)
+    kc, vc = rng.standard_normal((15, Hkv, bs, D)), rng.standard_normal((15, Hkv, bs, D))
+    kt, vt = rng.standard_normal((Bn, N, Hkv, D)), rng.standard_normal((Bn, N, Hkv, D))
+    pos = lens[:, None] + np.arange(N)[None]
+    path = np.tile(np.arange(N), (Bn, 1))
+    want = OK.commit_path(kc, vc, table, lens, OA.rope(kt, pos[:, :, None]), vt, path, counts)
+    rows = [np.concatenate([t[b, :counts[b]] for b in range(Bn)]) for t in (kt, vt)]
+    got = OK.append_tokens(kc, vc, table, lens, rows[0], rows[1], counts, rope_base=10000.0)
+    for g, w in zip(got, want):
+        np.testing.assert_array_equal(g, w)
