@@ -578,6 +578,61 @@ int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_str
                  const float* cos_sin, int32_t max_pos, int32_t B, int32_t Hkv,
                  int32_t head_dim, int32_t dtype, int32_t* status, void* stream);
 
+/*
+ * tv_decode_attn_workspace_size -- host (queries the current device).  Bytes of
+ * device workspace that tv_decode_attn needs for these heads, type and grid
+ * (num_ctas, 0 = one wave of the current device).  Depends on neither the batch
+ * nor the lengths; at most 16 MiB with num_ctas = 0.
+ */
+int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t dtype,
+                                  int32_t num_ctas, size_t* bytes);
+
+/*
+ * tv_decode_attn -- device, asynchronous.  Attention of one new token per
+ * request over the paged cache, for steps without a draft tree: the cache
+ * already holds the token's own key and value (tv_kv_append).  Output row (b, h)
+ * is softmax(s) V over the visible keys t of request b, KV head h / (Hq/Hkv),
+ *   s_t = cap(scale * q . k_t) + slopes[h] * (t - (L_b - 1)),
+ *   cap(x) = softcap * tanh(x / softcap), or x when softcap is 0.
+ * A request without a visible key (L_b = 0) gets a zero row with lse = -inf.
+ * No page defines the call: it is the N = 1 case of "Tree Verification", "Tree
+ * Attention", with the token's K/V in the cache.
+ *
+ * q          device [B, Hq, head_dim] (dtype), q_stride elements between
+ *            requests (heads contiguous), rotated (tv_kv_append).
+ * k_cache, v_cache, block_table: as in tv_tree_attn_verify, any block_size >= 1;
+ *            slots and blocks that hold no visible key are never read.
+ * seq_lens   device int32 [B]: L_b, the new token included; values outside
+ *            [0, max_blocks * block_size] are clamped into it.
+ * scale      softmax scale; softcap >= 0, finite.
+ * window     0: every key is visible.  Else t is visible when t >= L_b - window
+ *            or t < n_sink (the first n_sink keys stay visible; n_sink is
+ *            ignored without a window).
+ * slopes     device float32 [Hq] (nullable): distance bias per query head.
+ * out        device [B, Hq, head_dim] (dtype) out, contiguous.
+ * lse        device float32 [B, Hq] out (nullable): natural-log normaliser.
+ * workspace  device buffer of at least tv_decode_attn_workspace_size bytes, 256-
+ *            byte aligned.  Its arrival counters (the first 16 KiB) are cleared
+ *            first, or taken as zero with TV_ATTN_WORKSPACE_ZEROED; a call that
+ *            completes leaves them zero, whatever its sizes, so a buffer zeroed
+ *            once serves any sequence of tv_decode_attn calls.  Calls that overlap
+ *            on the GPU need their own, and so does tv_tree_attn_verify.
+ * num_ctas   persistent grid (0 = one wave); at most 4096, the value given to
+ *            tv_decode_attn_workspace_size.
+ * flags      0 or TV_ATTN_WORKSPACE_ZEROED.
+ * status     device int32 (nullable): TV_DEV_BAD_BLOCK (a visible position's
+ *            block is outside [0, num_blocks): its key and value count as zeros).
+ * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, any Hq / Hkv; q and the
+ * caches 16-byte aligned, q_stride a multiple of 16 bytes.
+ */
+int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                   int64_t num_blocks, int32_t block_size, const int32_t* block_table,
+                   int32_t max_blocks, const int32_t* seq_lens, int32_t B, int32_t Hq,
+                   int32_t Hkv, int32_t head_dim, int32_t dtype, float scale, float softcap,
+                   int32_t window, int32_t n_sink, const float* slopes, void* out, float* lse,
+                   void* workspace, size_t workspace_bytes, int32_t num_ctas, int32_t flags,
+                   int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -180,3 +180,41 @@ def tree_attention(q, k_cache, v_cache, block_table, seq_lens, k_tree, v_tree,
                 out[b, i, kvh * G:(kvh + 1) * G] = o
                 lse[b, i, kvh * G:(kvh + 1) * G] = l
     return out, lse
+
+
+def decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, softcap=0.0, window=0, n_sink=0,
+                     slopes=None):
+    """Attention of one token per request over its cached keys (its own among
+    them): q [B, Hq, D] -> (out [B, Hq, D], lse [B, Hq]), float64.
+
+    Row (b, h) sees keys t < L_b, with a ``window`` only t >= L_b - window or
+    t < n_sink; its scores are scale * q . k_t, capped to
+    softcap * tanh(x / softcap) when softcap > 0, plus
+    slopes[h] * (t - (L_b - 1)).  No visible key: a zero row, lse -inf.
+    """
+    q = np.asarray(q, dtype=np.float64)
+    Bn, Hq, D = q.shape
+    Hkv = k_cache.shape[1]
+    scale = 1.0 / np.sqrt(D) if scale is None else scale
+    out = np.zeros_like(q)
+    lse = np.full((Bn, Hq), -np.inf)
+    for b in range(Bn):
+        L = int(seq_lens[b])
+        t = np.arange(L)
+        if window:
+            t = t[(t >= L - window) | (t < n_sink)]
+        if not t.size:
+            continue
+        keys = gather_prefix(k_cache, block_table[b], L)[t]
+        values = gather_prefix(v_cache, block_table[b], L)[t]
+        for h in range(Hq):
+            s = keys[:, h // (Hq // Hkv)] @ q[b, h] * scale
+            if softcap:
+                s = softcap * np.tanh(s / softcap)
+            if slopes is not None:
+                s = s + float(slopes[h]) * (t - (L - 1))
+            m = s.max()
+            w = np.exp(s - m)
+            out[b, h] = w @ values[:, h // (Hq // Hkv)] / w.sum()
+            lse[b, h] = m + np.log(w.sum())
+    return out, lse

@@ -63,6 +63,9 @@ SIGNATURES = {
                                     _I32, _I32, _P, _P]),
     "tv_kv_append": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _I64, _I32, _P,
                                     _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "tv_decode_attn_workspace_size": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P]),
+    "tv_decode_attn": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F,
+                                      _F, _I32, _I32, _P, _P, _P, _P, _SZ, _I32, _I32, _P, _P]),
 }
 
 
@@ -562,3 +565,50 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
                               bs, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(new_seq_lens),
                               _ptr(cos_sin), max_pos, B, Hkv, D, _code(dt), _ptr(status), _stream(stream)))
     return q_out, new_seq_lens
+
+
+def tv_decode_attn_workspace_size(Hq, Hkv, head_dim, dtype, num_ctas=0):
+    out = ctypes.c_size_t(0)
+    _check("tv_decode_attn_workspace_size",
+           lib().tv_decode_attn_workspace_size(Hq, Hkv, head_dim, _code(dtype), num_ctas, ctypes.addressof(out)))
+    return out.value
+
+
+def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, softcap=0.0, window=0, n_sink=0,
+                   slopes=None, out=None, lse=None, workspace=None, num_ctas=0, flags=0, status=None, stream=None):
+    """Attention of one new token per request over the paged cache (which holds
+    its K/V already); returns out [B, Hq, D].  q [B, Hq, D] may be strided
+    between requests; softcap, window / n_sink and slopes as in the header;
+    lse float32 [B, Hq] is filled when given."""
+    _dev(seq_lens, "seq_lens", (torch.int32,))
+    B = seq_lens.numel()
+    _dev_cache(k_cache, v_cache, block_table, B)
+    num_blocks, Hkv, bs, D = k_cache.shape
+    dt = k_cache.dtype
+    Hq = q.shape[1]
+    _dev_rows(q, "q", dt, (Hq, D))
+    if q.shape[0] != B:
+        raise ValueError(f"q has {q.shape[0]} rows, expected {B}")
+    if slopes is not None:
+        _dev_shaped(slopes, "slopes", torch.float32, (Hq,))
+    if out is None:
+        out = torch.empty(B, Hq, D, dtype=dt, device=q.device)
+    else:
+        _dev_shaped(out, "out", dt, (B, Hq, D))
+    if lse is not None:
+        _dev_shaped(lse, "lse", torch.float32, (B, Hq))
+    if status is not None:
+        _dev(status, "status", (torch.int32,))
+    if workspace is None:
+        workspace = alloc_workspace(tv_decode_attn_workspace_size(Hq, Hkv, D, dt, num_ctas), q.device)
+        flags |= TV_ATTN_WORKSPACE_ZEROED
+    else:
+        _dev(workspace, "workspace", (torch.uint8,))
+    _one_device(q, k_cache, v_cache, block_table, seq_lens, slopes, out, lse, workspace, status)
+    _check("tv_decode_attn",
+           lib().tv_decode_attn(_ptr(q), q.stride(0), _ptr(k_cache), _ptr(v_cache), num_blocks, bs, _ptr(block_table),
+                                block_table.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, _code(dt),
+                                1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), window, n_sink,
+                                _ptr(slopes), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), num_ctas,
+                                flags, _ptr(status), _stream(stream)))
+    return out

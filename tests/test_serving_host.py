@@ -75,3 +75,70 @@ def test_append_oracle_is_the_commit_of_a_chain():
     got = OK.append_tokens(kc, vc, table, lens, rows[0], rows[1], counts, rope_base=10000.0)
     for g, w in zip(got, want):
         np.testing.assert_array_equal(g, w)
+
+
+DECODE = dict(q=FAKE, q_stride=256, k_cache=FAKE, v_cache=FAKE, num_blocks=9, block_size=16, table=FAKE, max_blocks=4,
+              seq_lens=FAKE, B=3, Hq=4, Hkv=2, head_dim=64, dtype=1, scale=0.125, softcap=0.0, window=0, n_sink=0,
+              slopes=None, out=FAKE, lse=None, workspace=FAKE, workspace_bytes=16 << 20, num_ctas=8, flags=0,
+              status=None, stream=None)
+
+
+@pytest.mark.parametrize("change,code,text", [
+    (dict(B=-1), -1, b"bad sizes"), (dict(Hq=5), -1, b"bad sizes"), (dict(Hkv=0), -1, b"bad sizes"),
+    (dict(window=-1), -1, b"bad sizes"), (dict(n_sink=-1), -1, b"bad sizes"), (dict(block_size=0), -1, b"bad sizes"),
+    (dict(num_ctas=4097), -1, b"bad sizes"), (dict(num_ctas=-1), -1, b"bad sizes"),
+    (dict(dtype=7), -4, b"dtype"), (dict(head_dim=32), -4, b"head_dim 32"),
+    (dict(softcap=-1.0), -1, b"softcap"), (dict(softcap=float("nan")), -1, b"softcap"),
+    (dict(softcap=float("inf")), -1, b"softcap"), (dict(scale=float("inf")), -1, b"scale"),
+    (dict(flags=1), -1, b"unknown flags"), (dict(q=None), -1, b"null"), (dict(out=None), -1, b"null"),
+    (dict(table=None), -1, b"null"), (dict(q_stride=-256), -1, b"16 bytes"), (dict(q_stride=257), -1, b"16 bytes"),
+    (dict(k_cache=ctypes.c_void_p(4104)), -1, b"16 bytes"), (dict(workspace=None), -5, b"workspace"),
+    (dict(workspace_bytes=100), -5, b"workspace"), (dict(workspace=ctypes.c_void_p(4096 + 128)), -5, b"workspace"),
+])
+def test_decode_refuses_on_the_host(change, code, text):
+    assert _call("tv_decode_attn", DECODE, **change) == code
+    assert text in capi.lib().tv_last_error()
+
+
+def test_decode_of_an_empty_batch_does_nothing():
+    assert _call("tv_decode_attn", DECODE, B=0) == 0
+
+
+def test_decode_workspace_size():
+    n = [capi.tv_decode_attn_workspace_size(8, 2, 128, torch.bfloat16, num_ctas=k) for k in (1, 152, 304)]
+    assert n[0] >= 16384 and n == sorted(n) and n[2] <= 16 << 20
+    with pytest.raises(capi.TVError):
+        capi.tv_decode_attn_workspace_size(9, 2, 128, torch.bfloat16, num_ctas=1)
+
+
+def test_decode_oracle_is_the_one_node_tree():
+    """The token's K/V in the cache, or as the root of a one-node tree over the prefix: the same definition."""
+    rng = np.random.default_rng(4)
+    Bn, Hq, Hkv, D, bs = 3, 4, 2, 32, 4
+    lens = np.array([0, 3, 9])
+    table = rng.permutation(12).reshape(3, 4)
+    kc, vc = rng.standard_normal((12, Hkv, bs, D)), rng.standard_normal((12, Hkv, bs, D))
+    q = rng.standard_normal((Bn, Hq, D))
+    kt, vt = rng.standard_normal((Bn, 1, Hkv, D)), rng.standard_normal((Bn, 1, Hkv, D))
+    want, wlse = OA.tree_attention(q[:, None], kc, vc, table, lens, kt, vt, np.array([-1]), rotate=False)
+    kc, vc, now, _ = OK.append_tokens(kc, vc, table, lens, kt[:, 0], vt[:, 0], np.ones(3, dtype=int))
+    got, lse = OA.decode_attention(q, kc, vc, table, now)
+    np.testing.assert_allclose(got, want[:, 0], rtol=0, atol=1e-13)
+    np.testing.assert_allclose(lse, wlse[:, 0], rtol=0, atol=1e-13)
+
+
+def test_decode_oracle_masks_caps_and_biases():
+    """Against torch's own softmax over a dense mask."""
+    rng = np.random.default_rng(5)
+    L, Hq, D = 11, 2, 8
+    k, v = rng.standard_normal((1, 1, 16, D)), rng.standard_normal((1, 1, 16, D))
+    q = rng.standard_normal((1, Hq, D)) * 4
+    slopes = np.array([0.5, 0.0625])
+    got, lse = OA.decode_attention(q, k, v, np.array([[0]]), [L], softcap=3.0, window=4, n_sink=2, slopes=slopes)
+    s = torch.from_numpy(q[0] @ k[0, 0, :L].T / np.sqrt(D))
+    s = 3.0 * torch.tanh(s / 3.0) + torch.from_numpy(slopes)[:, None] * (torch.arange(L) - (L - 1))
+    s[:, 2:7] = -float("inf")
+    np.testing.assert_allclose(got[0], (torch.softmax(s, -1) @ torch.from_numpy(v[0, 0, :L])).numpy(), atol=1e-13)
+    np.testing.assert_allclose(lse[0], torch.logsumexp(s, -1).numpy(), atol=1e-13)
+    empty, elast = OA.decode_attention(q, k, v, np.array([[0]]), [0])
+    assert (empty == 0).all() and (elast == -np.inf).all()
