@@ -62,6 +62,7 @@ extern "C" {
 #define TV_BF16 1
 
 #define TV_MAX_NODES 64
+#define TV_MAX_TOP_K 32 /* alternatives per entry of tv_token_logprobs */
 
 /* Kernel selection for tv_tree_attn_verify (flags & 3). */
 #define TV_ATTN_AUTO 0      /* tensor-core kernel when the shape allows it */
@@ -632,6 +633,38 @@ int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cache, const v
                    int32_t window, int32_t n_sink, const float* slopes, void* out, float* lse,
                    void* workspace, size_t workspace_bytes, int32_t num_ctas, int32_t flags,
                    int32_t* status, void* stream);
+
+/*
+ * tv_token_logprobs -- device, asynchronous.  Log probabilities of given tokens
+ * under rows of logits, with each row's entropy and its most likely
+ * alternatives, from one pass over the row.  Takes what acceptance returns: out
+ * and path of tv_tree_accept_greedy are tokens and node ("Encode branch
+ * histories ...": node i's logits predict the token emitted at it).
+ *
+ * logits    device [B, N, V] (dtype), contiguous.
+ * tokens    device int32 [B, C]: the token of each entry, -1 = no entry.
+ * node      device int32 [B, C] (nullable: entry c reads row c, C <= N): the row
+ *           each entry reads, -1 = no entry.  Rows may repeat.
+ * logprob   device float32 [B, C] out: x[token] - log sum exp(x); 0 for no entry.
+ * entropy   device float32 [B, C] out (nullable): -sum p ln p; 0 for no entry.
+ * top_k     0 .. TV_MAX_TOP_K, at most V: alternatives per entry.
+ * top_ids   device int32 [B, C, top_k] out: the largest logits' indices, largest
+ *           first, equal ones by ascending index; -1 for no entry.
+ * top_logprobs device float32 [B, C, top_k] out: their log probabilities; -inf
+ *           for no entry.
+ * A token outside [0, V) (TV_DEV_BAD_TOKEN) or a node outside [0, N)
+ * (TV_DEV_BAD_TOPOLOGY), -1 apart, counts as no entry.  A logit of -inf is an
+ * excluded token: probability 0, log probability -inf, last among the
+ * alternatives.  A row whose logits are all -inf, or that holds a NaN or +inf,
+ * has no distribution: its log probabilities and entropy are NaN (the
+ * alternatives keep their order, a NaN taken as -inf there).  Sums and results are
+ * float32 for either dtype.  Nothing but the results depends on earlier calls.
+ * logits 16-byte aligned (else TV_ERR_INVALID_ARG); any V.
+ */
+int tv_token_logprobs(const void* logits, const int32_t* tokens, const int32_t* node, int32_t B,
+                      int32_t N, int32_t C, int32_t V, int32_t dtype, float* logprob,
+                      float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs,
+                      int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

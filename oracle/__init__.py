@@ -13,16 +13,19 @@ Everything is written as the plain definition the pages give, in float64
 
 * ``tree``        -- rank paths -> parent / depth / ancestor rows / positions.
 * ``attention``   -- depth-indexed RoPE and, per node, ordinary causal
-                     attention over the node's own root-to-node path.
+                     attention over the node's own root-to-node path;
+                     attention of one token over its cached keys.
 * ``accept``      -- greedy tree walk, the chain verifier of the sampling
                      page, the tree walk with sibling residual updates, and
                      the fixed-point inverse-CDF sampler they share.
 * ``kvcache``     -- commit of the accepted path's tree K/V into the paged
                      cache, and appending of new tokens' K/V to it.
+* ``logprobs``    -- log probabilities of emitted tokens, entropy and top
+                     alternatives of their rows.
 
 Every function is pinned by ``tests/test_oracle_*.py`` (``-m "not gpu"``)
 against facts the pages print or mathematics fixes; no function here is
 "parity unpinned".
 """
 
-from . import accept, attention, kvcache, tree  # noqa: F401
+from . import accept, attention, kvcache, logprobs, tree  # noqa: F401

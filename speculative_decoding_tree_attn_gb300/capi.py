@@ -29,6 +29,7 @@ TV_SAMPLE_AUTO, TV_SAMPLE_CLUSTER, TV_SAMPLE_SINGLE_CTA, TV_SAMPLE_STREAM, TV_SA
 TV_DEV_BAD_TOPOLOGY, TV_DEV_BAD_TOKEN, TV_DEV_OUT_OVERFLOW, TV_DEV_BAD_POSITION, TV_DEV_TIMEOUT = 1, 2, 4, 8, 16
 TV_DEV_BAD_BLOCK = 32
 TV_DEV_BAD_OFFSETS = 64
+TV_MAX_TOP_K = 32
 STATUS_NAMES = {0: "TV_OK", -1: "TV_ERR_INVALID_ARG", -2: "TV_ERR_MISSING_PARENT", -3: "TV_ERR_TOO_MANY_NODES",
                 -4: "TV_ERR_UNSUPPORTED", -5: "TV_ERR_WORKSPACE", -6: "TV_ERR_CUDA"}
 
@@ -66,6 +67,7 @@ SIGNATURES = {
     "tv_decode_attn_workspace_size": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P]),
     "tv_decode_attn": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F,
                                       _F, _I32, _I32, _P, _P, _P, _P, _SZ, _I32, _I32, _P, _P]),
+    "tv_token_logprobs": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P]),
 }
 
 
@@ -612,3 +614,45 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
                                 _ptr(slopes), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), num_ctas,
                                 flags, _ptr(status), _stream(stream)))
     return out
+
+
+def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entropy=None, top_ids=None,
+                      top_logprobs=None, status=None, stream=None):
+    """Log probabilities of tokens [B, C] under rows node [B, C] (None: row c) of
+    logits [B, N, V] (float32 or bf16); returns (logprob, entropy [B, C] float32,
+    top_ids int32, top_logprobs float32 [B, C, top_k]).  tokens and node may be
+    out and path of tv_tree_accept_*: -1 is no entry."""
+    _dev(logits, "logits", (torch.float32, torch.bfloat16))
+    _dev(tokens, "tokens", (torch.int32,))
+    if logits.dim() != 3 or tokens.dim() != 2 or tokens.shape[0] != logits.shape[0]:
+        raise ValueError(f"logits [B, N, V] and tokens [B, C] expected, got {tuple(logits.shape)}, "
+                         f"{tuple(tokens.shape)}")
+    B, N, V = logits.shape
+    C = tokens.shape[1]
+    if node is not None:
+        _dev_shaped(node, "node", torch.int32, (B, C))
+    dev = logits.device
+    if logprob is None:
+        logprob = torch.empty(B, C, dtype=torch.float32, device=dev)
+    else:
+        _dev_shaped(logprob, "logprob", torch.float32, (B, C))
+    if entropy is None:
+        entropy = torch.empty(B, C, dtype=torch.float32, device=dev)
+    else:
+        _dev_shaped(entropy, "entropy", torch.float32, (B, C))
+    if top_ids is None:
+        top_ids = torch.empty(B, C, max(top_k, 0), dtype=torch.int32, device=dev)
+    else:
+        _dev_shaped(top_ids, "top_ids", torch.int32, (B, C, top_k))
+    if top_logprobs is None:
+        top_logprobs = torch.empty(B, C, max(top_k, 0), dtype=torch.float32, device=dev)
+    else:
+        _dev_shaped(top_logprobs, "top_logprobs", torch.float32, (B, C, top_k))
+    if status is not None:
+        _dev(status, "status", (torch.int32,))
+    _one_device(logits, tokens, node, logprob, entropy, top_ids, top_logprobs, status)
+    _check("tv_token_logprobs",
+           lib().tv_token_logprobs(_ptr(logits), _ptr(tokens), _ptr(node), B, N, C, V, _code(logits.dtype),
+                                   _ptr(logprob), _ptr(entropy), top_k, _ptr(top_ids), _ptr(top_logprobs),
+                                   _ptr(status), _stream(stream)))
+    return logprob, entropy, top_ids, top_logprobs

@@ -11,6 +11,7 @@ import torch
 
 from oracle import attention as OA
 from oracle import kvcache as OK
+from oracle import logprobs as OL
 from speculative_decoding_tree_attn_gb300 import build as B
 from speculative_decoding_tree_attn_gb300 import capi
 
@@ -142,3 +143,49 @@ def test_decode_oracle_masks_caps_and_biases():
     np.testing.assert_allclose(lse[0], torch.logsumexp(s, -1).numpy(), atol=1e-13)
     empty, elast = OA.decode_attention(q, k, v, np.array([[0]]), [0])
     assert (empty == 0).all() and (elast == -np.inf).all()
+
+
+LOGPROBS = dict(logits=FAKE, tokens=FAKE, node=None, B=2, N=3, C=3, V=100, dtype=0, logprob=FAKE, entropy=FAKE, top_k=4,
+                top_ids=FAKE, top_logprobs=FAKE, status=None, stream=None)
+
+
+@pytest.mark.parametrize("change,code,text", [
+    (dict(B=-1), -1, b"bad sizes"), (dict(N=0), -1, b"bad sizes"), (dict(V=0), -1, b"bad sizes"),
+    (dict(C=4), -1, b"bad sizes"), (dict(C=-1), -1, b"bad sizes"), (dict(dtype=3), -4, b"dtype"),
+    (dict(top_k=33), -1, b"top_k"), (dict(top_k=-1), -1, b"top_k"), (dict(V=3), -1, b"top_k"),
+    (dict(logits=None), -1, b"null"), (dict(tokens=None), -1, b"null"), (dict(logprob=None), -1, b"null"),
+    (dict(top_ids=None), -1, b"null"), (dict(top_logprobs=None), -1, b"null"),
+    (dict(logits=ctypes.c_void_p(4100)), -1, b"16-byte"), (dict(B=1 << 30, C=3), -4, b"2^31"),
+])
+def test_logprobs_refuse_on_the_host(change, code, text):
+    assert _call("tv_token_logprobs", LOGPROBS, **change) == code
+    assert text in capi.lib().tv_last_error()
+
+
+def test_logprobs_of_nothing():
+    assert _call("tv_token_logprobs", LOGPROBS, B=0) == 0
+    assert _call("tv_token_logprobs", LOGPROBS, C=0) == 0
+
+
+def test_logprobs_oracle_against_torch():
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((2, 3, 50)) * 3
+    x[0, 1, ::3] = -np.inf
+    x[1, 2, 4] = x[1, 2, 9] = 20.0
+    tok = rng.integers(0, 50, size=(2, 3))
+    tok[1, 0] = -1
+    lp, ent, ids, top = OL.token_logprobs(x, tok, None, 5)
+    t = torch.from_numpy(x)
+    ref = torch.log_softmax(t, -1)
+    want = torch.where(torch.from_numpy(tok) >= 0, ref.gather(-1, torch.from_numpy(tok).clamp(min=0)[..., None])[..., 0], 0.0)
+    np.testing.assert_allclose(lp, want.numpy(), atol=1e-13)
+    h = torch.special.entr(torch.softmax(t, -1)).sum(-1).numpy()
+    h[1, 0] = 0
+    np.testing.assert_allclose(ent, h, atol=1e-13)
+    assert ids[1, 2, :2].tolist() == [4, 9] and (ids[1, 0] == -1).all() and (top[1, 0] == -np.inf).all()
+    for b, n in ((0, 0), (0, 1), (0, 2), (1, 1)):
+        v, i = torch.topk(ref[b, n], 5)
+        assert ids[b, n].tolist() == i.tolist()
+        np.testing.assert_allclose(top[b, n], v.numpy(), atol=1e-13)
+    nan = OL.token_logprobs(np.full((1, 1, 4), -np.inf), np.array([[2]]), None, 2)
+    assert np.isnan(nan[0]).all() and np.isnan(nan[1]).all() and nan[2][0, 0].tolist() == [0, 1]
