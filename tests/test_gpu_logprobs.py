@@ -32,13 +32,14 @@ def _check(logits, tokens, node=None, top_k=0, want_status=0):
     V = x.shape[-1]
     spread = 104.0
     rel = (V / 256 + 16) * 2.0 ** -24 + 2.0 ** -21 + 2 * 2.0 ** -24 * spread
-    big = np.where(np.isfinite(x), np.abs(x), 0).max()
+    rows = np.arange(tokens.shape[1])[None].repeat(x.shape[0], 0) if node is None else to_np(node).clip(0, x.shape[1] - 1)
+    best = np.abs(np.take_along_axis(np.nan_to_num(x.astype(np.float64)).max(-1), rows, 1))  # |m| [B, C]
     with np.errstate(invalid="ignore"):
-        for g, r in ((lp, ref[0]), (top, ref[3])):
+        for g, r, m in ((lp, ref[0], best), (top, ref[3], np.broadcast_to(best[..., None], ref[3].shape))):
             fin = np.isfinite(r)
             assert np.array_equal(np.isnan(g), np.isnan(r)) and np.array_equal(g[~fin & ~np.isnan(r)], r[~fin & ~np.isnan(r)])
-            # ln S moves by rel; the subtractions round at |x|, |m|, ln V at most
-            assert (np.abs(g - r)[fin] <= rel + 4 * 2.0 ** -24 * (2 * big + np.log(V) + np.abs(r[fin]))).all()
+            # ln S moves by rel; the subtractions round at |x| <= |result| + |m| + ln V, at |m| and at ln V
+            assert (np.abs(g - r)[fin] <= rel + 4 * 2.0 ** -24 * (2 * (m[fin] + np.log(V)) + np.abs(r[fin]))).all()
         fin = np.isfinite(ref[1])
         assert np.array_equal(np.isnan(ent), ~fin)
         # H = ln S + T, T = (1/S) sum e (m - x) <= H: each off by rel of itself
