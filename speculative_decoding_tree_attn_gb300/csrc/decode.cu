@@ -80,6 +80,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Counts an arrival; releases what the CTA wrote before its last barrier and
+// acquires what the earlier arrivals released.
+__device__ __forceinline__ uint32_t arrive(uint32_t* counter) {
+  uint32_t before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  return before;
+}
+
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, float32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -319,21 +327,25 @@ struct Bf16Math {
 };
 
 // ---------------------------------------------------------------------------
-// float32: FMAs.  A lane keeps D / 32 dimensions of Q and O for 8 heads; 4 keys x
-// 8 heads of partial products are summed over the lanes by 31 exchanges that
-// leave each lane one (key, head), and the weights come back through shared
-// memory as broadcasts.
+// float32: FMAs.  A lane keeps D / 32 dimensions of Q and O for NH heads (the
+// least power of two that holds the KV head's, 8 at most).  The partial products
+// of 32 (key, head) pairs are summed over the lanes by 31 exchanges that leave
+// each lane one pair, and the weights come back through shared memory as
+// broadcasts.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, int NH>
 struct F32Math {
   using Out = float;
-  static constexpr int kHeads = 8;
+  static constexpr int kHeads = NH;
   static constexpr int kRowBytes = 4 * D;
-  static constexpr int kWarpScratch = kKeys * 8 * 4;  // the group's weights [key][head]
+  static constexpr int kWarpScratch = kKeys * NH * 4;  // the group's weights [key][head]
   static constexpr int kE = D / 32;
-  static constexpr int kVec = kE < 4 ? kE : 4;  // consecutive dimensions of a lane
-  float q[8][kE], o[8][kE];
-  float m, l, slope;  // of head lane % 8
+  static constexpr int kVec = kE < 4 ? kE : 4;                      // consecutive dimensions of a lane
+  static constexpr int kPairs = kKeys * NH < 32 ? kKeys * NH : 32;  // (key, head) pairs summed at once
+  static constexpr int kAtOnce = kPairs / NH;                       // keys
+  static constexpr int kSets = kKeys / kAtOnce;
+  float q[NH][kE], o[NH][kE];
+  float m, l, slope;  // of head lane % NH
 
   static __device__ __forceinline__ int piece(int r, int c) { return r * kRowBytes + (c << 4); }
   static __device__ __forceinline__ int dim(int lane, int e) { return lane * kVec + (e / kVec) * 32 * kVec + e % kVec; }
@@ -351,7 +363,7 @@ struct F32Math {
 
   __device__ __forceinline__ void begin(const DecodeParams& p, const char* qrow, int h0, int nh, int lane) {
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
         q[h][e] = h < nh ? __ldg(reinterpret_cast<const float*>(qrow + h * kRowBytes) + dim(lane, e)) : 0.f;
@@ -359,29 +371,30 @@ struct F32Math {
       }
     m = -INFINITY;
     l = 0.f;
-    slope = p.slopes && (lane & 7) < nh ? __ldg(p.slopes + h0 + (lane & 7)) * kLog2e : 0.f;
+    slope = p.slopes && lane % NH < nh ? __ldg(p.slopes + h0 + lane % NH) * kLog2e : 0.f;
   }
 
   __device__ __forceinline__ void group(const DecodeParams& p, const Scorer& score, const Span& sp, int key, uint32_t kt,
                                         uint32_t vt, int lane, float* weights) {
-    float s[4];
+    float s[kSets];
+    float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[32];
+    for (int i = 0; i < kSets; ++i) {
+      float v[kPairs];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         float x[kE];
-        lane_row(x, kt + (4 * i + k) * kRowBytes, lane);
+        lane_row(x, kt + (kAtOnce * i + k) * kRowBytes, lane);
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
+        for (int h = 0; h < NH; ++h) {
           float a = q[h][0] * x[0];
 #pragma unroll
           for (int e = 1; e < kE; ++e) a = fmaf(q[h][e], x[e], a);
-          v[8 * k + h] = a;
+          v[NH * k + h] = a;
         }
       }
 #pragma unroll
-      for (int w = 16; w; w >>= 1) {
+      for (int w = kPairs / 2; w; w >>= 1) {
         const bool up = lane & w;
 #pragma unroll
         for (int j = 0; j < w; ++j) {
@@ -389,20 +402,21 @@ struct F32Math {
           v[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
         }
       }
-      const int t = key + 4 * i + (lane >> 3);
+      if constexpr (kPairs == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+      const int t = key + kAtOnce * i + lane % kPairs / NH;
       s[i] = fmaf(slope, (float)(t - (sp.L - 1)), score(v[0]));
       if (!visible(sp, t)) s[i] = -INFINITY;
+      mx = fmaxf(mx, s[i]);
     }
-    float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+#pragma unroll
+    for (int w = NH; w < kPairs; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
     if (__any_sync(0xffffffffu, mx > m + 8.f)) {
       const float m2 = fmaxf(m, mx);
       const float c = m == -INFINITY ? 0.f : exp2_approx(m - m2);
       m = m2;
       l *= c;
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
+      for (int h = 0; h < NH; ++h) {
         const float ch = __shfl_sync(0xffffffffu, c, h);
 #pragma unroll
         for (int e = 0; e < kE; ++e) o[h][e] *= ch;
@@ -410,21 +424,20 @@ struct F32Math {
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSets; ++i) {
       const float w = exp2_approx(s[i] - m);
       l += w;
-      weights[32 * i + lane] = w;
+      if (kPairs == 32 || lane < kPairs) weights[kPairs * i + lane] = w;
     }
     __syncwarp();
 #pragma unroll 4
     for (int k = 0; k < kKeys; ++k) {
-      float x[kE];
+      float x[kE], w[NH];
       lane_row(x, vt + k * kRowBytes, lane);
-      const float4 wa = *reinterpret_cast<const float4*>(weights + 8 * k);
-      const float4 wb = *reinterpret_cast<const float4*>(weights + 8 * k + 4);
-      const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-      for (int h = 0; h < 8; ++h)
+      for (int h = 0; h < NH; ++h) w[h] = weights[NH * k + h];
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < kE; ++e) o[h][e] = fmaf(w[h], x[e], o[h][e]);
     }
@@ -432,14 +445,14 @@ struct F32Math {
 
   __device__ __forceinline__ void flush(int, float* o_out, float* ml, int lane) {
     float v = l;
-    v += __shfl_xor_sync(0xffffffffu, v, 8);
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-    if (lane < 8) {
+#pragma unroll
+    for (int w = NH; w < kPairs; w <<= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+    if (lane < NH) {
       ml[2 * lane] = m;
       ml[2 * lane + 1] = v;
     }
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
         const int d = dim(lane, e);
@@ -477,7 +490,15 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   extern __shared__ __align__(128) char smem[];
   __shared__ int64_t s_scan[kWarps];
   __shared__ int64_t s_total, s_base;
-  __shared__ int s_b, s_last;
+  __shared__ int s_b;
+  __shared__ bool s_last;
+  struct Piece {  // this CTA's piece of a cut unit
+    int64_t c0;   // the unit's first CTA
+    int others;   // its other pieces; -1: no such unit
+    int heads;
+    int64_t out_row;
+  };
+  __shared__ Piece s_piece[2];  // of the unit that the slice's start cuts, of the one that its end cuts
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kStage;
   float* merge = reinterpret_cast<float*>(smem + S::kRing);
@@ -498,6 +519,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     s_total = all * per_request;
     s_base = 0;
     s_b = -1;
+    s_piece[0].others = s_piece[1].others = -1;
   }
   __syncthreads();
   const int64_t T = s_total;
@@ -604,12 +626,22 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   const Scorer score(p);
   int stage = 0;
   Math math;
+  uint32_t before_lead = 0, before_tail = 0;  // pieces that arrived before this CTA's (thread 0; not waited for until the end)
   for (int64_t t = t0; t < t1;) {
     const int kvh = at.unit / p.head_groups, hg = at.unit % p.head_groups;
     const int h0 = kvh * p.G + hg * kHeads;                    // first query head
     const int nh = min(kHeads, p.G - hg * kHeads);
     const int tile1 = (int)min((int64_t)at.tiles, at.tile + (t1 - t));
     math.begin(p, p.q + at.b * p.q_stride + (int64_t)h0 * Math::kRowBytes, h0, nh, lane);
+    if (t + tile1 - at.tile < t1) {  // the next unit's queries, into this SM's cache
+      const bool same = at.unit + 1 < per_request;
+      const int unit = same ? at.unit + 1 : 0;
+      const int hq = unit / p.head_groups * p.G + unit % p.head_groups * kHeads;
+      const int n = min(kHeads, p.G - unit % p.head_groups * kHeads) * (Math::kRowBytes / 128);
+      if (tid < n)
+        asm volatile("{.reg .b32 x; ld.global.ca.b32 x, [%0];}" ::"l"(
+            p.q + (same ? at.b : at.b + 1) * p.q_stride + (int64_t)hq * Math::kRowBytes + tid * 128));
+    }
     for (int tile = at.tile; tile < tile1; ++tile) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
@@ -629,7 +661,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     const int64_t out_row = (int64_t)at.b * p.Hq + h0;
     typename Math::Out* out = reinterpret_cast<typename Math::Out*>(p.out) + out_row * D;
 #pragma unroll
-    for (int n = 0; n < kHeads / 8; ++n) {
+    for (int n = 0; n < (kHeads + 7) / 8; ++n) {
       const int heads = min(8, nh - 8 * n);
       if (heads <= 0) break;
       __syncthreads();  // the buffer's last readers
@@ -666,43 +698,12 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     }
     if (!whole) {
       const int64_t c0 = cta_of(u0, T, P), c1 = cta_of(u0 + at.tiles - 1, T, P);
-      __threadfence();
-      __syncthreads();
+      __syncthreads();  // the piece is written; thread 0's release covers it
       if (tid == 0) {
-        const uint32_t n = atomicAdd(p.arrive + c0, 1u);
-        s_last = n == (uint32_t)(c1 - c0);
-        if (s_last) p.arrive[c0] = 0;  // every piece is here
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int x = tid; x < nh * (D / 4); x += kThreads) {
-          const int h = x / (D / 4), u = x % (D / 4);
-          // slot 1 of the first CTA, slot 0 of the others
-          auto ml = [&](int64_t c) {
-            return __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((2 * c + (c == c0)) * kHeads + h) * 2));
-          };
-          float mm = -INFINITY;
-#pragma unroll 8
-          for (int64_t c = c0; c <= c1; ++c) mm = fmaxf(mm, ml(c).x);
-          float ll = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float2 a = ml(c);
-            const float w = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mm);
-            const float4 o =
-                __ldcg(reinterpret_cast<const float4*>(p.part_o + ((2 * c + (c == c0)) * kHeads + h) * D + 4 * u));
-            ll = fmaf(a.y, w, ll);
-            v.x = fmaf(o.x, w, v.x);
-            v.y = fmaf(o.y, w, v.y);
-            v.z = fmaf(o.z, w, v.z);
-            v.w = fmaf(o.w, w, v.w);
-          }
-          const float r = 1.f / ll;
-          store4(out + h * D + 4 * u, make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
-          if (p.lse && u == 0) p.lse[out_row + h] = (mm + log2f(ll)) * kLn2;
-        }
+        const int k = at.tile == 0 ? 1 : 0;
+        s_piece[k] = {c0, (int)(c1 - c0), nh, out_row};
+        const uint32_t n = arrive(p.arrive + c0);
+        if (k) before_tail = n; else before_lead = n;
       }
     }
     t += tile1 - at.tile;
@@ -710,6 +711,48 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     if (at.tile == at.tiles) next_unit(at);
   }
   cp_async_wait<0>();
+
+  // ---- joins ----
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Piece mine = s_piece[k];
+    if (mine.others < 0) continue;
+    if (tid == 0) {
+      s_last = (k ? before_tail : before_lead) == (uint32_t)mine.others;
+      if (s_last) p.arrive[mine.c0] = 0;  // every piece is here
+    }
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      typename Math::Out* out = reinterpret_cast<typename Math::Out*>(p.out) + mine.out_row * D;
+      for (int x = tid; x < mine.heads * (D / 4); x += kThreads) {
+        const int h = x / (D / 4), u = x % (D / 4);
+        // slot 1 of the unit's first CTA, slot 0 of the others
+        auto slot = [&](int i) { return ((2 * (mine.c0 + i) + (i == 0)) * kHeads + h); };
+        float mm = -INFINITY;
+#pragma unroll 8
+        for (int i = 0; i <= mine.others; ++i) mm = fmaxf(mm, __ldcg(p.part_ml + slot(i) * 2));
+        float ll = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = 0; i <= mine.others; ++i) {
+          const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2));
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(i) * D + 4 * u));
+          const float w = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mm);
+          ll = fmaf(a.y, w, ll);
+          v.x = fmaf(o.x, w, v.x);
+          v.y = fmaf(o.y, w, v.y);
+          v.z = fmaf(o.z, w, v.z);
+          v.w = fmaf(o.w, w, v.w);
+        }
+        const float r = 1.f / ll;
+        store4(out + h * D + 4 * u, make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
+        if (p.lse && u == 0) p.lse[mine.out_row + h] = (mm + log2f(ll)) * kLn2;
+      }
+    }
+    __syncthreads();
+  }
 }
 
 template <class Math, int D>
@@ -722,21 +765,34 @@ int launch_decode(DecodeParams p, int ctas, cudaStream_t s) {
   return TV_OK;
 }
 
-// Query heads of a unit: 16 where a KV head serves more than 8 (two 8-column
-// products share a key's loads), except where their sums would not fit in registers.
-int unit_heads(int G, int D, int dtype) { return dtype == TV_BF16 && G > 8 && D <= 128 ? 16 : 8; }
+// Query heads of a unit.  bf16: 8, or 16 where a KV head serves more than 8 (two
+// 8-column products share a key's loads), except where their sums would not fit in
+// registers.  float32: as many as the KV head serves, 8 at most.
+int unit_heads(int G, int D, int dtype) {
+  if (dtype == TV_BF16) return G > 8 && D <= 128 ? 16 : 8;
+  return G == 1 ? 1 : G == 2 ? 2 : G <= 4 ? 4 : 8;
+}
+
+template <int D>
+int dispatch_heads(const DecodeParams& p, int dtype, int ctas, cudaStream_t s) {
+  const int heads = unit_heads(p.G, D, dtype);
+  if (dtype == TV_BF16) {
+    if constexpr (D <= 128)
+      if (heads == 16) return launch_decode<Bf16Math<D, 2>, D>(p, ctas, s);
+    return launch_decode<Bf16Math<D, 1>, D>(p, ctas, s);
+  }
+  switch (heads) {
+    case 1: return launch_decode<F32Math<D, 1>, D>(p, ctas, s);
+    case 2: return launch_decode<F32Math<D, 2>, D>(p, ctas, s);
+    case 4: return launch_decode<F32Math<D, 4>, D>(p, ctas, s);
+    default: return launch_decode<F32Math<D, 8>, D>(p, ctas, s);
+  }
+}
 
 int dispatch_decode(const DecodeParams& p, int D, int dtype, int ctas, cudaStream_t s) {
-  if (dtype == TV_F32) {
-    if (D == 64) return launch_decode<F32Math<64>, 64>(p, ctas, s);
-    if (D == 128) return launch_decode<F32Math<128>, 128>(p, ctas, s);
-    return launch_decode<F32Math<256>, 256>(p, ctas, s);
-  }
-  const bool two = unit_heads(p.G, D, dtype) == 16;
-  if (D == 64) return two ? launch_decode<Bf16Math<64, 2>, 64>(p, ctas, s) : launch_decode<Bf16Math<64, 1>, 64>(p, ctas, s);
-  if (D == 128)
-    return two ? launch_decode<Bf16Math<128, 2>, 128>(p, ctas, s) : launch_decode<Bf16Math<128, 1>, 128>(p, ctas, s);
-  return launch_decode<Bf16Math<256, 1>, 256>(p, ctas, s);
+  if (D == 64) return dispatch_heads<64>(p, dtype, ctas, s);
+  if (D == 128) return dispatch_heads<128>(p, dtype, ctas, s);
+  return dispatch_heads<256>(p, dtype, ctas, s);
 }
 
 // One CTA per SM unless the caller asks for another grid.
