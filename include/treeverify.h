@@ -613,7 +613,7 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * out        device [B, Hq, head_dim] (dtype) out, contiguous.
  * lse        device float32 [B, Hq] out (nullable): natural-log normaliser.
  * workspace  device buffer of at least tv_decode_attn_workspace_size bytes, 256-
- *            byte aligned.  Its arrival counters (the first 16 KiB) are cleared
+ *            byte aligned.  Its counters (the first 16 KiB) are cleared
  *            first, or taken as zero with TV_ATTN_WORKSPACE_ZEROED; a call that
  *            completes leaves them zero, whatever its sizes, so a buffer zeroed
  *            once serves any sequence of tv_decode_attn calls.  Calls that overlap
@@ -623,8 +623,10 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * flags      0 or TV_ATTN_WORKSPACE_ZEROED.
  * status     device int32 (nullable): TV_DEV_BAD_BLOCK (a visible position's
  *            block is outside [0, num_blocks): its key and value count as zeros).
- * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, any Hq / Hkv; q and the
- * caches 16-byte aligned, q_stride a multiple of 16 bytes.
+ * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, any Hq / Hkv; q, out and
+ * the caches 16-byte aligned, q_stride a multiple of 16 bytes.  TV_ERR_UNSUPPORTED
+ * where the work could reach 2^31 groups of 4-16 keys (requests x KV heads x
+ * head groups of 8 or 16 x max_blocks * block_size / keys).
  */
 int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                    int64_t num_blocks, int32_t block_size, const int32_t* block_table,

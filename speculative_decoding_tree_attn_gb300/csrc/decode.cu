@@ -9,17 +9,24 @@
 // Bound by HBM: a key costs 4 D bytes of bf16 K+V and 4 G D flops, G flop a byte
 // (4-16), far below the tensor pipes, so every byte is read once for all G heads
 // of its KV head and everything else stays off that path:
-// - Work is cut as in the tree kernels: a unit is (request, KV head, up to
-//   8 or 16 query heads); the units' tiles lie end to end and each CTA of a
-//   persistent grid takes an equal run of them.  A tile is one 16-key group per
-//   warp.  Each warp copies its own groups through its own ring in shared memory
+// - A unit is (request, KV head, up to 8 or 16 query heads).  A CTA's warps take a
+//   team of units at a time, all KV heads of a request where there are 8: they
+//   then read whole cache blocks together (one KV head's part of a 16-token block
+//   is 4 KB; with the warps on one head's keys instead, 64 requests of 1k-8k
+//   tokens took 202 us, with this 176 us).  Where the lengths leave too few tiles
+//   for that, several warps share a unit's keys.
+// - Teams' tiles (a group of keys per warp) lie end to end and each CTA of a
+//   persistent grid takes an equal run of them.  (Small runs at the end, taken by
+//   whichever CTA is done, would even out the SMs' unequal shares of the memory, 4 %
+//   in the stream alone; the pieces they cut the last requests into cost more.)
+// - Each warp copies its own groups through its own ring in shared memory
 //   (cp.async, rows looked up in the block table one step ahead), so nothing in
 //   the stream waits for another warp.
-// - Groups start at multiples of 16 keys.  Rows that are not visible are not read:
-//   the copy fills them with zeros, so a window also skips its work.
-// - Online softmax per warp in the log2 domain, sums in float32; the warps' sums
-//   meet in shared memory at the end of a unit.  A unit cut by a slice boundary
-//   leaves (max, sum, output) of each piece in the workspace; the piece that
+// - Groups start at multiples of their size.  Rows that are not visible are not
+//   read: the copy fills them with zeros, so a window also skips its work.
+// - Online softmax per warp in the log2 domain, sums in float32; warps that share
+//   a unit meet in shared memory at its end.  A team cut by a CTA's boundary
+//   leaves (max, sum, output) of each piece in the workspace; the CTA whose piece
 //   arrives last joins them in order, so results do not depend on timing.
 #include <algorithm>
 #include <cmath>
@@ -33,8 +40,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 4096;
-constexpr int64_t kCounterBytes = 4 * kMaxCtas;  // first in the workspace whatever the sizes
-constexpr int kKeys = 16;                        // keys of a group
+constexpr int64_t kCounterBytes = 4 * kMaxCtas;  // arrival counters by a cut team's first CTA: first in the workspace
 constexpr int kZeros = -1;    // cache row of a key that is not read
 constexpr int kNoGroup = -2;  // of a warp without a group in the tile
 
@@ -50,15 +56,18 @@ struct DecodeParams {
   const int32_t* seq_lens;
   int B, Hq, Hkv, G;
   int head_groups;  // units per (request, KV head)
+  int team_log;     // largest team, log2: a power of two that divides a request's units and the warps
+  int rows;         // query heads that a unit holds at most
+  uint32_t div_mul, div_shift;  // t / block_size = t * div_mul >> div_shift
   float scale, softcap;
   int window, n_sink;
   const float* slopes;
   char* out;
   float* lse;
   int32_t* status;
-  uint32_t* arrive;  // [kMaxCtas], by a split unit's first CTA
-  float* part_o;     // [P][2][heads][D]
-  float* part_ml;    // [P][2][heads][2]
+  uint32_t* arrive;  // [kMaxCtas]
+  float* part_o;     // [CTAs][2][team][rows][D]
+  float* part_ml;    // [CTAs][2][team][rows][2]
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
@@ -78,6 +87,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// x 2^(m - top), a sum against m as one against top; nothing has been summed against -inf.
+__device__ __forceinline__ float scaled(float x, float m, float top) {
+  return m == -INFINITY ? x : x * exp2_approx(m - top);
 }
 
 // Counts an arrival; releases what the CTA wrote before its last barrier and
@@ -101,13 +115,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// The visible keys of one request, in groups of 16 (absolute multiples).
+// The visible keys of one request, in groups of kKeys (absolute multiples).
 struct Span {
   int L, first, sink;  // t < sink or first <= t < L
   int lead;            // groups [0, lead) before the group of `first`
   int groups;
 };
 
+template <int kKeys>
 __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   Span s;
   const int64_t cap = (int64_t)p.max_blocks * p.block_size;
@@ -115,17 +130,19 @@ __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   s.L = (int)max((int64_t)0, min(L, cap));
   s.first = p.window > 0 ? max(0, s.L - p.window) : 0;
   s.sink = min(p.n_sink, s.first);
-  s.lead = min((s.sink + kKeys - 1) / kKeys, s.first / kKeys);
+  s.lead = min((int)(((uint32_t)s.sink + kKeys - 1) / kKeys), s.first / kKeys);
   s.groups = s.L > 0 ? s.lead + (s.L - 1) / kKeys + 1 - s.first / kKeys : 0;
   return s;
 }
+template <int kKeys>
 __device__ __forceinline__ int group_key(const Span& s, int i) {
   return (i < s.lead ? i : s.first / kKeys + i - s.lead) * kKeys;
 }
 __device__ __forceinline__ bool visible(const Span& s, int t) { return t < s.L && (t >= s.first || t < s.sink); }
 
-__device__ __forceinline__ int64_t cta_start(int64_t c, int64_t T, int64_t P) { return c * T / P; }
-__device__ __forceinline__ int64_t cta_of(int64_t t, int64_t T, int64_t P) { return ((t + 1) * P - 1) / T; }
+// CTA c of P takes tiles [cta_start(c), cta_start(c + 1)) of T.
+__device__ __forceinline__ int cta_start(int c, int T, int P) { return (int)((int64_t)c * T / P); }
+__device__ __forceinline__ int cta_of(int t, int T, int P) { return (int)((((int64_t)t + 1) * P - 1) / T); }
 
 // Score of one (head, key) in the log2 domain from its raw product.
 struct Scorer {
@@ -162,6 +179,8 @@ template <int D, int NB>
 struct Bf16Math {
   using Out = __nv_bfloat16;
   static constexpr int kHeads = 8 * NB;
+  static constexpr int kFlush = 8;  // heads merged at once
+  static constexpr int kKeys = 16;
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kWarpScratch = 0;
   uint4 q[NB][D / 32];
@@ -297,7 +316,59 @@ struct Bf16Math {
     }
   }
 
-  // This warp's maxima, sums and outputs of heads 8n .. 8n + 7.
+  __device__ __forceinline__ float4 four(int n, int e, int i, int u) const {
+    const float(&a)[4] = o[n][4 * i + 2 * u], (&b)[4] = o[n][4 * i + 2 * u + 1];
+    return make_float4(a[e], a[2 + e], b[e], b[2 + e]);
+  }
+  __device__ __forceinline__ void sum_up() {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+  }
+  // The finished rows of a unit that this warp had alone.
+  __device__ __forceinline__ void write_out(Out* out, float* lse, int nh, bool any, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    sum_up();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 8 * n + 2 * t + e;
+        if (h >= nh) continue;
+        const float r = any ? 1.f / l[n][e] : 0.f;
+        if (lse && g == 0) lse[h] = any ? (m[n][e] + log2f(l[n][e])) * kLn2 : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const float4 a = four(n, e, i, 0), b = four(n, e, i, 1);
+          const __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a.x * r, a.y * r), __floats2bfloat162_rn(a.z * r, a.w * r),
+                                       __floats2bfloat162_rn(b.x * r, b.y * r), __floats2bfloat162_rn(b.z * r, b.w * r)};
+          *reinterpret_cast<uint4*>(out + h * D + 8 * (g + 8 * i)) = *reinterpret_cast<const uint4*>(v);
+        }
+      }
+  }
+  // Its piece of one: outputs [head][D], (max, sum) [head][2].
+  __device__ __forceinline__ void write_piece(float* o_out, float* ml, int nh, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    sum_up();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 8 * n + 2 * t + e;
+        if (h >= nh) continue;
+        if (g == 0) __stcg(reinterpret_cast<float2*>(ml + 2 * h), make_float2(m[n][e], l[n][e]));
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            __stcg(reinterpret_cast<float4*>(o_out + h * D + 8 * (g + 8 * i) + 4 * u), four(n, e, i, u));
+      }
+  }
+
+  // This warp's maxima, sums and outputs of heads 8n .. 8n + 7 into the merge buffer.
   __device__ __forceinline__ void flush(int n, float* o_out, float* ml, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -318,16 +389,14 @@ struct Bf16Math {
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<float4*>(o_out + h * D + 4 * merge_unit(h, 2 * (g + 8 * i) + u)) =
-                make_float4(o[k][4 * i + 2 * u][e], o[k][4 * i + 2 * u][2 + e], o[k][4 * i + 2 * u + 1][e],
-                            o[k][4 * i + 2 * u + 1][2 + e]);
+            *reinterpret_cast<float4*>(o_out + h * D + 4 * merge_unit(h, 2 * (g + 8 * i) + u)) = four(k, e, i, u);
       }
     }
   }
 };
 
 // ---------------------------------------------------------------------------
-// float32: FMAs.  A lane keeps D / 32 dimensions of Q and O for NH heads (the
+// float32: FMAs.  Groups of 1024 / D keys.  A lane keeps D / 32 dimensions of Q and O for NH heads (the
 // least power of two that holds the KV head's, 8 at most).  The partial products
 // of 32 (key, head) pairs are summed over the lanes by 31 exchanges that leave
 // each lane one pair, and the weights come back through shared memory as
@@ -337,6 +406,8 @@ template <int D, int NH>
 struct F32Math {
   using Out = float;
   static constexpr int kHeads = NH;
+  static constexpr int kFlush = D == 256 && NH == 8 ? 4 : NH;
+  static constexpr int kKeys = 1024 / D;  // 8 KB of K and V
   static constexpr int kRowBytes = 4 * D;
   static constexpr int kWarpScratch = kKeys * NH * 4;  // the group's weights [key][head]
   static constexpr int kE = D / 32;
@@ -402,7 +473,8 @@ struct F32Math {
           v[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
         }
       }
-      if constexpr (kPairs == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+#pragma unroll
+      for (int w = kPairs; w < 32; w <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
       const int t = key + kAtOnce * i + lane % kPairs / NH;
       s[i] = fmaf(slope, (float)(t - (sp.L - 1)), score(v[0]));
       if (!visible(sp, t)) s[i] = -INFINITY;
@@ -443,177 +515,274 @@ struct F32Math {
     }
   }
 
-  __device__ __forceinline__ void flush(int, float* o_out, float* ml, int lane) {
+  __device__ __forceinline__ float sum_up() const {
     float v = l;
 #pragma unroll
     for (int w = NH; w < kPairs; w <<= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-    if (lane < NH) {
-      ml[2 * lane] = m;
-      ml[2 * lane + 1] = v;
+    return v;
+  }
+  static __device__ __forceinline__ void put(float* to, const float (&x)[kE], float r, int lane) {
+#pragma unroll
+    for (int e = 0; e < kE; e += kVec)
+      if constexpr (kVec == 4)
+        __stcg(reinterpret_cast<float4*>(to + dim(lane, e)),
+               make_float4(x[e] * r, x[e + 1] * r, x[e + 2] * r, x[e + 3] * r));
+      else
+        __stcg(reinterpret_cast<float2*>(to + dim(lane, e)), make_float2(x[e] * r, x[e + 1] * r));
+  }
+  __device__ __forceinline__ void write_out(Out* out, float* lse, int nh, bool any, int lane) {
+    const float v = sum_up();
+    if (lse && lane < nh) lse[lane] = any ? (m + log2f(v)) * kLn2 : -INFINITY;
+    const float r = any ? 1.f / v : 0.f;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const float rh = __shfl_sync(0xffffffffu, r, h);
+      if (h < nh) put(out + h * D, o[h], rh, lane);
     }
+  }
+  __device__ __forceinline__ void write_piece(float* o_out, float* ml, int nh, int lane) {
+    const float v = sum_up();
+    if (lane < nh) __stcg(reinterpret_cast<float2*>(ml + 2 * lane), make_float2(m, v));
 #pragma unroll
     for (int h = 0; h < NH; ++h)
+      if (h < nh) put(o_out + h * D, o[h], 1.f, lane);
+  }
+
+  __device__ __forceinline__ void flush(int n, float* o_out, float* ml, int lane) {
+    const float v = sum_up();
+    if (lane < NH && lane / kFlush == n) {
+      ml[2 * (lane % kFlush)] = m;
+      ml[2 * (lane % kFlush) + 1] = v;
+    }
+#pragma unroll
+    for (int k = 0; k < NH; ++k) {
+      if (k / kFlush != n) continue;
+      const int h = k % kFlush;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
         const int d = dim(lane, e);
-        o_out[h * D + 4 * merge_unit(h, d >> 2) + (d & 3)] = o[h][e];
+        o_out[h * D + 4 * merge_unit(h, d >> 2) + (d & 3)] = o[k][e];
       }
+    }
   }
 };
 
+__device__ __forceinline__ void add(float4& v, float4 o, float w) {
+  v.x = fmaf(o.x, w, v.x);
+  v.y = fmaf(o.y, w, v.y);
+  v.z = fmaf(o.z, w, v.z);
+  v.w = fmaf(o.w, w, v.w);
+}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
-// Shared memory of a CTA: the rings (192 KB: three groups a warp at 8 KB each, so
-// that two are in flight while one is computed), the merge buffer, its weights.
+// A CTA: 8 warps whose rings take 192 KB, so that 128 KB are in flight while a
+// third is computed; 4 warps where a group is 16 KB; 16 where it is 4 KB (twice
+// the instructions a byte).
 template <class Math, int D>
 struct Shape {
-  static constexpr int kTile = kKeys * Math::kRowBytes;  // K or V of a group
+  static constexpr int kTile = Math::kKeys * Math::kRowBytes;  // K or V of a group
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kWarps = kStage <= 8192 ? 8 : 65536 / kStage;
-  static constexpr int kStages = 196608 / (kWarps * kStage);
+  static constexpr int kWarps = 65536 / kStage;
+  static constexpr int kStages = 3;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kMerge = kWarps * 8 * D * 4;
+  static constexpr int kMerge = kWarps * Math::kFlush * D * 4;
   static constexpr int kSmem = kRing + kMerge + kWarps * (8 * 2 * 4 + Math::kWarpScratch);
-  static_assert(kSmem <= 227 * 1024 - 256, "shared memory of a CTA");
+  static_assert(kSmem <= 227 * 1024 - 512, "shared memory of a CTA");
 };
 
 template <class Math, int D>
 __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(const DecodeParams p) {
   using S = Shape<Math, D>;
   constexpr int kWarps = S::kWarps, kStages = S::kStages, kThreads = kWarps * 32, kHeads = Math::kHeads;
-  constexpr int kPieces = Math::kRowBytes / 16;            // 16-byte pieces of a row
-  constexpr int kCopies = kKeys * kPieces / 32;            // copies of a lane for a K or V tile
+  constexpr int kKeys = Math::kKeys, kRowBytes = Math::kRowBytes;
+  constexpr int kPieces = kRowBytes / 16;        // 16-byte pieces of a row
+  constexpr int kCopies = kKeys * kPieces / 32;  // copies of a lane for a K or V tile
+  constexpr int kLogWarps = kWarps == 16 ? 4 : kWarps == 8 ? 3 : 2;
   extern __shared__ __align__(128) char smem[];
-  __shared__ int64_t s_scan[kWarps];
-  __shared__ int64_t s_total, s_base;
-  __shared__ int s_b;
-  __shared__ bool s_last;
-  struct Piece {  // this CTA's piece of a cut unit
-    int64_t c0;   // the unit's first CTA
-    int others;   // its other pieces; -1: no such unit
-    int heads;
-    int64_t out_row;
+  struct Piece {  // this CTA's piece of a cut team
+    int c0;       // the team's first CTA
+    int others;   // its other pieces; -1: no such team
+    int b, block;
   };
-  __shared__ Piece s_piece[2];  // of the unit that the slice's start cuts, of the one that its end cuts
+  __shared__ Piece s_piece[2];  // of the team that the slice's start cuts, of the one that its end cuts
+  __shared__ int s_sum[kWarps][kLogWarps + 2];
+  __shared__ bool s_last[2];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kStage;
   float* merge = reinterpret_cast<float*>(smem + S::kRing);
   float* merge_ml = reinterpret_cast<float*>(smem + S::kRing + S::kMerge);  // [warp][8][2]
   float* scratch = merge_ml + kWarps * 16 + warp * (Math::kWarpScratch / 4);
-  const int per_request = p.Hkv * p.head_groups;
 
-  // ---- this CTA's slice of the tiles ----
-  auto tiles_of = [&](int b) { return max(1, (span_of(p, b).groups + kWarps - 1) / kWarps); };
-  int64_t sum = 0;
-  for (int b = tid; b < p.B; b += kThreads) sum += tiles_of(b);
-  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  if (lane == 0) s_scan[warp] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    int64_t all = 0;
-    for (int w = 0; w < kWarps; ++w) all += s_scan[w];
-    s_total = all * per_request;
-    s_base = 0;
-    s_b = -1;
-    s_piece[0].others = s_piece[1].others = -1;
+  // ---- teams and the cut ----
+  // tiles of all requests when 2^k warps share a unit's keys, and the longest request's groups
+  int sums[kLogWarps + 1], longest = 0;
+#pragma unroll
+  for (int k = 0; k <= kLogWarps; ++k) sums[k] = 0;
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int n = span_of<kKeys>(p, b).groups;
+    longest = max(longest, n);
+#pragma unroll
+    for (int k = 0; k <= kLogWarps; ++k) sums[k] += max(1, (n + (1 << k) - 1) >> k);
   }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+  for (int k = 0; k <= kLogWarps; ++k) sums[k] = __reduce_add_sync(0xffffffffu, sums[k]);
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k <= kLogWarps; ++k) s_sum[warp][k] = sums[k];
+    s_sum[warp][kLogWarps + 1] = longest;
+  }
+  if (tid == 0) s_piece[0].others = s_piece[1].others = -1;
   __syncthreads();
-  const int64_t T = s_total;
-  const int64_t P = min((int64_t)gridDim.x, T);
+  // The largest team that leaves every CTA 8 tiles and a request at most 16 pieces; else a unit at a time.
+  const int units = p.Hkv * p.head_groups;  // per request
+  longest = s_sum[0][kLogWarps + 1];
+#pragma unroll
+  for (int k = 0; k <= kLogWarps; ++k) sums[k] = s_sum[0][k];
+  for (int w = 1; w < kWarps; ++w) {
+    longest = max(longest, s_sum[w][kLogWarps + 1]);
+#pragma unroll
+    for (int k = 0; k <= kLogWarps; ++k) sums[k] += s_sum[w][k];
+  }
+  int team_log = -1, T = 0;
+#pragma unroll
+  for (int k = 0; k <= kLogWarps; ++k) {
+    const int log = kLogWarps - k;  // of the team
+    if (team_log >= 0 || log > p.team_log) continue;
+    T = sums[k] * (units >> log);
+    const int per = T / (int)gridDim.x;
+    if (log == 0 || (per >= 8 && (longest >> k) <= 16 * per)) team_log = log;
+  }
+  const int share_log = kLogWarps - team_log;        // warps on a unit's keys
+  const int member = warp & ((1 << team_log) - 1);   // this warp's unit in the team
+  const int share = warp >> team_log;                // and its place among those that share it
+  const int blocks = units >> team_log;              // teams per request
+  const int P = min((int)gridDim.x, T);
   if (blockIdx.x >= P) return;
-  const int64_t t0 = cta_start(blockIdx.x, T, P), t1 = cta_start(blockIdx.x + 1, T, P);
-  for (int base = 0; base < p.B; base += kThreads) {  // request of tile t0
-    const int b = base + tid;
-    const int64_t n = b < p.B ? (int64_t)tiles_of(b) * per_request : 0;
-    int64_t incl = n;
-    for (int w = 1; w < 32; w <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, w);
-      if (lane >= w) incl += v;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int64_t start = s_base + incl - n;
-    int64_t all = s_base;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) start += s_scan[w];
-      all += s_scan[w];
-    }
-    __syncthreads();
-    if (start <= t0 && t0 < start + n) {
-      s_b = b;
-      s_base = start;
-    } else if (tid == 0 && all <= t0) {
-      s_base = all;
-    }
-    __syncthreads();
-    if (s_b >= 0) break;
-  }
+  int t = cta_start(blockIdx.x, T, P);
+  const int t1 = cta_start(blockIdx.x + 1, T, P);
+  auto tiles_of = [&](const Span& s) { return max(1, (s.groups + (1 << share_log) - 1) >> share_log); };
 
-  struct Place {  // a tile: request, unit in it, tile in the unit
-    int b, unit, tile, tiles;
+  struct Place {  // a tile: request, team in it, tile in the team
+    int b, block, tile, tiles;
     Span span;
   };
   Place at;
-  at.b = s_b;
-  at.span = span_of(p, at.b);
-  at.tiles = max(1, (at.span.groups + kWarps - 1) / kWarps);
-  at.unit = (int)((t0 - s_base) / at.tiles);
-  at.tile = (int)((t0 - s_base) % at.tiles);
-  auto next_unit = [&](Place& x) {
+  at.b = 0;
+  for (int base = 0;; at.b += 32) {  // of tile t, 32 requests at a time
+    const int b = at.b + lane;
+    const int n = b < p.B ? tiles_of(span_of<kKeys>(p, b)) * blocks : 0;
+    int incl = n;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, w);
+      if (lane >= w) incl += v;
+    }
+    const unsigned behind = __ballot_sync(0xffffffffu, base + incl > t);
+    if (behind || at.b + 32 >= p.B) {
+      const int x = behind ? __ffs(behind) - 1 : 0;
+      base += __shfl_sync(0xffffffffu, incl - n, x);
+      at.b += x;
+      at.span = span_of<kKeys>(p, at.b);
+      at.tiles = tiles_of(at.span);
+      at.block = (t - base) / at.tiles;
+      at.tile = (t - base) % at.tiles;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  auto next_team = [&](Place& x) {
     x.tile = 0;
-    if (++x.unit == per_request) {
-      x.unit = 0;
+    if (++x.block == blocks) {
+      x.block = 0;
       if (++x.b < p.B) {
-        x.span = span_of(p, x.b);
-        x.tiles = max(1, (x.span.groups + kWarps - 1) / kWarps);
+        x.span = span_of<kKeys>(p, x.b);
+        x.tiles = tiles_of(x.span);
       }
     }
+  };
+  struct Unit {
+    int kvh, h0, nh;  // KV head, first query head, query heads
+  };
+  auto unit_of = [&](int block, int who) {
+    const int u = (block << team_log) + who;
+    Unit x;
+    x.kvh = p.head_groups == 1 ? u : u / p.head_groups;
+    const int hg = u - x.kvh * p.head_groups;
+    x.h0 = x.kvh * p.G + hg * kHeads;
+    x.nh = min(kHeads, p.G - hg * kHeads);
+    return x;
+  };
+  auto query = [&](int b, const Unit& u) { return p.q + b * p.q_stride + (int64_t)u.h0 * kRowBytes; };
+  auto touch_queries = [&](int b, int block) {  // into this SM's cache
+    const Unit u = unit_of(block, member);
+    const char* q = query(b, u);
+    for (int i = lane; i < u.nh * (kRowBytes / 128); i += 32)
+      asm volatile("{.reg .b32 x; ld.global.ca.b32 x, [%0];}" ::"l"(q + i * 128));
   };
 
   // ---- copies, kStages - 1 groups ahead, block table entries one more ----
   Place ahead = at;
-  int64_t ahead_left = t1 - t0;
-  // cache row of key lane % 16 of the next group
+  int ahead_left = t1 - t;
+  // cache row of key lane % kKeys of the next group
   auto look_up = [&]() -> int64_t {
     int64_t row = kNoGroup;
     if (ahead_left > 0) {
-      const int i = ahead.tile * kWarps + warp;
+      const int i = (ahead.tile << share_log) + share;
       if (i < ahead.span.groups) {
-        const int t = group_key(ahead.span, i) + lane % kKeys;
+        const int t = group_key<kKeys>(ahead.span, i) + lane % kKeys;
         row = kZeros;
         if (visible(ahead.span, t)) {
-          const int c = t / p.block_size;
+          const int c = (int)((uint64_t)(uint32_t)t * p.div_mul >> p.div_shift);
           const int64_t blk = __ldg(p.table + (int64_t)ahead.b * p.max_blocks + c);
           if (blk >= 0 && blk < p.num_blocks)
-            row = (blk * p.Hkv + ahead.unit / p.head_groups) * p.block_size + (t - c * p.block_size);
+            row = (blk * p.Hkv + unit_of(ahead.block, member).kvh) * p.block_size + (t - c * p.block_size);
           else if (p.status)
             atomicOr(p.status, TV_DEV_BAD_BLOCK);
         }
       }
       --ahead_left;
-      if (++ahead.tile == ahead.tiles) next_unit(ahead);
+      if (++ahead.tile == ahead.tiles) next_team(ahead);
     }
     return row;
   };
   auto copy = [&](int64_t row, int stage) {
     const uint32_t dst = ring + stage * S::kStage;
-    if (row != kNoGroup) {  // the same for the whole warp
+    const int64_t row0 = __shfl_sync(0xffffffffu, row, 0);
+    if (__all_sync(0xffffffffu, row == row0 + lane % kKeys && row >= 0)) {  // consecutive rows: one block
+      const char* k = p.k_cache + row0 * kRowBytes + 16 * lane;
+      const char* v = p.v_cache + row0 * kRowBytes + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int x = i * 32 + lane;
+        const uint32_t to = dst + Math::piece(x / kPieces, x % kPieces);
+        cp_async16(to, k + 512 * i, true);
+        cp_async16(to + S::kTile, v + 512 * i, true);
+      }
+    } else if (row != kNoGroup) {  // the same for the whole warp
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) {
         const int x = i * 32 + lane;
         const int r = x / kPieces, c = x % kPieces;
         const int64_t from = __shfl_sync(0xffffffffu, row, r);
-        const int64_t off = (from < 0 ? 0 : from) * Math::kRowBytes + 16 * c;
+        const int64_t off = (from < 0 ? 0 : from) * kRowBytes + 16 * c;
         cp_async16(dst + Math::piece(r, c), p.k_cache + off, from >= 0);
         cp_async16(dst + S::kTile + Math::piece(r, c), p.v_cache + off, from >= 0);
       }
     }
     cp_async_commit();
   };
+
+  // Row of the workspace's pieces: slot 1 of the CTA that a team starts in, slot 0 of the others.
+  auto part_row = [&](int c, bool starts, int who) {
+    return ((2 * (int64_t)c + starts) * (1 << p.team_log) + who) * p.rows;
+  };
+
+  touch_queries(at.b, at.block);
   int64_t row = look_up();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
@@ -622,25 +791,19 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     copy(now, s);
   }
 
-  // ---- units ----
+  // ---- the slice's teams ----
   const Scorer score(p);
   int stage = 0;
+  uint32_t before[2] = {0, 0};  // pieces that arrived before this CTA's (thread 0)
+  bool cut = false;
   Math math;
-  uint32_t before_lead = 0, before_tail = 0;  // pieces that arrived before this CTA's (thread 0; not waited for until the end)
-  for (int64_t t = t0; t < t1;) {
-    const int kvh = at.unit / p.head_groups, hg = at.unit % p.head_groups;
-    const int h0 = kvh * p.G + hg * kHeads;                    // first query head
-    const int nh = min(kHeads, p.G - hg * kHeads);
-    const int tile1 = (int)min((int64_t)at.tiles, at.tile + (t1 - t));
-    math.begin(p, p.q + at.b * p.q_stride + (int64_t)h0 * Math::kRowBytes, h0, nh, lane);
-    if (t + tile1 - at.tile < t1) {  // the next unit's queries, into this SM's cache
-      const bool same = at.unit + 1 < per_request;
-      const int unit = same ? at.unit + 1 : 0;
-      const int hq = unit / p.head_groups * p.G + unit % p.head_groups * kHeads;
-      const int n = min(kHeads, p.G - unit % p.head_groups * kHeads) * (Math::kRowBytes / 128);
-      if (tid < n)
-        asm volatile("{.reg .b32 x; ld.global.ca.b32 x, [%0];}" ::"l"(
-            p.q + (same ? at.b : at.b + 1) * p.q_stride + (int64_t)hq * Math::kRowBytes + tid * 128));
+  while (t < t1) {
+    const Unit unit = unit_of(at.block, member);
+    const int tile1 = min(at.tiles, at.tile + (t1 - t));
+    math.begin(p, query(at.b, unit), unit.h0, unit.nh, lane);
+    if (t + tile1 - at.tile < t1) {
+      const bool same = at.block + 1 < blocks;
+      touch_queries(same ? at.b : at.b + 1, same ? at.block + 1 : 0);
     }
     for (int tile = at.tile; tile < tile1; ++tile) {
       cp_async_wait<kStages - 2>();
@@ -648,119 +811,219 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
       const int64_t now = row;
       row = look_up();
       copy(now, stage == 0 ? kStages - 1 : stage - 1);
-      const int i = tile * kWarps + warp;
+      const int i = (tile << share_log) + share;
       if (i < at.span.groups)
-        math.group(p, score, at.span, group_key(at.span, i), ring + stage * S::kStage,
+        math.group(p, score, at.span, group_key<kKeys>(at.span, i), ring + stage * S::kStage,
                    ring + stage * S::kStage + S::kTile, lane, scratch);
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 
-    const int64_t u0 = t - at.tile;  // the unit's first tile
     const bool whole = at.tile == 0 && tile1 == at.tiles;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (at.tile == 0 ? 1 : 0);
-    const int64_t out_row = (int64_t)at.b * p.Hq + h0;
-    typename Math::Out* out = reinterpret_cast<typename Math::Out*>(p.out) + out_row * D;
+    const bool any = at.span.groups > 0;
+    if (share_log == 0) {
+      if (whole) {
+        const int64_t out_row = (int64_t)at.b * p.Hq + unit.h0;
+        math.write_out(reinterpret_cast<typename Math::Out*>(p.out) + out_row * D, p.lse ? p.lse + out_row : nullptr,
+                       unit.nh, any, lane);
+      } else {
+        const int64_t to = part_row(blockIdx.x, at.tile == 0, member);
+        math.write_piece(p.part_o + to * D, p.part_ml + to * 2, unit.nh, lane);
+      }
+    } else {
 #pragma unroll
-    for (int n = 0; n < (kHeads + 7) / 8; ++n) {
-      const int heads = min(8, nh - 8 * n);
-      if (heads <= 0) break;
-      __syncthreads();  // the buffer's last readers
-      math.flush(n, merge + warp * 8 * D, merge_ml + warp * 16, lane);
-      __syncthreads();
-      for (int x = tid; x < heads * (D / 4); x += kThreads) {
-        const int h = x / (D / 4), u = x % (D / 4);
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, merge_ml[w * 16 + 2 * h]);
-        float ll = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = merge_ml[w * 16 + 2 * h];
-          const float c = mw == -INFINITY ? 0.f : exp2_approx(mw - mm);
-          const float4 o = *reinterpret_cast<const float4*>(merge + (w * 8 + h) * D + 4 * merge_unit(h, u));
-          ll = fmaf(merge_ml[w * 16 + 2 * h + 1], c, ll);
-          v.x = fmaf(o.x, c, v.x);
-          v.y = fmaf(o.y, c, v.y);
-          v.z = fmaf(o.z, c, v.z);
-          v.w = fmaf(o.w, c, v.w);
-        }
-        const int hh = 8 * n + h;
-        if (whole) {
-          const float r = at.span.groups ? 1.f / ll : 0.f;
-          store4(out + hh * D + 4 * u, make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
-          if (p.lse && u == 0) p.lse[out_row + hh] = at.span.groups ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-        } else {
-          __stcg(reinterpret_cast<float4*>(p.part_o + (slot * kHeads + hh) * D + 4 * u), v);
-          if (u == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + (slot * kHeads + hh) * 2), make_float2(mm, ll));
+      for (int n = 0; n < kHeads / Math::kFlush; ++n) {
+        if (n * Math::kFlush >= p.rows) break;
+        __syncthreads();  // the buffer's last readers
+        math.flush(n, merge + warp * Math::kFlush * D, merge_ml + warp * 16, lane);
+        __syncthreads();
+        for (int x = tid; x < (Math::kFlush * (D / 4)) << team_log; x += kThreads) {
+          const int u = x % (D / 4), h = x / (D / 4) % Math::kFlush, who = x / (D / 4) / Math::kFlush;
+          const Unit of = unit_of(at.block, who);
+          const int hh = Math::kFlush * n + h;
+          if (hh >= of.nh) continue;
+          float mm = -INFINITY;
+          for (int w = who; w < kWarps; w += 1 << team_log) mm = fmaxf(mm, merge_ml[w * 16 + 2 * h]);
+          float ll = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int w = who; w < kWarps; w += 1 << team_log) {
+            const float mw = merge_ml[w * 16 + 2 * h];
+            const float c = mw == -INFINITY ? 0.f : exp2_approx(mw - mm);
+            const float4 o = *reinterpret_cast<const float4*>(merge + (w * Math::kFlush + h) * D + 4 * merge_unit(h, u));
+            ll = fmaf(merge_ml[w * 16 + 2 * h + 1], c, ll);
+            add(v, o, c);
+          }
+          if (whole) {
+            const float r = any ? 1.f / ll : 0.f;
+            const int64_t out_row = (int64_t)at.b * p.Hq + of.h0 + hh;
+            store4(reinterpret_cast<typename Math::Out*>(p.out) + out_row * D + 4 * u,
+                   make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
+            if (p.lse && u == 0) p.lse[out_row] = any ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+          } else {
+            const int64_t to = part_row(blockIdx.x, at.tile == 0, who) + hh;
+            __stcg(reinterpret_cast<float4*>(p.part_o + to * D + 4 * u), v);
+            if (u == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + to * 2), make_float2(mm, ll));
+          }
         }
       }
     }
     if (!whole) {
-      const int64_t c0 = cta_of(u0, T, P), c1 = cta_of(u0 + at.tiles - 1, T, P);
+      cut = true;
       __syncthreads();  // the piece is written; thread 0's release covers it
       if (tid == 0) {
-        const int k = at.tile == 0 ? 1 : 0;
-        s_piece[k] = {c0, (int)(c1 - c0), nh, out_row};
+        const int c0 = cta_of(t - at.tile, T, P), c1 = cta_of(t - at.tile + at.tiles - 1, T, P);
+        s_piece[at.tile == 0 ? 1 : 0] = {c0, c1 - c0, at.b, at.block};
         const uint32_t n = arrive(p.arrive + c0);
-        if (k) before_tail = n; else before_lead = n;
+        if (at.tile == 0) before[1] = n; else before[0] = n;
       }
     }
     t += tile1 - at.tile;
     at.tile = tile1;
-    if (at.tile == at.tiles) next_unit(at);
+    if (at.tile == at.tiles) next_team(at);
   }
   cp_async_wait<0>();
+  if (!cut) return;
 
-  // ---- joins ----
-  __syncthreads();
+  // ---- joins of the teams that the slice's ends cut, where this CTA's piece came last ----
+  if (tid == 0) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const Piece mine = s_piece[k];
-    if (mine.others < 0) continue;
-    if (tid == 0) {
-      s_last = (k ? before_tail : before_lead) == (uint32_t)mine.others;
-      if (s_last) p.arrive[mine.c0] = 0;  // every piece is here
+    for (int k = 0; k < 2; ++k) {
+      s_last[k] = s_piece[k].others >= 0 && before[k] == (uint32_t)s_piece[k].others;
+      if (s_last[k]) p.arrive[s_piece[k].c0] = 0;  // every piece is here
     }
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
-      typename Math::Out* out = reinterpret_cast<typename Math::Out*>(p.out) + mine.out_row * D;
-      for (int x = tid; x < mine.heads * (D / 4); x += kThreads) {
-        const int h = x / (D / 4), u = x % (D / 4);
-        // slot 1 of the unit's first CTA, slot 0 of the others
-        auto slot = [&](int i) { return ((2 * (mine.c0 + i) + (i == 0)) * kHeads + h); };
-        float mm = -INFINITY;
-#pragma unroll 8
-        for (int i = 0; i <= mine.others; ++i) mm = fmaxf(mm, __ldcg(p.part_ml + slot(i) * 2));
-        float ll = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = 0; i <= mine.others; ++i) {
-          const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2));
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(i) * D + 4 * u));
-          const float w = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mm);
-          ll = fmaf(a.y, w, ll);
-          v.x = fmaf(o.x, w, v.x);
-          v.y = fmaf(o.y, w, v.y);
-          v.z = fmaf(o.z, w, v.z);
-          v.w = fmaf(o.w, w, v.w);
-        }
-        const float r = 1.f / ll;
-        store4(out + h * D + 4 * u, make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
-        if (p.lse && u == 0) p.lse[mine.out_row + h] = (mm + log2f(ll)) * kLn2;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (!s_last[k]) continue;
+    const Piece mine = s_piece[k];
+    __threadfence();
+    const int64_t step = part_row(1, false, 0);
+    const int64_t first = part_row(mine.c0, true, 0), other = part_row(mine.c0, false, 0);
+    auto part = [&](int i, int row) { return (i ? other + i * step : first) + row; };  // piece i's row
+    // every row's maximum and sum: 8 lanes a row, a piece each in turn
+    const int rows = p.rows << team_log;
+    float* row_max = merge;
+    float* row_inv = merge + rows;
+    for (int r0 = 0; r0 < rows; r0 += kThreads / 8) {
+      const int r = min(r0 + tid / 8, rows - 1);
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll 4
+      for (int i = tid % 8; i <= mine.others; i += 8) {
+        const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml + part(i, r) * 2));
+        const float m2 = fmaxf(mm, a.x);
+        ll = scaled(ll, mm, m2) + scaled(a.y, a.x, m2);
+        mm = m2;
+      }
+#pragma unroll
+      for (int w = 1; w < 8; w <<= 1) {
+        const float m1 = __shfl_xor_sync(0xffffffffu, mm, w), l1 = __shfl_xor_sync(0xffffffffu, ll, w);
+        const float m2 = fmaxf(mm, m1);
+        ll = scaled(ll, mm, m2) + scaled(l1, m1, m2);
+        mm = m2;
+      }
+      if (tid % 8 == 0) {
+        row_max[r] = mm;
+        row_inv[r] = 1.f / ll;
+        const Unit unit = unit_of(mine.block, r / p.rows);
+        const int h = r % p.rows;
+        if (p.lse && h < unit.nh) p.lse[(int64_t)mine.b * p.Hq + unit.h0 + h] = (mm + log2f(ll)) * kLn2;
       }
     }
     __syncthreads();
+    // the outputs: kAtOnce of a thread and kBatch pieces at a time, as each step is a trip to L2
+    constexpr int kAtOnce = 4, kBatch = 8;
+    const int items = rows * (D / 4);
+    for (int x0 = tid; x0 < items; x0 += kThreads * kAtOnce) {
+      float4 v[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 <= mine.others; i0 += kBatch)
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int x = x0 + j * kThreads;
+          if (x >= items) continue;
+          float4 o[kBatch];
+          float w[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            if (i0 + k > mine.others) continue;
+            const int64_t at_row = part(i0 + k, x / (D / 4));
+            w[k] = __ldcg(p.part_ml + at_row * 2);
+            o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at_row * D + 4 * (x % (D / 4))));
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            if (i0 + k <= mine.others) add(v[j], o[k], scaled(1.f, w[k], row_max[x / (D / 4)]));
+        }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int x = x0 + j * kThreads, r = x / (D / 4), h = r % p.rows;
+        const Unit unit = unit_of(mine.block, r / p.rows);
+        if (x >= items || h >= unit.nh) continue;
+        const float k = row_inv[r];
+        store4(reinterpret_cast<typename Math::Out*>(p.out) + ((int64_t)mine.b * p.Hq + unit.h0 + h) * D + 4 * (x % (D / 4)),
+               make_float4(v[j].x * k, v[j].y * k, v[j].z * k, v[j].w * k));
+      }
+    }
+    __syncthreads();  // row_max is read; the next join writes it
   }
 }
 
+// Largest team of a shape, log2: a power of two that divides a request's units and the warps, with a piece of at
+// most 8192 outputs.
+int team_log_of(int units, int warps, int heads, int D) {
+  int k = 0;
+  while ((2 << k) <= warps && units % (2 << k) == 0 && (2 << k) * heads * D <= 8192) ++k;
+  return k;
+}
+
+// What the workspace holds for a shape and grid, besides the counters.
+struct Room {
+  int rows, head_groups, team_log;
+  size_t floats;  // outputs of all pieces
+  size_t bytes;
+};
+
 template <class Math, int D>
-int launch_decode(DecodeParams p, int ctas, cudaStream_t s) {
+Room room_of(int Hkv, int G, int ctas) {
+  Room r;
+  r.rows = std::min(G, Math::kHeads);
+  r.head_groups = (G + Math::kHeads - 1) / Math::kHeads;
+  // units modulo 16 are all that the team goes by
+  r.team_log = team_log_of((int)((int64_t)Hkv * r.head_groups % 16) + 16, Shape<Math, D>::kWarps, r.rows, D);
+  const size_t rows = ((size_t)ctas * 2 * r.rows) << r.team_log;
+  r.floats = rows * D;
+  r.bytes = rows * (D + 2) * 4;
+  return r;
+}
+
+// What a call asks of the instantiation that fits its shape: its room, or its launch.
+struct Call {
+  int ctas;
+  Room* room;       // non-null: only this
+  DecodeParams* p;
+  cudaStream_t stream;
+};
+
+template <class Math, int D>
+int call_decode(const Call& c, int Hkv, int G) {
+  const Room r = room_of<Math, D>(Hkv, G, c.ctas);
+  if (c.room) {
+    *c.room = r;
+    return TV_OK;
+  }
   constexpr int smem = Shape<Math, D>::kSmem;
-  p.head_groups = (p.G + Math::kHeads - 1) / Math::kHeads;
+  DecodeParams& p = *c.p;
+  p.head_groups = r.head_groups;
+  p.team_log = r.team_log;
+  p.rows = r.rows;
+  p.part_ml = p.part_o + r.floats;
+  const double tiles = (double)p.max_blocks * p.block_size / Math::kKeys + 2;
+  if (tiles * p.B * p.Hkv * p.head_groups >= (double)INT32_MAX)
+    return tv::fail(TV_ERR_UNSUPPORTED, "tv_decode_attn: the work could reach 2^31 groups of %d keys", Math::kKeys);
   TV_CUDA_TRY(cudaFuncSetAttribute(decode_kernel<Math, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  decode_kernel<Math, D><<<ctas, Shape<Math, D>::kWarps * 32, smem, s>>>(p);
+  decode_kernel<Math, D><<<c.ctas, Shape<Math, D>::kWarps * 32, smem, c.stream>>>(p);
   TV_LAUNCH_CHECK("decode_kernel");
   return TV_OK;
 }
@@ -768,31 +1031,23 @@ int launch_decode(DecodeParams p, int ctas, cudaStream_t s) {
 // Query heads of a unit.  bf16: 8, or 16 where a KV head serves more than 8 (two
 // 8-column products share a key's loads), except where their sums would not fit in
 // registers.  float32: as many as the KV head serves, 8 at most.
-int unit_heads(int G, int D, int dtype) {
-  if (dtype == TV_BF16) return G > 8 && D <= 128 ? 16 : 8;
-  return G == 1 ? 1 : G == 2 ? 2 : G <= 4 ? 4 : 8;
-}
-
 template <int D>
-int dispatch_heads(const DecodeParams& p, int dtype, int ctas, cudaStream_t s) {
-  const int heads = unit_heads(p.G, D, dtype);
+int dispatch_heads(const Call& c, int dtype, int Hkv, int G) {
   if (dtype == TV_BF16) {
     if constexpr (D <= 128)
-      if (heads == 16) return launch_decode<Bf16Math<D, 2>, D>(p, ctas, s);
-    return launch_decode<Bf16Math<D, 1>, D>(p, ctas, s);
+      if (G > 8) return call_decode<Bf16Math<D, 2>, D>(c, Hkv, G);
+    return call_decode<Bf16Math<D, 1>, D>(c, Hkv, G);
   }
-  switch (heads) {
-    case 1: return launch_decode<F32Math<D, 1>, D>(p, ctas, s);
-    case 2: return launch_decode<F32Math<D, 2>, D>(p, ctas, s);
-    case 4: return launch_decode<F32Math<D, 4>, D>(p, ctas, s);
-    default: return launch_decode<F32Math<D, 8>, D>(p, ctas, s);
-  }
+  if (G == 1) return call_decode<F32Math<D, 1>, D>(c, Hkv, G);
+  if (G == 2) return call_decode<F32Math<D, 2>, D>(c, Hkv, G);
+  if (G <= 4) return call_decode<F32Math<D, 4>, D>(c, Hkv, G);
+  return call_decode<F32Math<D, 8>, D>(c, Hkv, G);
 }
 
-int dispatch_decode(const DecodeParams& p, int D, int dtype, int ctas, cudaStream_t s) {
-  if (D == 64) return dispatch_heads<64>(p, dtype, ctas, s);
-  if (D == 128) return dispatch_heads<128>(p, dtype, ctas, s);
-  return dispatch_heads<256>(p, dtype, ctas, s);
+int dispatch_decode(const Call& c, int D, int dtype, int Hkv, int G) {
+  if (D == 64) return dispatch_heads<64>(c, dtype, Hkv, G);
+  if (D == 128) return dispatch_heads<128>(c, dtype, Hkv, G);
+  return dispatch_heads<256>(c, dtype, Hkv, G);
 }
 
 // One CTA per SM unless the caller asks for another grid.
@@ -825,8 +1080,9 @@ extern "C" int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t he
   if (!bytes) return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn_workspace_size: null pointer");
   int ctas = 0;
   if (int rc = grid_of(num_ctas, &ctas)) return rc;
-  const int heads = unit_heads(Hq / Hkv, head_dim, dtype);
-  *bytes = (size_t)kCounterBytes + (size_t)ctas * 2 * heads * (head_dim + 2) * 4;
+  Room room;
+  if (int rc = dispatch_decode({ctas, &room, nullptr, nullptr}, head_dim, dtype, Hkv, Hq / Hkv)) return rc;
+  *bytes = (size_t)kCounterBytes + room.bytes;
   return TV_OK;
 }
 
@@ -883,6 +1139,11 @@ extern "C" int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cac
   p.status = status;
   p.arrive = static_cast<uint32_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-  p.part_ml = p.part_o + (size_t)ctas * 2 * unit_heads(p.G, head_dim, dtype) * head_dim;
-  return dispatch_decode(p, head_dim, dtype, ctas, st);
+  // t < 2^31, 2^(s-1) < d <= 2^s, m = ceil(2^(31+s) / d) < 2^32: t m / 2^(31+s) has the whole part of t / d, being
+  // larger by t (m d - 2^(31+s)) / (d 2^(31+s)) < 1 / d
+  uint32_t sh = 0;
+  while ((1ll << sh) < block_size) ++sh;
+  p.div_shift = 31 + sh;
+  p.div_mul = (uint32_t)(((1ull << p.div_shift) + block_size - 1) / block_size);
+  return dispatch_decode({ctas, nullptr, &p, st}, head_dim, dtype, Hkv, p.G);
 }
