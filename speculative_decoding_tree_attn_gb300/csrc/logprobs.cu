@@ -8,18 +8,35 @@
 // histories in masks and positions": node i's logits predict the token emitted
 // at it.
 //
-// One CTA per entry: a pass for (m, S, sum), then one pass per alternative for
-// the largest key below the last one.
-#include <cmath>
-
+// One pass: a row is read once, by a cluster of 1-8 CTAs (the fewer rows, the
+// more), in 16-byte vectors that each thread copies to its own places in shared
+// memory two batches ahead (no barrier; 32 KB in flight a CTA, 4 CTAs an SM).
+// Bound by HBM: V elements a row; an exponential and about six other instructions
+// each, which for bf16 is three quarters of the exponential unit (16 a clock and
+// SM) and half of the issue slots at the full rate of the memory.  Everything is
+// summed in the log2 domain against r = fl(m log2 e): with S = sum 2^(x log2 e - r)
+// the rounding of r cancels in x log2 e - r - log2 S, and a distance is one FMA.
+//
+// The alternatives cost little beside that.  A thread's maximum is kept anyway, and
+// the top_k-th of the warps' 4 largest each is a bar that at least top_k elements
+// reach, and few more.  Only keys above the bar are written down, in the warp's
+// buffer; where one fills up (equal logits, an order of its own), the warp sorts it
+// into a list whose top_k-th key is its own bar from then on.  At the end the CTA's
+// keys above the last bar are ranked by counting.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <cfloat>
+
 #include "common.h"
+
+namespace cg = cooperative_groups;
 
 namespace {
 
 struct LogprobParams {
-  const void* logits;
+  const char* logits;
   const int32_t* tokens;
   const int32_t* node;
   int B, N, C, V;
@@ -31,95 +48,445 @@ struct LogprobParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kVectors = 4;  // of a thread at a time
+constexpr int kStages = 3;
+constexpr int kRing = kStages * kVectors * kThreads * 16;
+constexpr int kTold = 32 / kWarps;  // thread maxima that a warp tells the others
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLeast = -0x1p100f;
 
-// Larger key: larger value, then lower index; NaN as -inf, -0 as +0.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Larger key: larger value, then lower index; NaN as -inf, -0 as +0.  0 is below every key.
 __device__ __forceinline__ uint64_t order_key(float x, int i) {
   x = x == x ? x + 0.f : -INFINITY;
   const uint32_t u = __float_as_uint(x);
   const uint32_t o = u & 0x80000000u ? ~u : u | 0x80000000u;
   return (uint64_t)o << 32 | (uint32_t)~i;
 }
+__device__ __forceinline__ float key_value(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return o == 0 ? -INFINITY : __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(256) logprob_kernel(LogprobParams p) {
-  const int64_t e = blockIdx.x;
-  const int b = (int)(e / p.C), c = (int)(e % p.C);
-  const int tok = p.tokens[e];
-  const int node = p.node ? p.node[e] : c;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  __shared__ float sm[8], ss[8], sx[8];
-  __shared__ uint64_t sk[8];
-  if (tok < 0 || tok >= p.V || node < 0 || node >= p.N) {
-    if (tid == 0) {
-      int bad = 0;
-      if (tok != -1 && (tok < 0 || tok >= p.V)) bad |= TV_DEV_BAD_TOKEN;
-      if (node != -1 && (node < 0 || node >= p.N)) bad |= TV_DEV_BAD_TOPOLOGY;
-      if (bad && p.status) atomicOr(p.status, bad);
-      p.logprob[e] = 0.f;
-      if (p.entropy) p.entropy[e] = 0.f;
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static constexpr uint32_t kMinusInf = 0xff800000u;
+  static __device__ __forceinline__ float largest(uint4 v) {  // NaN if one is
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  static __device__ __forceinline__ uint4 held(uint4 v) {  // at least kLeast
+    return make_uint4(__float_as_uint(fmaxf(__uint_as_float(v.x), kLeast)), __float_as_uint(fmaxf(__uint_as_float(v.y), kLeast)),
+                      __float_as_uint(fmaxf(__uint_as_float(v.z), kLeast)), __float_as_uint(fmaxf(__uint_as_float(v.w), kLeast)));
+  }
+  static __device__ __forceinline__ void unpack(uint4 v, float (&x)[kN]) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static constexpr uint32_t kMinusInf = 0xff80ff80u;
+  static __device__ __forceinline__ float largest(uint4 v) {
+    uint32_t m;
+    asm("{\n\t.reg .b32 a, b;\n\tmax.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 b, %3, %4;\n\tmax.NaN.bf16x2 %0, a, b;\n\t}"
+        : "=r"(m)
+        : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 held(uint4 v) {
+    auto two = [](uint32_t x) {
+      uint32_t y;
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xf180f180u));  // -2^100
+      return y;
+    };
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+  }
+  static __device__ __forceinline__ void unpack(uint4 v, float (&x)[kN]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    for (int k = tid; k < p.top_k; k += blockDim.x) {
-      p.top_ids[e * p.top_k + k] = -1;
-      p.top_logprobs[e * p.top_k + k] = -INFINITY;
+  }
+};
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// m: the largest x, or up to 8 less; against r = fl(m log2 e), d = x log2 e - r: s = sum 2^d, t = sum 2^d d.
+// Logits are held at -2^100, whose power is 0 (an excluded one's infinite distance
+// would make its product NaN).  The maximum's own distance is r's rounding, which
+// has to stay small: for |m| > 2^20 (no logits of a model), d = (x - m) log2 e, held
+// at -300.
+constexpr float kFar = -300.f;
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e); }
+__device__ __forceinline__ bool huge(float m) { return fabsf(m) > 1048576.f && m != -INFINITY; }
+__device__ __forceinline__ float distance(float x, float m) {
+  return huge(m) ? (x - m) * kLog2e : __fmaf_rn(x, kLog2e, -reference(m));
+}
+struct Sums {
+  float m, s, t;
+  __device__ __forceinline__ void raise(float m2) {  // to a larger maximum
+    const float d = m == -INFINITY ? kFar
+                                   : fmaxf(huge(m) || huge(m2) ? (m - m2) * kLog2e : reference(m) - reference(m2), kFar);
+    const float c = exp2_approx(d);
+    t = c * fmaf(d, s, t);
+    s *= c;
+    m = m2;
+  }
+  __device__ __forceinline__ void add(float d) {
+    const float e = exp2_approx(d);
+    s += e;
+    t = fmaf(e, d, t);
+  }
+};
+__device__ __forceinline__ Sums warp_join(Sums a) {  // every lane the same result
+  float m = a.m;
+#pragma unroll
+  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  if (a.m < m) a.raise(m);
+#pragma unroll
+  for (int w = 16; w; w >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, w);
+    a.t += __shfl_xor_sync(0xffffffffu, a.t, w);
+  }
+  return a;
+}
+
+// The candidates of a warp: keys above the bar wait in its buffer in shared memory;
+// when there are 32 they are sorted into a list, one key per lane, descending.
+struct Best {
+  uint64_t mine = 0, bar = 0;  // top_k keys of the row are at least the bar
+  float bar_value = -INFINITY;
+  int waiting = 0;
+
+  __device__ __forceinline__ void raise(uint64_t key) {
+    if (key > bar) {
+      bar = key;
+      bar_value = key_value(key);
+    }
+  }
+  __device__ __forceinline__ void offer(uint64_t key, uint64_t* buffer, int k, int lane) {  // every lane its key
+    const unsigned hit = __ballot_sync(0xffffffffu, key > bar);
+    if (key > bar) buffer[waiting + __popc(hit & ((1u << lane) - 1))] = key;
+    waiting += __popc(hit);
+    if (waiting >= 32) take(buffer, k, lane);
+  }
+  __device__ void take(uint64_t* buffer, int k, int lane) {  // the first 32 waiting
+    __syncwarp();
+    uint64_t x = buffer[lane];
+    const uint64_t rest = 32 + lane < waiting ? buffer[32 + lane] : 0;
+    __syncwarp();
+    if (32 + lane < waiting) buffer[lane] = rest;
+    waiting -= 32;
+#pragma unroll 1
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll 1
+      for (int w = size >> 1; w; w >>= 1) {
+        const uint64_t o = __shfl_xor_sync(0xffffffffu, x, w);
+        x = (!(lane & size) == !(lane & w)) == (x > o) ? x : o;  // blocks descend where the size's bit is clear
+      }
+    join(x, lane);
+    raise(__shfl_sync(0xffffffffu, mine, k - 1));
+  }
+  // The 32 largest of two descending lists.
+  __device__ __forceinline__ void join(uint64_t other, int lane) {
+    const uint64_t o = __shfl_sync(0xffffffffu, other, 31 - lane);
+    mine = o > mine ? o : mine;
+#pragma unroll 1
+    for (int w = 16; w; w >>= 1) {
+      const uint64_t x = __shfl_xor_sync(0xffffffffu, mine, w);
+      mine = !(lane & w) == (mine > x) ? mine : x;
+    }
+  }
+  // This warp's 4 largest thread maxima, for the bar.
+  __device__ __forceinline__ void tell(uint32_t* shared, float m, int lane) const {
+    uint32_t o = (uint32_t)(order_key(m, 0) >> 32), mine4 = 0;
+#pragma unroll
+    for (int j = 0; j < kTold; ++j) {
+      const uint32_t v = __reduce_max_sync(0xffffffffu, o);
+      if (lane == j) mine4 = v;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, o == v)) - 1) o = 0;
+    }
+    if (lane < kTold) *(volatile uint32_t*)(shared + lane) = mine4;
+  }
+  __device__ __forceinline__ void heed(const uint32_t* shared, int k, int lane) {  // the k-th of all warps'
+    uint32_t v = *(const volatile uint32_t*)(shared + lane);
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+      for (int w = size >> 1; w; w >>= 1) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, v, w);
+        v = !(lane & size) == !(lane & w) ? max(v, o) : min(v, o);
+      }
+    raise((uint64_t)__shfl_sync(0xffffffffu, v, k - 1) << 32);  // under every index of that value
+  }
+};
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParams p) {
+  using V_ = Vec<T>;
+  constexpr int kN = V_::kN;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t e = blockIdx.x / ctas;
+  const int b = (int)(e / p.C), c = (int)(e - (int64_t)b * p.C);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int tok = __ldg(p.tokens + e);
+  const int node = p.node ? __ldg(p.node + e) : c;
+  __shared__ Sums s_sums[kWarps + 1];
+  __shared__ int s_bad;
+  __shared__ uint64_t s_wait[kWarps][64], s_best[32];
+  extern __shared__ __align__(16) char s_ring[];
+  uint64_t* s_pool = reinterpret_cast<uint64_t*>(s_ring);  // [kWarps * 64], once the stream is over
+  __shared__ uint32_t s_bar[32];
+  __shared__ int s_pool_size;
+  if (tok < 0 || tok >= p.V || node < 0 || node >= p.N) {  // no entry: the same for the whole cluster
+    if (rank == 0) {
+      if (tid == 0) {
+        int bad = 0;
+        if (tok != -1 && (tok < 0 || tok >= p.V)) bad |= TV_DEV_BAD_TOKEN;
+        if (node != -1 && (node < 0 || node >= p.N)) bad |= TV_DEV_BAD_TOPOLOGY;
+        if (bad && p.status) atomicOr(p.status, bad);
+        p.logprob[e] = 0.f;
+        if (p.entropy) p.entropy[e] = 0.f;
+      }
+      if (kTop && tid < p.top_k) {
+        p.top_ids[e * p.top_k + tid] = -1;
+        p.top_logprobs[e * p.top_k + tid] = -INFINITY;
+      }
     }
     return;
   }
-  const T* row = static_cast<const T*>(p.logits) + ((int64_t)b * p.N + node) * p.V;
-  float m = -INFINITY;
-  for (int i = tid; i < p.V; i += 256) m = fmaxf(m, to_f32(row[i]));
-  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  if (lane == 0) sm[warp] = m;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, sm[w]);
-  float s = 0.f, x1 = 0.f;
-  for (int i = tid; i < p.V; i += 256) {
-    const float d = to_f32(row[i]) - m, ex = expf(d);
-    s += ex;
-    x1 += d == -INFINITY ? 0.f : ex * d;
-  }
-  for (int w = 16; w; w >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, w);
-    x1 += __shfl_xor_sync(0xffffffffu, x1, w);
-  }
-  if (lane == 0) {
-    ss[warp] = s;
-    sx[warp] = x1;
-  }
-  __syncthreads();
-  s = x1 = 0.f;
-  for (int w = 0; w < 8; ++w) {
-    s += ss[w];
-    x1 += sx[w];
-  }
-  const float ln_s = logf(s);
-  if (tid == 0) {
-    p.logprob[e] = to_f32(row[tok]) - m - ln_s;
-    if (p.entropy) p.entropy[e] = ln_s - x1 / s;
-  }
-  uint64_t last = ~0ull;
-  for (int k = 0; k < p.top_k; ++k) {
-    uint64_t best = 0;
-    for (int i = tid; i < p.V; i += 256) {
-      const uint64_t key = order_key(to_f32(row[i]), i);
-      if (key < last && key > best) best = key;
+  const T* row = reinterpret_cast<const T*>(p.logits) + ((int64_t)b * p.N + node) * p.V;
+  // elements before the first 16-byte boundary, vectors, elements behind the last
+  const int lead = min(p.V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) % 16 / sizeof(T)));
+  const int vectors = (p.V - lead) / kN;
+  const int loose = p.V - vectors * kN;
+  const uint4* vec = reinterpret_cast<const uint4*>(row + lead);
+  const int v0 = (int)((int64_t)vectors * rank / ctas), v1 = (int)((int64_t)vectors * (rank + 1) / ctas);
+  const float x_tok = tid == 0 && rank == 0 ? to_f32(row[tok]) : 0.f;
+
+  Sums sums = {-INFINITY, 0.f, 0.f};
+  Best best;
+  float peak = -INFINITY;  // the largest logit, or a NaN
+  // this thread's places in the ring: [stage][vector]; a vector past the end is all -inf there
+  constexpr int kBatch = kThreads * kVectors, kStageBytes = kBatch * 16;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + tid * 16;
+  const uint4* from = vec + v0 + tid;
+  int left = v1 - v0 - tid;  // vectors that this thread has yet to fetch, in steps of kThreads
+  auto fetch = [&](uint32_t to) {
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) {
+      if (left > u * kThreads)
+        cp_async16(to + u * kThreads * 16, from + u * kThreads);
+      else
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + u * kThreads * 16), "r"(V_::kMinusInf) : "memory");
     }
-    for (int w = 16; w; w >>= 1) {
-      const uint64_t o = __shfl_xor_sync(0xffffffffu, best, w);
-      best = o > best ? o : best;
-    }
-    if (lane == 0) sk[warp] = best;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    from += kBatch;
+    left -= kBatch;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(ring + i * kStageBytes);
+  if (kTop) {
+    if (tid < 32) s_bar[tid] = 0;
+    if (tid == 0) s_pool_size = 0;
     __syncthreads();
-    for (int w = 0; w < 8; ++w) best = sk[w] > best ? sk[w] : best;
-    __syncthreads();
-    if (tid == 0) {
-      const int id = (int)~(uint32_t)best;
-      p.top_ids[e * p.top_k + k] = id;
-      p.top_logprobs[e * p.top_k + k] = to_f32(row[id]) - m - ln_s;
-    }
-    last = best;
   }
+  uint32_t at = ring, to = ring + (kStages - 1) * kStageBytes;
+  float limit = -INFINITY;  // sums are raised to a maximum 8 above their own: powers of up to 2^12 until then
+  bool far = false;         // huge(sums.m)
+  int refresh = v0;         // the batch after which the bar is raised: the 1st, 2nd, 6th, 22nd, ..
+#pragma unroll 1
+  for (int base = v0; base < v1; base += kBatch) {  // the same for every warp of the CTA
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    fetch(to);
+    uint4 now[kVectors];
+    float top[kVectors];
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) {
+      now[u] = lds128(at + u * kThreads * 16);
+      top[u] = V_::largest(now[u]);
+    }
+    float m = top[0];
+#pragma unroll
+    for (int u = 1; u < kVectors; ++u) m = max_nan(m, top[u]);
+    peak = max_nan(peak, m);
+    if (m > limit) {
+      sums.raise(m);
+      limit = m + 8.f;
+      far = huge(m);
+    }
+    if (far) {
+#pragma unroll 1
+      for (int u = 0; u < kVectors; ++u) {
+        float x[kN];
+        V_::unpack(lds128(at + u * kThreads * 16), x);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) sums.add(fmaxf((x[i] - sums.m) * kLog2e, kFar));
+      }
+    } else {
+      const float r = reference(sums.m);
+#pragma unroll
+      for (int u = 0; u < kVectors; ++u) {
+        float x[kN];
+        V_::unpack(V_::held(now[u]), x);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) sums.add(__fmaf_rn(x[i], kLog2e, -r));
+      }
+    }
+    if (kTop) {
+      if (base == refresh) {
+        best.tell(s_bar + warp * kTold, peak, lane);
+        if (base == v0) __syncthreads();
+        best.heed(s_bar, p.top_k, lane);
+        refresh = v0 + 4 * (base - v0) + kBatch;
+      }
+      if (__any_sync(0xffffffffu, !(m < best.bar_value))) {
+        unsigned vectors_hit = 0;
+#pragma unroll
+        for (int u = 0; u < kVectors; ++u)
+          if (__any_sync(0xffffffffu, !(top[u] < best.bar_value))) vectors_hit |= 1u << u;
+#pragma unroll 1
+        while (vectors_hit) {  // few: read again, which leaves the registers to the stream
+          const int u = __ffs(vectors_hit) - 1;
+          vectors_hit &= vectors_hit - 1;
+          const int v = base + tid + u * kThreads;
+          float x[kN];
+          V_::unpack(lds128(at + u * kThreads * 16), x);
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (__any_sync(0xffffffffu, !(x[i] < best.bar_value)))
+              best.offer(v < v1 ? order_key(x[i], lead + v * kN + i) : 0, s_wait[warp], p.top_k, lane);
+        }
+      }
+    }
+    at = at == ring + (kStages - 1) * kStageBytes ? ring : at + kStageBytes;
+    to = to == ring + (kStages - 1) * kStageBytes ? ring : to + kStageBytes;
+  }
+  if (rank == 0 && warp == 0) {  // fewer than 16 elements besides the vectors
+    const int i = lane < lead ? lane : lead + vectors * kN + lane - lead;
+    const bool here = lane < loose;
+    const float x = here ? to_f32(row[i]) : -INFINITY;
+    if (x > sums.m) sums.raise(x);
+    peak = max_nan(peak, x);
+    sums.add(fmaxf(distance(x, sums.m), kFar));
+    if (kTop) best.offer(here ? order_key(x, i) : 0, s_wait[warp], p.top_k, lane);
+  }
+
+  // ---- the CTA's warps, then the cluster's CTAs ----
+  if (kTop) best.tell(s_bar + warp * kTold, peak, lane);
+  sums = warp_join(sums);
+  if (lane == 0) s_sums[warp] = sums;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");  // nothing is left on its way into the ring
+  const int any_bad = __syncthreads_or(!(peak <= FLT_MAX));  // a NaN or +inf
+  if (kTop) {
+    best.heed(s_bar, p.top_k, lane);
+    auto keep = [&](uint64_t key) {
+      const unsigned hit = __ballot_sync(0xffffffffu, key > best.bar);
+      int at = 0;
+      if (lane == 0 && hit) at = atomicAdd(&s_pool_size, __popc(hit));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1));
+      if (key > best.bar) s_pool[at] = key;
+    };
+    // the list's own keys reach the bar that came from it
+    best.bar = best.bar ? best.bar - 1 : 0;
+    keep(best.mine);
+    keep(lane < best.waiting ? s_wait[warp][lane] : 0);
+    if (tid < 32) s_best[tid] = 0;
+    __syncthreads();
+    const int n = s_pool_size;
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t key = s_pool[i];
+      int above = 0;
+      for (int k = 0; k < n; ++k) above += s_pool[k] > key;
+      if (above < 32) s_best[above] = key;
+    }
+  }
+  const Sums nothing = {-INFINITY, 0.f, 0.f};
+  if (warp == 0) {
+    sums = warp_join(lane < kWarps ? s_sums[lane] : nothing);
+    if (lane == 0) {
+      s_sums[kWarps] = sums;
+      s_bad = any_bad;
+    }
+  }
+  if (ctas > 1) {
+    cluster.sync();
+  } else {
+    __syncthreads();
+  }
+  if (rank == 0 && warp == 0) {
+    if (kTop) best.mine = s_best[lane];
+    Sums all = sums;
+    int wrong = any_bad;
+    if (ctas > 1) {
+      all = warp_join(lane < ctas ? *cluster.map_shared_rank(&s_sums[kWarps], lane) : nothing);
+      wrong = __any_sync(0xffffffffu, lane < ctas && *cluster.map_shared_rank(&s_bad, lane));
+      if (kTop)
+        for (int r = 1; r < ctas; ++r) best.join(*cluster.map_shared_rank(&s_best[lane], r), lane);
+    }
+    // a row without a distribution: a NaN or +inf in it, or nothing above -inf
+    const float log2_s = wrong || all.m == -INFINITY ? NAN : log2f(all.s);
+    const float ln_s = (log2_s - distance(all.m, all.m)) * kLn2;  // ln sum e^(x - m)
+    if (lane == 0) {
+      p.logprob[e] = x_tok - all.m - ln_s;
+      if (p.entropy) p.entropy[e] = (log2_s - all.t / all.s) * kLn2;
+    }
+    if (kTop && lane < p.top_k) {
+      p.top_ids[e * p.top_k + lane] = (int)~(uint32_t)best.mine;
+      p.top_logprobs[e * p.top_k + lane] = key_value(best.mine) - all.m - ln_s;
+    }
+  }
+  if (ctas > 1) cluster.sync();  // its shared memory is read until here
+}
+
+template <typename T>
+int launch_logprobs(const LogprobParams& p, int sm_count, cudaStream_t stream) {
+  // A cluster per row, doubled while the grid has under 2 CTAs an SM and a CTA at least 16 KB of the row.
+  const int64_t rows = (int64_t)p.B * p.C;
+  int ctas = 1;
+  while (ctas < 8 && rows * ctas < 2 * sm_count && (int64_t)p.V * sizeof(T) >= 2 * 16384 * ctas) ctas *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRing;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  auto kernel = p.top_k ? logprob_kernel<T, true> : logprob_kernel<T, false>;
+  TV_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing));
+  TV_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
+  return TV_OK;
 }
 
 }  // namespace
@@ -138,14 +505,12 @@ extern "C" int tv_token_logprobs(const void* logits, const int32_t* tokens, cons
     return tv::fail(TV_ERR_INVALID_ARG, "tv_token_logprobs: null pointer");
   if (reinterpret_cast<uintptr_t>(logits) & 15)
     return tv::fail(TV_ERR_INVALID_ARG, "tv_token_logprobs: logits must be 16-byte aligned");
-  if ((int64_t)B * C >= INT32_MAX)
-    return tv::fail(TV_ERR_UNSUPPORTED, "tv_token_logprobs: B * C exceeds 2^31");
-  LogprobParams p{logits, tokens, node, B, N, C, V, logprob, entropy, top_k, top_ids, top_logprobs, status};
-  const unsigned grid = (unsigned)(B * C);
-  if (dtype == TV_BF16)
-    logprob_kernel<__nv_bfloat16><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-  else
-    logprob_kernel<float><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-  TV_LAUNCH_CHECK("logprob_kernel");
-  return TV_OK;
+  if ((int64_t)B * C >= INT32_MAX / 8)
+    return tv::fail(TV_ERR_UNSUPPORTED, "tv_token_logprobs: B * C exceeds 2^31 / 8");
+  tv::DeviceInfo dev;
+  if (int rc = tv::current_device_info(&dev)) return rc;
+  LogprobParams p{static_cast<const char*>(logits), tokens, node, B, N, C, V, logprob, entropy, top_k, top_ids,
+                  top_logprobs, status};
+  return dtype == TV_BF16 ? launch_logprobs<__nv_bfloat16>(p, dev.sm_count, (cudaStream_t)stream)
+                          : launch_logprobs<float>(p, dev.sm_count, (cudaStream_t)stream);
 }

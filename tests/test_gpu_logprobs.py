@@ -133,6 +133,23 @@ def test_special_rows(name, dtype, copies):
         np.testing.assert_allclose(to_np(many[0][0, 0]), ref[0][0, 0], rtol=2e-5, atol=2e-5)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_at_the_ends_of_the_type(dtype):
+    """A row masked to the lowest value throughout is uniform; one logit near the largest value takes everything."""
+    V, lo = 30011, torch.finfo(DT[dtype]).min
+    x = torch.full((1, 4, V), lo, dtype=DT[dtype], device="cuda")
+    x[0, 1, 77] = -lo
+    x[0, 2, :] = -lo
+    x[0, 3, 5] = lo / 2
+    t = torch.tensor([[9, 77, 8, 9]], dtype=torch.int32, device="cuda")
+    lp, ent, ids, top = (g[0].tolist() for g in capi.tv_token_logprobs(x, t, top_k=2))
+    # one float32 sum of V equal terms, rel of the bound above: under 2e-5
+    for r in (0, 2):
+        assert abs(lp[r] + np.log(V)) <= 2e-5 and abs(ent[r] - np.log(V)) <= 2e-4 and ids[r] == [0, 1]
+    assert lp[1] == 0 and ent[1] == 0 and ids[1] == [77, 0] and top[1][0] == 0 and top[1][1] < -1e38
+    assert lp[3] < -1e38 and ent[3] == 0 and ids[3] == [5, 0] and top[3][0] == 0
+
+
 def test_what_greedy_acceptance_returns():
     """out and path of the greedy walk go straight in; each emitted token is its row's first alternative."""
     w = W.WORKLOADS["gqa_b8_l512_2048_n26"]
