@@ -126,42 +126,66 @@ def _dev(t, name, dtypes):
     return t
 
 
-def _dev_rows(t, name, dtype, tail):
-    """A CUDA tensor [T, *tail] of dtype whose rows are contiguous (any stride between them)."""
+def _current():
+    """Current device and its current stream's handle, without the objects that torch.cuda makes for them
+    (8 us of a call's 20); no tensor is on device -2."""
+    if not torch.cuda.is_initialized():
+        return -2, 0
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _refuse(t, name, dtype, shape, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 3 or t.shape[1:] != tail:
-        raise ValueError(f"{name} must be {dtype} [T, {tail[0]}, {tail[1]}], got {t.dtype} {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 and tail[1] > 1 or t.stride(1) != tail[1] and tail[0] > 1):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    want = "x".join("*" if n is None else str(n) for n in shape)
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {want}, got {t.dtype} {tuple(t.shape)}"
+                     + ("" if t.is_contiguous() else ", not contiguous"))
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of exactly this type and shape on device dev."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _arg_rows(t, name, dtype, shape, dev):
+    """Address and row stride of a tensor [T, H, D] whose rows are contiguous (any stride between them)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _refuse(t, name, dtype, shape, dev)
+    rows, inner, last = t.stride()
+    if (last != 1 and shape[2] > 1 or inner != shape[2] and shape[1] > 1) and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
-    return t
+    return t.data_ptr(), rows
 
 
-def _dev_shaped(t, name, dtype, shape):
-    """A contiguous CUDA tensor of exactly this dtype and shape."""
-    _dev(t, name, (dtype,))
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
+def _arg_cache(k_cache, v_cache, block_table, B, dev):
+    """Addresses and sizes of a paged cache [num_blocks, Hkv, block_size, D] and its block table [B, max_blocks]."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.dtype not in (torch.float32, torch.bfloat16):
+        _refuse(k_cache, "k_cache", "float32 or bfloat16", (None,) * 4, dev)
+    shape = k_cache.shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        _refuse(block_table, "block_table", torch.int32, (B, None), dev)
+    width = block_table.shape[1]
+    dt = k_cache.dtype
+    return (_arg(k_cache, "k_cache", dt, shape, dev), _arg(v_cache, "v_cache", dt, shape, dev), shape, dt,
+            _arg(block_table, "block_table", torch.int32, (B, width), dev), width)
 
 
-def _one_device(*tensors):
-    """Every tensor lives on the current device (whose stream the call uses)."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"tensor on {t.device}, current device is cuda:{cur}")
+def _arg_batch(seq_lens, dev):
+    """Address and length of seq_lens [B]."""
+    if not isinstance(seq_lens, torch.Tensor):
+        _refuse(seq_lens, "seq_lens", torch.int32, (None,), dev)
+    B = seq_lens.numel()
+    return _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), B
 
 
-def _dev_cache(k_cache, v_cache, block_table, B):
-    """Checks a paged cache [num_blocks, Hkv, block_size, D] and its block table [B, max_blocks]."""
-    _dev(k_cache, "k_cache", (torch.float32, torch.bfloat16))
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [num_blocks, Hkv, block_size, D], got {tuple(k_cache.shape)}")
-    _dev_shaped(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
-    _dev(block_table, "block_table", (torch.int32,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
+def _arg_status(status, dev):
+    return None if status is None else _arg(status, "status", torch.int32, status.shape, dev)
 
 
 def _code(dtype):
@@ -528,44 +552,33 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
     seq_lens; q [T, Hq, D] is rotated into q_out (may be q).  Rows of k_new, v_new,
     q and q_out may be strided.  cu_new int32 [B + 1]: packed offsets; None: T / B
     tokens each.  Returns (q_out, new_seq_lens int32 [B])."""
-    _dev(seq_lens, "seq_lens", (torch.int32,))
-    B = seq_lens.numel()
-    _dev_cache(k_cache, v_cache, block_table, B)
-    num_blocks, Hkv, bs, D = k_cache.shape
-    dt = k_cache.dtype
-    _dev_rows(k_new, "k_new", dt, (Hkv, D))
-    _dev_rows(v_new, "v_new", dt, (Hkv, D))
+    dev, st = _current()
+    lens, B = _arg_batch(seq_lens, dev)
+    kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
     T = k_new.shape[0]
+    k, k_stride = _arg_rows(k_new, "k_new", dt, (T, Hkv, D), dev)
+    v, v_stride = _arg_rows(v_new, "v_new", dt, (T, Hkv, D), dev)
+    cs = qp = qo = cu = None
     Hq = max_pos = q_stride = out_stride = 0
-    if v_new.shape[0] != T:
-        raise ValueError(f"v_new has {v_new.shape[0]} rows, k_new {T}")
     if cos_sin is not None:
         max_pos = cos_sin.shape[0]
-        _dev_shaped(cos_sin, "cos_sin", torch.float32, (max_pos, 2, D // 2))
+        cs = _arg(cos_sin, "cos_sin", torch.float32, (max_pos, 2, D // 2), dev)
     if q is not None:
         Hq = q.shape[1]
-        _dev_rows(q, "q", dt, (Hq, D))
+        qp, q_stride = _arg_rows(q, "q", dt, (T, Hq, D), dev)
         if q_out is None:
             q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device)
-        else:
-            _dev_rows(q_out, "q_out", dt, (Hq, D))
-        if q.shape[0] != T or q_out.shape[0] != T:
-            raise ValueError(f"q and q_out must have k_new's {T} rows")
-        q_stride, out_stride = q.stride(0), q_out.stride(0)
+        qo, out_stride = _arg_rows(q_out, "q_out", dt, (T, Hq, D), dev)
     if cu_new is not None:
-        _dev_shaped(cu_new, "cu_new", torch.int32, (B + 1,))
+        cu = _arg(cu_new, "cu_new", torch.int32, (B + 1,), dev)
     if new_seq_lens is None:
         new_seq_lens = torch.empty_like(seq_lens)
-    else:
-        _dev_shaped(new_seq_lens, "new_seq_lens", torch.int32, seq_lens.shape)
-    if status is not None:
-        _dev(status, "status", (torch.int32,))
-    _one_device(k_cache, v_cache, block_table, seq_lens, k_new, v_new, q, q_out, cos_sin, cu_new, new_seq_lens, status)
-    _check("tv_kv_append",
-           lib().tv_kv_append(_ptr(q), q_stride, _ptr(q_out), out_stride, Hq, _ptr(k_new), k_new.stride(0),
-                              _ptr(v_new), v_new.stride(0), _ptr(cu_new), T, _ptr(k_cache), _ptr(v_cache), num_blocks,
-                              bs, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(new_seq_lens),
-                              _ptr(cos_sin), max_pos, B, Hkv, D, _code(dt), _ptr(status), _stream(stream)))
+    code = lib().tv_kv_append(qp, q_stride, qo, out_stride, Hq, k, k_stride, v, v_stride, cu, T, kc, vc, num_blocks, bs,
+                              table, width, lens, _arg(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev), cs,
+                              max_pos, B, Hkv, D, TV_F32 if dt is torch.float32 else TV_BF16, _arg_status(status, dev),
+                              st if stream is None else stream.cuda_stream)
+    if code:
+        _check("tv_kv_append", code)
     return q_out, new_seq_lens
 
 
@@ -582,37 +595,27 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     its K/V already); returns out [B, Hq, D].  q [B, Hq, D] may be strided
     between requests; softcap, window / n_sink and slopes as in the header;
     lse float32 [B, Hq] is filled when given."""
-    _dev(seq_lens, "seq_lens", (torch.int32,))
-    B = seq_lens.numel()
-    _dev_cache(k_cache, v_cache, block_table, B)
-    num_blocks, Hkv, bs, D = k_cache.shape
-    dt = k_cache.dtype
+    dev, st = _current()
+    lens, B = _arg_batch(seq_lens, dev)
+    kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
     Hq = q.shape[1]
-    _dev_rows(q, "q", dt, (Hq, D))
-    if q.shape[0] != B:
-        raise ValueError(f"q has {q.shape[0]} rows, expected {B}")
-    if slopes is not None:
-        _dev_shaped(slopes, "slopes", torch.float32, (Hq,))
+    qp, q_stride = _arg_rows(q, "q", dt, (B, Hq, D), dev)
     if out is None:
         out = torch.empty(B, Hq, D, dtype=dt, device=q.device)
-    else:
-        _dev_shaped(out, "out", dt, (B, Hq, D))
-    if lse is not None:
-        _dev_shaped(lse, "lse", torch.float32, (B, Hq))
-    if status is not None:
-        _dev(status, "status", (torch.int32,))
     if workspace is None:
         workspace = alloc_workspace(tv_decode_attn_workspace_size(Hq, Hkv, D, dt, num_ctas), q.device)
         flags |= TV_ATTN_WORKSPACE_ZEROED
-    else:
-        _dev(workspace, "workspace", (torch.uint8,))
-    _one_device(q, k_cache, v_cache, block_table, seq_lens, slopes, out, lse, workspace, status)
-    _check("tv_decode_attn",
-           lib().tv_decode_attn(_ptr(q), q.stride(0), _ptr(k_cache), _ptr(v_cache), num_blocks, bs, _ptr(block_table),
-                                block_table.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, _code(dt),
-                                1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), window, n_sink,
-                                _ptr(slopes), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), num_ctas,
-                                flags, _ptr(status), _stream(stream)))
+    n_ws = workspace.numel()
+    code = lib().tv_decode_attn(qp, q_stride, kc, vc, num_blocks, bs, table, width, lens, B, Hq, Hkv, D,
+                                TV_F32 if dt is torch.float32 else TV_BF16,
+                                1.0 / math.sqrt(D) if scale is None else scale, softcap, window, n_sink,
+                                None if slopes is None else _arg(slopes, "slopes", torch.float32, (Hq,), dev),
+                                _arg(out, "out", dt, (B, Hq, D), dev),
+                                None if lse is None else _arg(lse, "lse", torch.float32, (B, Hq), dev),
+                                _arg(workspace, "workspace", torch.uint8, (n_ws,), dev), n_ws, num_ctas, flags,
+                                _arg_status(status, dev), st if stream is None else stream.cuda_stream)
+    if code:
+        _check("tv_decode_attn", code)
     return out
 
 
@@ -622,37 +625,32 @@ def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entro
     logits [B, N, V] (float32 or bf16); returns (logprob, entropy [B, C] float32,
     top_ids int32, top_logprobs float32 [B, C, top_k]).  tokens and node may be
     out and path of tv_tree_accept_*: -1 is no entry."""
-    _dev(logits, "logits", (torch.float32, torch.bfloat16))
-    _dev(tokens, "tokens", (torch.int32,))
-    if logits.dim() != 3 or tokens.dim() != 2 or tokens.shape[0] != logits.shape[0]:
-        raise ValueError(f"logits [B, N, V] and tokens [B, C] expected, got {tuple(logits.shape)}, "
-                         f"{tuple(tokens.shape)}")
+    dev, st = _current()
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3 or logits.dtype not in (torch.float32, torch.bfloat16):
+        _refuse(logits, "logits", "float32 or bfloat16", (None,) * 3, dev)
     B, N, V = logits.shape
+    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
+        _refuse(tokens, "tokens", torch.int32, (B, None), dev)
     C = tokens.shape[1]
-    if node is not None:
-        _dev_shaped(node, "node", torch.int32, (B, C))
-    dev = logits.device
+    f32, where = torch.float32, logits.device
+    x = _arg(logits, "logits", logits.dtype, (B, N, V), dev)
+    tok = _arg(tokens, "tokens", torch.int32, (B, C), dev)
+    row = None if node is None else _arg(node, "node", torch.int32, (B, C), dev)
+    k = max(top_k, 0)
     if logprob is None:
-        logprob = torch.empty(B, C, dtype=torch.float32, device=dev)
-    else:
-        _dev_shaped(logprob, "logprob", torch.float32, (B, C))
+        logprob = torch.empty((B, C), dtype=f32, device=where)
     if entropy is None:
-        entropy = torch.empty(B, C, dtype=torch.float32, device=dev)
-    else:
-        _dev_shaped(entropy, "entropy", torch.float32, (B, C))
+        entropy = torch.empty((B, C), dtype=f32, device=where)
     if top_ids is None:
-        top_ids = torch.empty(B, C, max(top_k, 0), dtype=torch.int32, device=dev)
-    else:
-        _dev_shaped(top_ids, "top_ids", torch.int32, (B, C, top_k))
+        top_ids = torch.empty((B, C, k), dtype=torch.int32, device=where)
     if top_logprobs is None:
-        top_logprobs = torch.empty(B, C, max(top_k, 0), dtype=torch.float32, device=dev)
-    else:
-        _dev_shaped(top_logprobs, "top_logprobs", torch.float32, (B, C, top_k))
-    if status is not None:
-        _dev(status, "status", (torch.int32,))
-    _one_device(logits, tokens, node, logprob, entropy, top_ids, top_logprobs, status)
-    _check("tv_token_logprobs",
-           lib().tv_token_logprobs(_ptr(logits), _ptr(tokens), _ptr(node), B, N, C, V, _code(logits.dtype),
-                                   _ptr(logprob), _ptr(entropy), top_k, _ptr(top_ids), _ptr(top_logprobs),
-                                   _ptr(status), _stream(stream)))
+        top_logprobs = torch.empty((B, C, k), dtype=f32, device=where)
+    code = lib().tv_token_logprobs(x, tok, row, B, N, C, V, TV_F32 if logits.dtype is f32 else TV_BF16,
+                                   _arg(logprob, "logprob", f32, (B, C), dev),
+                                   _arg(entropy, "entropy", f32, (B, C), dev), top_k,
+                                   _arg(top_ids, "top_ids", torch.int32, (B, C, k), dev),
+                                   _arg(top_logprobs, "top_logprobs", f32, (B, C, k), dev), _arg_status(status, dev),
+                                   st if stream is None else stream.cuda_stream)
+    if code:
+        _check("tv_token_logprobs", code)
     return logprob, entropy, top_ids, top_logprobs

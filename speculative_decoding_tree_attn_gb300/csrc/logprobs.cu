@@ -88,6 +88,27 @@ __device__ __forceinline__ float key_value(uint64_t key) {
   return o == 0 ? -INFINITY : __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 template <typename T>
 struct Vec;
 template <>
@@ -351,14 +372,26 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
         for (int i = 0; i < kN; ++i) sums.add(fmaxf((x[i] - sums.m) * kLog2e, kFar));
       }
     } else {
+      // two at a time in a register pair: three instructions for both besides their exponentials
       const float r = reference(sums.m);
+      const uint64_t scale = pack2(kLog2e, kLog2e), shift = pack2(-r, -r);
+      uint64_t s2 = 0, t2 = 0;
 #pragma unroll
       for (int u = 0; u < kVectors; ++u) {
         float x[kN];
         V_::unpack(V_::held(now[u]), x);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) sums.add(__fmaf_rn(x[i], kLog2e, -r));
+        for (int i = 0; i < kN; i += 2) {
+          const uint64_t d = fma2(pack2(x[i], x[i + 1]), scale, shift);
+          const float2 y = unpack2(d);
+          const uint64_t e = pack2(exp2_approx(y.x), exp2_approx(y.y));
+          s2 = add2(s2, e);
+          t2 = fma2(e, d, t2);
+        }
       }
+      const float2 a = unpack2(s2), b = unpack2(t2);
+      sums.s += a.x + a.y;
+      sums.t += b.x + b.y;
     }
     if (kTop) {
       if (base == refresh) {

@@ -300,3 +300,22 @@ def test_is_the_one_node_tree(dtype):
     got = capi.tv_decode_attn(inp["q"][:, 0], kc, vc, inp["block_table"], lens)
     tol = 2e-2 if dtype == "bf16" else 1e-4  # the tree kernels' own
     assert float((got.float() - want[:, 0].float()).abs().max()) <= tol
+
+
+def test_binding_checks_every_argument():
+    """Each wrong type, shape, layout and place is refused by name before anything is launched."""
+    c = _case([40, 9], 4, 2, 64, "bf16", 16, 171)
+    good = dict(q=c["q"], k_cache=c["k"], v_cache=c["v"], block_table=c["table"], seq_lens=c["lens"])
+    bad = dict(q=c["q"][:1], k_cache=c["k"].half(), v_cache=c["v"][:, :1], block_table=c["table"][:1],
+               seq_lens=c["lens"].long(), out=torch.empty(2, 4, 64, device="cuda"),
+               lse=torch.empty(2, 3, device="cuda"), slopes=torch.ones(3, device="cuda"),
+               workspace=torch.zeros(100, dtype=torch.int32, device="cuda"), status=torch.zeros(1, device="cuda"))
+    for name, x in bad.items():
+        with pytest.raises(ValueError, match=name):
+            capi.tv_decode_attn(**{**good, name: x})
+    with pytest.raises(ValueError, match="contiguous rows"):
+        capi.tv_decode_attn(**{**good, "q": c["q"].transpose(1, 2).contiguous().transpose(1, 2)})
+    with pytest.raises(ValueError, match="k_cache"):
+        capi.tv_decode_attn(**{**good, "k_cache": c["k"].cpu()})
+    with pytest.raises(capi.TVError, match="workspace"):
+        capi.tv_decode_attn(**good, workspace=torch.zeros(100, dtype=torch.uint8, device="cuda"))

@@ -189,3 +189,14 @@ def test_logprobs_oracle_against_torch():
         np.testing.assert_allclose(top[b, n], v.numpy(), atol=1e-13)
     nan = OL.token_logprobs(np.full((1, 1, 4), -np.inf), np.array([[2]]), None, 2)
     assert np.isnan(nan[0]).all() and np.isnan(nan[1]).all() and nan[2][0, 0].tolist() == [0, 1]
+
+
+def test_binding_names_what_it_refuses():
+    lens, table = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    cache, q = torch.zeros(3, 1, 16, 64), torch.zeros(2, 4, 64)
+    for call in (lambda: capi.tv_decode_attn(q, cache, cache, table, lens),
+                 lambda: capi.tv_decode_attn(q, cache, cache, table, [0, 0]),
+                 lambda: capi.tv_token_logprobs(torch.zeros(2, 3, 10), lens[:, None]),
+                 lambda: capi.tv_token_logprobs(None, lens[:, None])):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            call()
