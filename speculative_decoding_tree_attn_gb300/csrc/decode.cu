@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   }
   if (tid == 0) s_piece[0].others = s_piece[1].others = -1;
   __syncthreads();
-  // The largest team that leaves every CTA 8 tiles and a request at most 16 pieces; else a unit at a time.
+  // The largest team that leaves every CTA 8 tiles and a team about 3 pieces; else a unit at a time.
   const int units = p.Hkv * p.head_groups;  // per request
   longest = s_sum[0][kLogWarps + 1];
 #pragma unroll
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     if (team_log >= 0 || log > p.team_log) continue;
     T = sums[k] * (units >> log);
     const int per = T / (int)gridDim.x;
-    if (log == 0 || (per >= 8 && (longest >> k) <= 16 * per)) team_log = log;
+    if (log == 0 || (per >= 8 && (longest >> k) <= 2 * per)) team_log = log;
   }
   const int share_log = kLogWarps - team_log;        // warps on a unit's keys
   const int member = warp & ((1 << team_log) - 1);   // this warp's unit in the team
