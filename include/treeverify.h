@@ -569,7 +569,7 @@ int tv_kv_commit(void* k_cache, void* v_cache, int64_t num_blocks, int32_t block
  * a later token whose own block is valid may be stored past that length.
  * q_out rows are written for every token whose position is in the rotary table.
  * head_dim in {16, 32, 64, 128, 256}; every buffer and token stride a multiple
- * of 16 bytes (else TV_ERR_INVALID_ARG).
+ * of 16 bytes (else TV_ERR_INVALID_ARG; the strides of a single token are not used).
  */
 int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t Hq,
                  const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
@@ -624,7 +624,8 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * status     device int32 (nullable): TV_DEV_BAD_BLOCK (a visible position's
  *            block is outside [0, num_blocks): its key and value count as zeros).
  * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, any Hq / Hkv; q, out and
- * the caches 16-byte aligned, q_stride a multiple of 16 bytes.  TV_ERR_UNSUPPORTED
+ * the caches 16-byte aligned, q_stride a multiple of 16 bytes (unused for one
+ * request).  TV_ERR_UNSUPPORTED
  * where the work could reach 2^31 groups of 4-16 keys (requests x KV heads x
  * head groups of 8 or 16 x max_blocks * block_size / keys).
  */

@@ -163,6 +163,12 @@ def _arg_rows(t, name, dtype, shape, dev):
     return t.data_ptr(), rows
 
 
+def _rows(t, name, dev):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        _refuse(t, name, "float32 or bfloat16", (None,) * 3, dev)
+    return t.shape[0]
+
+
 def _arg_cache(k_cache, v_cache, block_table, B, dev):
     """Addresses and sizes of a paged cache [num_blocks, Hkv, block_size, D] and its block table [B, max_blocks]."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.dtype not in (torch.float32, torch.bfloat16):
@@ -555,15 +561,16 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
     dev, st = _current()
     lens, B = _arg_batch(seq_lens, dev)
     kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
-    T = k_new.shape[0]
+    T = _rows(k_new, "k_new", dev)
     k, k_stride = _arg_rows(k_new, "k_new", dt, (T, Hkv, D), dev)
     v, v_stride = _arg_rows(v_new, "v_new", dt, (T, Hkv, D), dev)
     cs = qp = qo = cu = None
     Hq = max_pos = q_stride = out_stride = 0
     if cos_sin is not None:
-        max_pos = cos_sin.shape[0]
+        max_pos = _rows(cos_sin, "cos_sin", dev)
         cs = _arg(cos_sin, "cos_sin", torch.float32, (max_pos, 2, D // 2), dev)
     if q is not None:
+        _rows(q, "q", dev)
         Hq = q.shape[1]
         qp, q_stride = _arg_rows(q, "q", dt, (T, Hq, D), dev)
         if q_out is None:
@@ -598,6 +605,7 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     dev, st = _current()
     lens, B = _arg_batch(seq_lens, dev)
     kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
+    _rows(q, "q", dev)
     Hq = q.shape[1]
     qp, q_stride = _arg_rows(q, "q", dt, (B, Hq, D), dev)
     if out is None:

@@ -29,6 +29,7 @@
 //   leaves (max, sum, output) of each piece in the workspace; the CTA whose piece
 //   arrives last joins them in order, so results do not depend on timing.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -148,7 +149,10 @@ __device__ __forceinline__ int cta_of(int t, int T, int P) { return (int)((((int
 struct Scorer {
   float mul, cap2, cap_mul;  // mul: scale log2 e;  cap2: softcap log2 e, 0 without
   __device__ __forceinline__ explicit Scorer(const DecodeParams& p)
-      : mul(p.scale * kLog2e), cap2(p.softcap * kLog2e), cap_mul(p.softcap > 0.f ? 2.f * kLog2e * p.scale / p.softcap : 0.f) {}
+      : mul(p.scale * kLog2e), cap2(p.softcap * kLog2e), cap_mul(0.f) {
+    // a finite factor for the smallest caps too: 0 has to stay 0
+    if (p.softcap > 0.f) cap_mul = fmaxf(fminf(2.f * kLog2e * p.scale / p.softcap, FLT_MAX), -FLT_MAX);
+  }
   __device__ __forceinline__ float operator()(float x) const {
     // tanh y = 1 - 2 / (1 + e^2y): absolute error of a few 2^-24, saturating at both ends
     if (cap2 > 0.f) return cap2 - 2.f * cap2 * __frcp_rn(1.f + exp2_approx(x * cap_mul));
@@ -1103,7 +1107,7 @@ extern "C" int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cac
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out)
     return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: null pointer");
   const int64_t e = dtype == TV_F32 ? 4 : 2;
-  if (q_stride < 0 || (q_stride * e) % 16 ||
+  if ((B > 1 && (q_stride < 0 || (q_stride * e) % 16)) ||
       ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
         reinterpret_cast<uintptr_t>(out)) & 15))
     return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: buffers and the q stride must be multiples of 16 bytes");

@@ -255,9 +255,10 @@ extern "C" int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_
     return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: new_seq_lens must not alias seq_lens");
   const int64_t e = dtype == TV_F32 ? 4 : 2;
   const int64_t kv_row = (int64_t)Hkv * head_dim, q_row = (int64_t)Hq * head_dim;
-  if (k_stride < 0 || v_stride < 0 || (q && (q_stride < 0 || (T > 1 && q_out_stride < q_row))))
+  const bool many = T > 1;  // one token's strides do not matter
+  if (many && (k_stride < 0 || v_stride < 0 || (q && (q_stride < 0 || q_out_stride < q_row))))
     return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: bad token stride");
-  if ((k_stride * e) % 16 || (v_stride * e) % 16 || (q && ((q_stride * e) % 16 || (q_out_stride * e) % 16)) ||
+  if ((many && ((k_stride * e) % 16 || (v_stride * e) % 16 || (q && ((q_stride * e) % 16 || (q_out_stride * e) % 16)))) ||
       ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
         reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) | reinterpret_cast<uintptr_t>(q) |
         reinterpret_cast<uintptr_t>(q ? q_out : nullptr) | reinterpret_cast<uintptr_t>(cos_sin)) & 15))

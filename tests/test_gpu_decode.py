@@ -114,6 +114,17 @@ def test_splits(dtype, D, num_ctas):
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("G,D,dtype", [(1, 64, "bf16"), (4, 128, "bf16"), (8, 128, "bf16"), (16, 64, "bf16"),
+                                       (12, 128, "bf16"), (3, 256, "bf16"), (1, 64, "f32"), (2, 128, "f32"),
+                                       (8, 256, "f32"), (5, 128, "f32")])
+@pytest.mark.parametrize("num_ctas", [4, 10, 16])
+def test_heads_read_together(G, D, dtype, num_ctas):
+    """Enough work a CTA that its warps take several KV heads at a time; requests cut between CTAs, unused slots."""
+    c = _case([1000, 990, 0, 1003, 997, 1, 960, 1000, 985], 8 * G, 8, D, dtype, 16, 2500 + G + D)
+    out, lse = _run(c, num_ctas=num_ctas)
+    _check(c, out, lse)
+
+
 OPTIONS = [
     dict(softcap=5.0), dict(softcap=30.0, scale=0.7), dict(window=1), dict(window=100), dict(window=128, n_sink=4),
     dict(window=33, n_sink=17), dict(window=1000, n_sink=50), dict(window=5, n_sink=100000), dict(n_sink=4),
@@ -139,6 +150,25 @@ def test_masks_caps_and_biases(opt, Hq, Hkv, D, dtype, bs):
     for num_ctas in (0, 9):
         out, lse = _run(c, num_ctas=num_ctas, **opt)
         _check(c, out, lse, **opt)
+
+
+def test_a_cap_near_zero():
+    """Every score is held at the cap: all keys alike, zeros among them."""
+    c = _case([300, 17], 4, 2, 64, "bf16", 16, 61)
+    c["q"][0, 0] = 0
+    for cap in (1e-3, 1e-30, 1e-38):
+        out, lse = _run(c, softcap=cap)
+        _check(c, out, lse, softcap=cap)
+
+
+def test_one_request_with_any_stride():
+    c = _case([100], 4, 2, 64, "bf16", 16, 62)
+    want, _ = _run(c)
+    odd = torch.empty(4, 64, 1, device="cuda", dtype=torch.bfloat16).permute(2, 0, 1)
+    odd.copy_(c["q"])
+    assert odd.stride(0) == 1
+    got, _ = _run(dict(c, q=odd))
+    assert torch.equal(got, want)
 
 
 def test_extreme_scores():

@@ -206,3 +206,64 @@ def test_append_then_tree_attention_reads_the_prompt():
     assert torch.equal(new, inp["seq_lens"])
     got = capi.tv_tree_attn_verify(inp["q"], kc, vc, inp["block_table"], new, inp["k_tree"], inp["v_tree"], mask)
     assert torch.equal(got, want)
+
+
+def test_one_token_with_any_stride():
+    c = _case([7], [1], 4, 2, 64, "bf16", 16, 31, fused=False)
+    want = _append(c, cu=False)
+    odd = {}
+    for n in "qkv":
+        odd[n] = torch.empty(c[n].shape[1], 64, 1, device="cuda", dtype=torch.bfloat16).permute(2, 0, 1)
+        odd[n].copy_(c[n])
+        assert odd[n].stride(0) == 1
+    for a, b in zip(_append(dict(c, **odd), cu=False), want):
+        assert torch.equal(a, b)
+
+
+def test_a_step_captured_and_replayed():
+    """Replays append at the lengths that are in the buffer then; the offsets may change too."""
+    c = _case([5, 30], [1, 1], 4, 2, 64, "bf16", 16, 33, fused=False)
+    kc, vc = torch.zeros_like(c["k_cache"]), torch.zeros_like(c["v_cache"])
+    new, q_out = torch.empty_like(c["lens"]), torch.empty_like(c["q"])
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    lens = c["lens"].clone()
+
+    def call():
+        capi.tv_kv_append(c["k"], c["v"], kc, vc, c["table"], lens, cos_sin=c["cs"], q=c["q"], q_out=q_out, cu_new=cu,
+                          new_seq_lens=new)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for at, offsets in (([5, 30], [0, 1, 2]), ([0, 14], [0, 0, 2]), ([4, 2], [0, 2, 2])):
+        lens.copy_(torch.tensor(at, dtype=torch.int32))
+        cu.copy_(torch.tensor(offsets, dtype=torch.int32))
+        kc.zero_()
+        vc.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        k2, v2 = torch.zeros_like(kc), torch.zeros_like(vc)
+        q2, l2 = capi.tv_kv_append(c["k"], c["v"], k2, v2, c["table"], lens, cos_sin=c["cs"], q=c["q"], cu_new=cu)
+        assert torch.equal(kc, k2) and torch.equal(vc, v2) and torch.equal(new, l2) and torch.equal(q_out, q2)
+        assert l2.tolist() == [at[b] + offsets[b + 1] - offsets[b] for b in range(2)]
+
+
+def test_binding_checks_every_argument():
+    c = _case([7, 3], [2, 2], 4, 2, 64, "bf16", 16, 35, fused=False)
+    good = dict(k_new=c["k"], v_new=c["v"], k_cache=c["k_cache"], v_cache=c["v_cache"], block_table=c["table"],
+                seq_lens=c["lens"], cos_sin=c["cs"], q=c["q"], cu_new=c["cu"])
+    bad = dict(k_new=c["k"].float(), v_new=c["v"][:3], k_cache=c["k_cache"][0], v_cache=c["v_cache"].float(),
+               block_table=c["table"].long(), seq_lens=c["lens"].cpu(), cos_sin=c["cs"][:, 0], q=c["q"][0],
+               cu_new=c["cu"][:2], q_out=c["q"].float(), new_seq_lens=c["lens"].long(), status=c["lens"].float())
+    for name, x in bad.items():
+        with pytest.raises(ValueError, match=name):
+            capi.tv_kv_append(**{**good, name: x})
+    with pytest.raises(capi.TVError, match="cos_sin"):
+        capi.tv_kv_append(**{**good, "cos_sin": None})
+    with pytest.raises(capi.TVError, match="alias"):
+        capi.tv_kv_append(**good, new_seq_lens=c["lens"])
