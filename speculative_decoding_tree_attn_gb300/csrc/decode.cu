@@ -12,13 +12,15 @@
 // - A unit is (request, KV head, up to 8 or 16 query heads).  A CTA's warps take a
 //   team of units at a time, all KV heads of a request where there are 8: they
 //   then read whole cache blocks together (one KV head's part of a 16-token block
-//   is 4 KB; with the warps on one head's keys instead, 64 requests of 1k-8k
-//   tokens took 202 us, with this 176 us).  Where the lengths leave too few tiles
-//   for that, several warps share a unit's keys.
+//   is 4 KB) and meet only at a cut.  64 requests of 1k-8k tokens, 32/8 heads of 128:
+//   189 us (0.95 of the measured copy rate), with the warps on one unit's keys 203.
+//   Where the lengths leave too few tiles, or too many pieces, several warps share a
+//   unit's keys (16 x 32k, 64/8 heads: 320 us, 0.99; as whole teams 334).
 // - Teams' tiles (a group of keys per warp) lie end to end and each CTA of a
-//   persistent grid takes an equal run of them.  (Small runs at the end, taken by
-//   whichever CTA is done, would even out the SMs' unequal shares of the memory, 4 %
-//   in the stream alone; the pieces they cut the last requests into cost more.)
+//   persistent grid takes an equal run of them.  SMs do not get equal shares of the
+//   memory: the first CTA is done at 0.87 of the last one's time.  Small runs at the
+//   end, taken by whichever CTA is done, gained 4 % in the stream alone and lost it
+//   to the pieces that they cut the last requests into.
 // - Each warp copies its own groups through its own ring in shared memory
 //   (cp.async, rows looked up in the block table one step ahead), so nothing in
 //   the stream waits for another warp.
@@ -31,6 +33,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -626,7 +629,8 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   int sums[kLogWarps + 1], longest = 0;
 #pragma unroll
   for (int k = 0; k <= kLogWarps; ++k) sums[k] = 0;
-  for (int b = tid; b < p.B; b += kThreads) {
+  const bool few = p.B <= 32;  // every warp sums for itself
+  for (int b = few ? lane : tid; b < p.B; b += kThreads) {
     const int n = span_of<kKeys>(p, b).groups;
     longest = max(longest, n);
 #pragma unroll
@@ -635,23 +639,25 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
   for (int k = 0; k <= kLogWarps; ++k) sums[k] = __reduce_add_sync(0xffffffffu, sums[k]);
-  if (lane == 0) {
-#pragma unroll
-    for (int k = 0; k <= kLogWarps; ++k) s_sum[warp][k] = sums[k];
-    s_sum[warp][kLogWarps + 1] = longest;
-  }
   if (tid == 0) s_piece[0].others = s_piece[1].others = -1;
-  __syncthreads();
+  if (!few) {
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k <= kLogWarps; ++k) s_sum[warp][k] = sums[k];
+      s_sum[warp][kLogWarps + 1] = longest;
+    }
+    __syncthreads();
+    longest = s_sum[0][kLogWarps + 1];
+#pragma unroll
+    for (int k = 0; k <= kLogWarps; ++k) sums[k] = s_sum[0][k];
+    for (int w = 1; w < kWarps; ++w) {
+      longest = max(longest, s_sum[w][kLogWarps + 1]);
+#pragma unroll
+      for (int k = 0; k <= kLogWarps; ++k) sums[k] += s_sum[w][k];
+    }
+  }
   // The largest team that leaves every CTA 8 tiles and a team about 3 pieces; else a unit at a time.
   const int units = p.Hkv * p.head_groups;  // per request
-  longest = s_sum[0][kLogWarps + 1];
-#pragma unroll
-  for (int k = 0; k <= kLogWarps; ++k) sums[k] = s_sum[0][k];
-  for (int w = 1; w < kWarps; ++w) {
-    longest = max(longest, s_sum[w][kLogWarps + 1]);
-#pragma unroll
-    for (int k = 0; k <= kLogWarps; ++k) sums[k] += s_sum[w][k];
-  }
   int team_log = -1, T = 0;
 #pragma unroll
   for (int k = 0; k <= kLogWarps; ++k) {
@@ -900,76 +906,125 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     if (!s_last[k]) continue;
-    const Piece mine = s_piece[k];
-    __threadfence();
-    const int64_t step = part_row(1, false, 0);
-    const int64_t first = part_row(mine.c0, true, 0), other = part_row(mine.c0, false, 0);
-    auto part = [&](int i, int row) { return (i ? other + i * step : first) + row; };  // piece i's row
-    // every row's maximum and sum: 8 lanes a row, a piece each in turn
+    const Piece mine = s_piece[k];  // read behind the barrier: what thread 0's arrival acquired is there for all
+    // row of piece i in the workspace (at most 4096 CTAs, 2 pieces, 64 KB of outputs: under 2^31 floats)
+    const int step = (int)part_row(1, false, 0);
+    const int first = (int)part_row(mine.c0, true, 0), other = (int)part_row(mine.c0, false, 0);
+    auto part = [&](int i, int row) { return (i ? other + i * step : first) + row; };
+    auto to_row = [&](int r, bool& here) {  // output row of the pieces' row r
+      const Unit unit = unit_of(mine.block, r / p.rows);
+      here = r % p.rows < unit.nh;
+      return (int64_t)mine.b * p.Hq + unit.h0 + r % p.rows;
+    };
+    auto put = [&](int64_t row, int u, float4 v, float x) {
+      store4(reinterpret_cast<typename Math::Out*>(p.out) + row * D + 4 * u, make_float4(v.x * x, v.y * x, v.z * x, v.w * x));
+    };
     const int rows = p.rows << team_log;
+    const int items = rows * (D / 4);
+    constexpr int kBatch = kThreads > 256 ? 4 : 8;  // pieces that a thread has on their way at once (registers)
+    if (mine.others < kBatch) {  // all of them: one trip to L2
+      for (int x = tid; x < items; x += kThreads) {
+        const int r = x / (D / 4), u = x % (D / 4);
+        float4 o[kBatch];
+        float2 a[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (i > mine.others) continue;
+          const uint32_t from = (uint32_t)part(i, r);
+          a[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + from);
+          o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (from * (D / 4) + u));
+        }
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i <= mine.others) mm = fmaxf(mm, a[i].x);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (i > mine.others) continue;
+          const float w = scaled(1.f, a[i].x, mm);
+          ll = fmaf(a[i].y, w, ll);
+          add(v, o[i], w);
+        }
+        bool here;
+        const int64_t row = to_row(r, here);
+        if (!here) continue;
+        put(row, u, v, 1.f / ll);
+        if (p.lse && u == 0) p.lse[row] = (mm + log2f(ll)) * kLn2;
+      }
+      continue;
+    }
+    // every row's maximum and sum: 8 or 32 lanes a row, a piece each in turn
     float* row_max = merge;
     float* row_inv = merge + rows;
-    for (int r0 = 0; r0 < rows; r0 += kThreads / 8) {
-      const int r = min(r0 + tid / 8, rows - 1);
+    const int wide = rows * 32 <= kThreads ? 32 : 8;
+    for (int r0 = 0; r0 < rows; r0 += kThreads / wide) {
+      const int r = min(r0 + tid / wide, rows - 1);
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll 4
-      for (int i = tid % 8; i <= mine.others; i += 8) {
-        const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml + part(i, r) * 2));
+      for (int i = tid % wide; i <= mine.others; i += wide) {
+        const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part(i, r));
         const float m2 = fmaxf(mm, a.x);
         ll = scaled(ll, mm, m2) + scaled(a.y, a.x, m2);
         mm = m2;
       }
-#pragma unroll
-      for (int w = 1; w < 8; w <<= 1) {
+      for (int w = 1; w < wide; w <<= 1) {
         const float m1 = __shfl_xor_sync(0xffffffffu, mm, w), l1 = __shfl_xor_sync(0xffffffffu, ll, w);
         const float m2 = fmaxf(mm, m1);
         ll = scaled(ll, mm, m2) + scaled(l1, m1, m2);
         mm = m2;
       }
-      if (tid % 8 == 0) {
+      if (tid % wide == 0) {
         row_max[r] = mm;
         row_inv[r] = 1.f / ll;
-        const Unit unit = unit_of(mine.block, r / p.rows);
-        const int h = r % p.rows;
-        if (p.lse && h < unit.nh) p.lse[(int64_t)mine.b * p.Hq + unit.h0 + h] = (mm + log2f(ll)) * kLn2;
+        bool here;
+        const int64_t row = to_row(r, here);
+        if (p.lse && here) p.lse[row] = (mm + log2f(ll)) * kLn2;
       }
     }
     __syncthreads();
-    // the outputs: kAtOnce of a thread and kBatch pieces at a time, as each step is a trip to L2
-    constexpr int kAtOnce = 4, kBatch = 8;
-    const int items = rows * (D / 4);
-    for (int x0 = tid; x0 < items; x0 += kThreads * kAtOnce) {
-      float4 v[kAtOnce];
+    // the outputs: some of a thread's and some pieces at a time, as each step is a trip to L2
+    auto sum_up = [&](auto results, auto pieces) {
+      constexpr int kAtOnce = decltype(results)::value, kPieces = decltype(pieces)::value;
+      for (int x0 = tid; x0 < items; x0 += kThreads * kAtOnce) {
+        float4 v[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 <= mine.others; i0 += kBatch)
+        for (int j = 0; j < kAtOnce; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i0 = 0; i0 <= mine.others; i0 += kPieces)
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int x = x0 + j * kThreads;
-          if (x >= items) continue;
-          float4 o[kBatch];
-          float w[kBatch];
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int x = x0 + j * kThreads;
+            if (x >= items) continue;
+            const int r = x / (D / 4);
+            const float top = row_max[r];
+            float4 o[kPieces];
+            float w[kPieces];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            if (i0 + k > mine.others) continue;
-            const int64_t at_row = part(i0 + k, x / (D / 4));
-            w[k] = __ldcg(p.part_ml + at_row * 2);
-            o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at_row * D + 4 * (x % (D / 4))));
+            for (int k = 0; k < kPieces; ++k) {
+              if (i0 + k > mine.others) continue;
+              const uint32_t at_row = (uint32_t)part(i0 + k, r);
+              w[k] = __ldcg(p.part_ml + at_row * 2);
+              o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at_row * (D / 4) + x % (D / 4)));
+            }
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+              if (i0 + k <= mine.others) add(v[j], o[k], scaled(1.f, w[k], top));
           }
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-            if (i0 + k <= mine.others) add(v[j], o[k], scaled(1.f, w[k], row_max[x / (D / 4)]));
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int x = x0 + j * kThreads, r = x / (D / 4);
+          if (x >= items) continue;
+          bool here;
+          const int64_t row = to_row(r, here);
+          if (here) put(row, x % (D / 4), v[j], row_inv[r]);
         }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int x = x0 + j * kThreads, r = x / (D / 4), h = r % p.rows;
-        const Unit unit = unit_of(mine.block, r / p.rows);
-        if (x >= items || h >= unit.nh) continue;
-        const float k = row_inv[r];
-        store4(reinterpret_cast<typename Math::Out*>(p.out) + ((int64_t)mine.b * p.Hq + unit.h0 + h) * D + 4 * (x % (D / 4)),
-               make_float4(v[j].x * k, v[j].y * k, v[j].z * k, v[j].w * k));
       }
-    }
+    };
+    if (items <= kThreads)
+      sum_up(std::integral_constant<int, 1>{}, std::integral_constant<int, 2 * kBatch>{});
+    else
+      sum_up(std::integral_constant<int, 4>{}, std::integral_constant<int, kBatch>{});
     __syncthreads();  // row_max is read; the next join writes it
   }
 }
