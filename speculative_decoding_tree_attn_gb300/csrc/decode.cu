@@ -93,6 +93,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // x 2^(m - top), a sum against m as one against top; nothing has been summed against -inf.
 __device__ __forceinline__ float scaled(float x, float m, float top) {
   return m == -INFINITY ? x : x * exp2_approx(m - top);
@@ -154,13 +160,18 @@ struct Scorer {
   __device__ __forceinline__ explicit Scorer(const DecodeParams& p)
       : mul(p.scale * kLog2e), cap2(p.softcap * kLog2e), cap_mul(0.f) {
     // a finite factor for the smallest caps too: 0 has to stay 0
-    if (p.softcap > 0.f) cap_mul = fmaxf(fminf(2.f * kLog2e * p.scale / p.softcap, FLT_MAX), -FLT_MAX);
+    if (p.softcap > 0.f) cap_mul = fmaxf(fminf(p.scale / p.softcap, FLT_MAX), -FLT_MAX);
   }
-  __device__ __forceinline__ float operator()(float x) const {
-    // tanh y = 1 - 2 / (1 + e^2y): absolute error of a few 2^-24, saturating at both ends
-    if (cap2 > 0.f) return cap2 - 2.f * cap2 * __frcp_rn(1.f + exp2_approx(x * cap_mul));
-    return x * mul;
+  // tanh y within 6 2^-24 of itself: up to 1.25 the seventh convergent of Lambert's continued fraction
+  // y / (1 + y^2 / (3 + y^2 / (5 + ..))), beyond 1 - 2 / (1 + e^2y), which loses its last bits only for small y.
+  static __device__ __forceinline__ float tanh_of(float y) {
+    const float z = y * y;
+    const float n = fmaf(fmaf(z + 378.f, z, 17325.f), z, 135135.f);
+    const float d = fmaf(fmaf(fmaf(28.f, z, 3150.f), z, 62370.f), z, 135135.f);
+    const float far = 1.f - 2.f * rcp_approx(1.f + exp2_approx(y * (2.f * kLog2e)));
+    return z <= 1.5625f ? y * (n * rcp_approx(d)) : far;
   }
+  __device__ __forceinline__ float operator()(float x) const { return cap2 > 0.f ? cap2 * tanh_of(x * cap_mul) : x * mul; }
 };
 
 // Position of 16-byte unit u of a head's row in the merge buffer: spreads the

@@ -152,6 +152,21 @@ def test_masks_caps_and_biases(opt, Hq, Hkv, D, dtype, bs):
         _check(c, out, lse, **opt)
 
 
+@pytest.mark.parametrize("cap,scale", [(50.0, None), (50.0, 3.0), (8.0, 0.5), (1.0, 0.3)])
+def test_a_cap_keeps_float32(cap, scale):
+    """The cap's tanh is good to a few float32 roundings of itself, small scores and large: the output's error against
+    the oracle, over its norm, stays by the float32 sums' own (D / 2 roundings of a score, at most 2^-24 of it each)."""
+    c = _case([900, 2000, 64], 4, 2, 128, "f32", 16, 63)
+    opt = dict(softcap=cap, **({"scale": scale} if scale else {}))
+    out, lse = _run(c, **opt)
+    ref, rlse = OA.decode_attention(to_np(c["q"]), np.nan_to_num(to_np(c["k"])), np.nan_to_num(to_np(c["v"])),
+                                    c["table"].cpu().numpy(), c["lens"].cpu().numpy(), **opt)
+    # a score's error: 6 roundings for the tanh and at most 62 in the sum of its 128 products, of the largest score's size
+    top = min(cap, float(np.abs(rlse).max()))
+    assert np.linalg.norm(to_np(out) - ref) <= 2 * 68 * 2.0 ** -24 * max(top, 1.0) * np.linalg.norm(ref)
+    assert np.abs(to_np(lse) - rlse).max() <= 68 * 2.0 ** -24 * max(top, 1.0)
+
+
 def test_a_cap_near_zero():
     """Every score is held at the cap: all keys alike, zeros among them."""
     c = _case([300, 17], 4, 2, 64, "bf16", 16, 61)
