@@ -145,17 +145,17 @@ def _refuse(t, name, dtype, shape, dev):
                      + ("" if t.is_contiguous() else ", not contiguous"))
 
 
-def _arg(t, name, dtype, shape, dev):
+def _arg(t, name, dtype, shape, dev, Tensor=torch.Tensor):
     """Address of a contiguous tensor of exactly this type and shape on device dev."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
             and t.get_device() == dev):
         _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _arg_rows(t, name, dtype, shape, dev):
+def _arg_rows(t, name, dtype, shape, dev, Tensor=torch.Tensor):
     """Address and row stride of a tensor [T, H, D] whose rows are contiguous (any stride between them)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
         _refuse(t, name, dtype, shape, dev)
     rows, inner, last = t.stride()
     if (last != 1 and shape[2] > 1 or inner != shape[2] and shape[1] > 1) and t.numel():
@@ -574,15 +574,20 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
         Hq = q.shape[1]
         qp, q_stride = _arg_rows(q, "q", dt, (T, Hq, D), dev)
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=dt, device=q.device)
-        qo, out_stride = _arg_rows(q_out, "q_out", dt, (T, Hq, D), dev)
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            qo, out_stride = q_out.data_ptr(), Hq * D
+        else:
+            qo, out_stride = _arg_rows(q_out, "q_out", dt, (T, Hq, D), dev)
     if cu_new is not None:
         cu = _arg(cu_new, "cu_new", torch.int32, (B + 1,), dev)
     if new_seq_lens is None:
         new_seq_lens = torch.empty_like(seq_lens)
+        new = new_seq_lens.data_ptr()
+    else:
+        new = _arg(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev)
     code = lib().tv_kv_append(qp, q_stride, qo, out_stride, Hq, k, k_stride, v, v_stride, cu, T, kc, vc, num_blocks, bs,
-                              table, width, lens, _arg(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev), cs,
-                              max_pos, B, Hkv, D, TV_F32 if dt is torch.float32 else TV_BF16, _arg_status(status, dev),
+                              table, width, lens, new, cs, max_pos, B, Hkv, D,
+                              TV_F32 if dt is torch.float32 else TV_BF16, _arg_status(status, dev),
                               st if stream is None else stream.cuda_stream)
     if code:
         _check("tv_kv_append", code)
@@ -609,7 +614,10 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     Hq = q.shape[1]
     qp, q_stride = _arg_rows(q, "q", dt, (B, Hq, D), dev)
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=dt, device=q.device)
+        out = torch.empty((B, Hq, D), dtype=dt, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, "out", dt, (B, Hq, D), dev)
     if workspace is None:
         workspace = alloc_workspace(tv_decode_attn_workspace_size(Hq, Hkv, D, dt, num_ctas), q.device)
         flags |= TV_ATTN_WORKSPACE_ZEROED
@@ -617,8 +625,7 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     code = lib().tv_decode_attn(qp, q_stride, kc, vc, num_blocks, bs, table, width, lens, B, Hq, Hkv, D,
                                 TV_F32 if dt is torch.float32 else TV_BF16,
                                 1.0 / math.sqrt(D) if scale is None else scale, softcap, window, n_sink,
-                                None if slopes is None else _arg(slopes, "slopes", torch.float32, (Hq,), dev),
-                                _arg(out, "out", dt, (B, Hq, D), dev),
+                                None if slopes is None else _arg(slopes, "slopes", torch.float32, (Hq,), dev), op,
                                 None if lse is None else _arg(lse, "lse", torch.float32, (B, Hq), dev),
                                 _arg(workspace, "workspace", torch.uint8, (n_ws,), dev), n_ws, num_ctas, flags,
                                 _arg_status(status, dev), st if stream is None else stream.cuda_stream)
@@ -645,20 +652,19 @@ def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entro
     tok = _arg(tokens, "tokens", torch.int32, (B, C), dev)
     row = None if node is None else _arg(node, "node", torch.int32, (B, C), dev)
     k = max(top_k, 0)
-    if logprob is None:
-        logprob = torch.empty((B, C), dtype=f32, device=where)
-    if entropy is None:
-        entropy = torch.empty((B, C), dtype=f32, device=where)
-    if top_ids is None:
-        top_ids = torch.empty((B, C, k), dtype=torch.int32, device=where)
-    if top_logprobs is None:
-        top_logprobs = torch.empty((B, C, k), dtype=f32, device=where)
-    code = lib().tv_token_logprobs(x, tok, row, B, N, C, V, TV_F32 if logits.dtype is f32 else TV_BF16,
-                                   _arg(logprob, "logprob", f32, (B, C), dev),
-                                   _arg(entropy, "entropy", f32, (B, C), dev), top_k,
-                                   _arg(top_ids, "top_ids", torch.int32, (B, C, k), dev),
-                                   _arg(top_logprobs, "top_logprobs", f32, (B, C, k), dev), _arg_status(status, dev),
-                                   st if stream is None else stream.cuda_stream)
+
+    def output(t, name, dtype, shape):  # given, or made here
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=where)
+            return t, t.data_ptr()
+        return t, _arg(t, name, dtype, shape, dev)
+
+    logprob, p_lp = output(logprob, "logprob", f32, (B, C))
+    entropy, p_ent = output(entropy, "entropy", f32, (B, C))
+    top_ids, p_ids = output(top_ids, "top_ids", torch.int32, (B, C, k))
+    top_logprobs, p_top = output(top_logprobs, "top_logprobs", f32, (B, C, k))
+    code = lib().tv_token_logprobs(x, tok, row, B, N, C, V, TV_F32 if logits.dtype is f32 else TV_BF16, p_lp, p_ent, top_k,
+                                   p_ids, p_top, _arg_status(status, dev), st if stream is None else stream.cuda_stream)
     if code:
         _check("tv_token_logprobs", code)
     return logprob, entropy, top_ids, top_logprobs
