@@ -604,7 +604,7 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * k_cache, v_cache, block_table: as in tv_tree_attn_verify, any block_size >= 1;
  *            slots and blocks that hold no visible key are never read.
  * seq_lens   device int32 [B]: L_b, the new token included; values outside
- *            [0, max_blocks * block_size] are clamped into it.
+ *            [0, max_blocks * block_size] (or past 2^31 - 64) are clamped.
  * scale      softmax scale; softcap >= 0, finite.
  * window     0: every key is visible.  Else t is visible when t >= L_b - window
  *            or t < n_sink (the first n_sink keys stay visible; n_sink is

@@ -558,6 +558,10 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
     seq_lens; q [T, Hq, D] is rotated into q_out (may be q).  Rows of k_new, v_new,
     q and q_out may be strided.  cu_new int32 [B + 1]: packed offsets; None: T / B
     tokens each.  Returns (q_out, new_seq_lens int32 [B])."""
+    if stream is not None:  # under it, so that what the call allocates is ordered and reused with its work
+        with torch.cuda.stream(stream):
+            return tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cos_sin=cos_sin, q=q, q_out=q_out,
+                                cu_new=cu_new, new_seq_lens=new_seq_lens, status=status)
     dev, st = _current()
     lens, B = _arg_batch(seq_lens, dev)
     kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
@@ -587,8 +591,7 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
         new = _arg(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev)
     code = lib().tv_kv_append(qp, q_stride, qo, out_stride, Hq, k, k_stride, v, v_stride, cu, T, kc, vc, num_blocks, bs,
                               table, width, lens, new, cs, max_pos, B, Hkv, D,
-                              TV_F32 if dt is torch.float32 else TV_BF16, _arg_status(status, dev),
-                              st if stream is None else stream.cuda_stream)
+                              TV_F32 if dt is torch.float32 else TV_BF16, _arg_status(status, dev), st)
     if code:
         _check("tv_kv_append", code)
     return q_out, new_seq_lens
@@ -607,6 +610,11 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     its K/V already); returns out [B, Hq, D].  q [B, Hq, D] may be strided
     between requests; softcap, window / n_sink and slopes as in the header;
     lse float32 [B, Hq] is filled when given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, scale=scale, softcap=softcap, window=window,
+                                  n_sink=n_sink, slopes=slopes, out=out, lse=lse, workspace=workspace,
+                                  num_ctas=num_ctas, flags=flags, status=status)
     dev, st = _current()
     lens, B = _arg_batch(seq_lens, dev)
     kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
@@ -628,7 +636,7 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
                                 None if slopes is None else _arg(slopes, "slopes", torch.float32, (Hq,), dev), op,
                                 None if lse is None else _arg(lse, "lse", torch.float32, (B, Hq), dev),
                                 _arg(workspace, "workspace", torch.uint8, (n_ws,), dev), n_ws, num_ctas, flags,
-                                _arg_status(status, dev), st if stream is None else stream.cuda_stream)
+                                _arg_status(status, dev), st)
     if code:
         _check("tv_decode_attn", code)
     return out
@@ -640,6 +648,10 @@ def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entro
     logits [B, N, V] (float32 or bf16); returns (logprob, entropy [B, C] float32,
     top_ids int32, top_logprobs float32 [B, C, top_k]).  tokens and node may be
     out and path of tv_tree_accept_*: -1 is no entry."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tv_token_logprobs(logits, tokens, node=node, top_k=top_k, logprob=logprob, entropy=entropy,
+                                     top_ids=top_ids, top_logprobs=top_logprobs, status=status)
     dev, st = _current()
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3 or logits.dtype not in (torch.float32, torch.bfloat16):
         _refuse(logits, "logits", "float32 or bfloat16", (None,) * 3, dev)
@@ -664,7 +676,7 @@ def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entro
     top_ids, p_ids = output(top_ids, "top_ids", torch.int32, (B, C, k))
     top_logprobs, p_top = output(top_logprobs, "top_logprobs", f32, (B, C, k))
     code = lib().tv_token_logprobs(x, tok, row, B, N, C, V, TV_F32 if logits.dtype is f32 else TV_BF16, p_lp, p_ent, top_k,
-                                   p_ids, p_top, _arg_status(status, dev), st if stream is None else stream.cuda_stream)
+                                   p_ids, p_top, _arg_status(status, dev), st)
     if code:
         _check("tv_token_logprobs", code)
     return logprob, entropy, top_ids, top_logprobs

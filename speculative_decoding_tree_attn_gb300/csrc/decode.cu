@@ -135,7 +135,7 @@ struct Span {
 template <int kKeys>
 __device__ __forceinline__ Span span_of(const DecodeParams& p, int b) {
   Span s;
-  const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+  const int64_t cap = min((int64_t)p.max_blocks * p.block_size, (int64_t)INT32_MAX - 63);  // a group's end is an int
   const int64_t L = __ldg(p.seq_lens + b);
   s.L = (int)max((int64_t)0, min(L, cap));
   s.first = p.window > 0 ? max(0, s.L - p.window) : 0;

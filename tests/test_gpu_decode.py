@@ -300,6 +300,21 @@ def test_calls_on_two_streams():
         assert all(torch.equal(w, x) for x in o)
 
 
+def test_a_call_on_another_stream_allocates_there():
+    """Outputs and workspace that the call makes itself belong to the stream it is given: many calls in a row, with the
+    current stream busy reusing freed memory, give what one call gives."""
+    c = _case([3000, 50, 700], 8, 2, 128, "bf16", 16, 133)
+    want, _ = _run(c)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        outs.append(capi.tv_decode_attn(c["q"], c["k"], c["v"], c["table"], c["lens"], stream=s))
+        torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_cache_offsets_past_32_bits():
     Hkv, bs, D = 8, 64, 128
     nblk = (1 << 31) // (Hkv * bs * D) + 8

@@ -184,6 +184,20 @@ def test_outputs_given_and_captured():
             assert torch.equal(got, want)
 
 
+def test_a_call_on_another_stream_allocates_there():
+    x, t = _rows(2, 4, 20000, "f32", 14)
+    want = capi.tv_token_logprobs(x, t, top_k=6)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        outs.append(capi.tv_token_logprobs(x, t, top_k=6, stream=s))
+        torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for got in outs:
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_row_offsets_past_32_bits():
     V = 128000
     N = (1 << 32) // V + 3
