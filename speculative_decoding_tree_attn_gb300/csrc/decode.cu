@@ -164,14 +164,31 @@ struct Scorer {
   }
   // tanh y within 6 2^-24 of itself: up to 1.25 the seventh convergent of Lambert's continued fraction
   // y / (1 + y^2 / (3 + y^2 / (5 + ..))), beyond 1 - 2 / (1 + e^2y), which loses its last bits only for small y.
-  static __device__ __forceinline__ float tanh_of(float y) {
-    const float z = y * y;
-    const float n = fmaf(fmaf(z + 378.f, z, 17325.f), z, 135135.f);
-    const float d = fmaf(fmaf(fmaf(28.f, z, 3150.f), z, 62370.f), z, 135135.f);
-    const float far = 1.f - 2.f * rcp_approx(1.f + exp2_approx(y * (2.f * kLog2e)));
-    return z <= 1.5625f ? y * (n * rcp_approx(d)) : far;
+  // (Both forms for a warp only where one of its scores needs the second.)
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&x)[N]) const {
+    if (cap2 > 0.f) {
+      float z[N], most = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i] *= cap_mul;
+        z[i] = x[i] * x[i];
+        most = fmaxf(most, z[i]);
+      }
+      const bool far = __any_sync(0xffffffffu, most > 1.5625f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float n = fmaf(fmaf(z[i] + 378.f, z[i], 17325.f), z[i], 135135.f);
+        const float d = fmaf(fmaf(fmaf(28.f, z[i], 3150.f), z[i], 62370.f), z[i], 135135.f);
+        float t = x[i] * (n * rcp_approx(d));
+        if (far && !(z[i] <= 1.5625f)) t = 1.f - 2.f * rcp_approx(1.f + exp2_approx(x[i] * (2.f * kLog2e)));
+        x[i] = cap2 * t;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] *= mul;
+    }
   }
-  __device__ __forceinline__ float operator()(float x) const { return cap2 > 0.f ? cap2 * tanh_of(x * cap_mul) : x * mul; }
 };
 
 // Position of 16-byte unit u of a head's row in the merge buffer: spreads the
@@ -252,8 +269,7 @@ struct Bf16Math {
     float mx[NB][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = score(s[n][e]);
+      score(s[n]);
       if (p.slopes) {
         const float d0 = (float)(key + g - (sp.L - 1)), d1 = (float)(key + g + 8 - (sp.L - 1));
 #pragma unroll
@@ -493,8 +509,13 @@ struct F32Math {
       }
 #pragma unroll
       for (int w = kPairs; w < 32; w <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+      s[i] = v[0];
+    }
+    score(s);
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
       const int t = key + kAtOnce * i + lane % kPairs / NH;
-      s[i] = fmaf(slope, (float)(t - (sp.L - 1)), score(v[0]));
+      s[i] = fmaf(slope, (float)(t - (sp.L - 1)), s[i]);
       if (!visible(sp, t)) s[i] = -INFINITY;
       mx = fmaxf(mx, s[i]);
     }
