@@ -151,7 +151,9 @@ __device__ __forceinline__ int group_key(const Span& s, int i) {
 __device__ __forceinline__ bool visible(const Span& s, int t) { return t < s.L && (t >= s.first || t < s.sink); }
 
 // CTA c of P takes tiles [cta_start(c), cta_start(c + 1)) of T.
-__device__ __forceinline__ int cta_start(int c, int T, int P) { return (int)((int64_t)c * T / P); }
+__device__ __forceinline__ int cta_start(int c, int T, int P) {  // c T / P in 32 bits, P <= 4096
+  return c * (T / P) + (int)((uint32_t)(c * (T % P)) / (uint32_t)P);
+}
 __device__ __forceinline__ int cta_of(int t, int T, int P) { return (int)((((int64_t)t + 1) * P - 1) / T); }
 
 // Score of one (head, key) in the log2 domain from its raw product.
