@@ -563,8 +563,9 @@ int tv_kv_commit(void* k_cache, void* v_cache, int64_t num_blocks, int32_t block
  * cos_sin   device float32 [max_pos, 2, head_dim/2] from tv_rope_table (nullable:
  *           keys are stored as given).
  * A request with bad offsets (TV_DEV_BAD_OFFSETS) or L_b < 0
- * (TV_DEV_BAD_POSITION) gets no tokens.  A token whose position is outside the
- * rotary table (TV_DEV_BAD_POSITION) or has no valid block in the table
+ * (TV_DEV_BAD_POSITION) gets no tokens; a row that out-of-order offsets give to
+ * two others goes to one of them.  A token whose position is outside the rotary
+ * table (TV_DEV_BAD_POSITION) or has no valid block in the table
  * (TV_DEV_OUT_OVERFLOW) is not stored and ends the returned length there;
  * a later token whose own block is valid may be stored past that length.
  * q_out rows are written for every token whose position is in the rotary table.
@@ -595,7 +596,8 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * is softmax(s) V over the visible keys t of request b, KV head h / (Hq/Hkv),
  *   s_t = cap(scale * q . k_t) + slopes[h] * (t - (L_b - 1)),
  *   cap(x) = softcap * tanh(x / softcap), or x when softcap is 0.
- * A request without a visible key (L_b = 0) gets a zero row with lse = -inf.
+ * A request without a visible key (L_b = 0) gets a zero row with lse = -inf; a
+ * score of -inf (float32) has no weight.  Visible values are finite.
  * No page defines the call: it is the N = 1 case of "Tree Verification", "Tree
  * Attention", with the token's K/V in the cache.
  *

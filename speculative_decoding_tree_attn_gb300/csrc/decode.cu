@@ -45,6 +45,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 4096;
 constexpr int64_t kCounterBytes = 4 * kMaxCtas;  // arrival counters by a cut team's first CTA: first in the workspace
+constexpr float kNoScore = -FLT_MAX;  // maximum of no scores, and of -inf alone: finite, so that -inf weighs 0 against it
 constexpr int kZeros = -1;    // cache row of a key that is not read
 constexpr int kNoGroup = -2;  // of a warp without a group in the tile
 
@@ -99,10 +100,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// x 2^(m - top), a sum against m as one against top; nothing has been summed against -inf.
-__device__ __forceinline__ float scaled(float x, float m, float top) {
-  return m == -INFINITY ? x : x * exp2_approx(m - top);
-}
+// A sum against m as one against top.
+__device__ __forceinline__ float scaled(float x, float m, float top) { return x * exp2_approx(m - top); }
 
 // Counts an arrival; releases what the CTA wrote before its last barrier and
 // acquires what the earlier arrivals released.
@@ -242,7 +241,7 @@ struct Bf16Math {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hc = 8 * n + 2 * t + e;
-        m[n][e] = -INFINITY;
+        m[n][e] = kNoScore;
         l[n][e] = 0.f;
         slope[n][e] = p.slopes && hc < nh ? __ldg(p.slopes + h0 + hc) * kLog2e : 0.f;
       }
@@ -305,7 +304,7 @@ struct Bf16Math {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float m2 = fmaxf(m[n][e], mx[n][e]);
-          c[e] = m[n][e] == -INFINITY ? 0.f : exp2_approx(m[n][e] - m2);
+          c[e] = exp2_approx(m[n][e] - m2);
           m[n][e] = m2;
           l[n][e] *= c[e];
         }
@@ -476,7 +475,7 @@ struct F32Math {
         q[h][e] = h < nh ? __ldg(reinterpret_cast<const float*>(qrow + h * kRowBytes) + dim(lane, e)) : 0.f;
         o[h][e] = 0.f;
       }
-    m = -INFINITY;
+    m = kNoScore;
     l = 0.f;
     slope = p.slopes && lane % NH < nh ? __ldg(p.slopes + h0 + lane % NH) * kLog2e : 0.f;
   }
@@ -525,7 +524,7 @@ struct F32Math {
     for (int w = NH; w < kPairs; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
     if (__any_sync(0xffffffffu, mx > m + 8.f)) {
       const float m2 = fmaxf(m, mx);
-      const float c = m == -INFINITY ? 0.f : exp2_approx(m - m2);
+      const float c = exp2_approx(m - m2);
       m = m2;
       l *= c;
 #pragma unroll
@@ -885,14 +884,13 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
           const Unit of = unit_of(at.block, who);
           const int hh = Math::kFlush * n + h;
           if (hh >= of.nh) continue;
-          float mm = -INFINITY;
+          float mm = kNoScore;
           for (int w = who; w < kWarps; w += 1 << team_log) mm = fmaxf(mm, merge_ml[w * 16 + 2 * h]);
           float ll = 0.f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int w = who; w < kWarps; w += 1 << team_log) {
-            const float mw = merge_ml[w * 16 + 2 * h];
-            const float c = mw == -INFINITY ? 0.f : exp2_approx(mw - mm);
+            const float c = exp2_approx(merge_ml[w * 16 + 2 * h] - mm);
             const float4 o = *reinterpret_cast<const float4*>(merge + (w * Math::kFlush + h) * D + 4 * merge_unit(h, u));
             ll = fmaf(merge_ml[w * 16 + 2 * h + 1], c, ll);
             add(v, o, c);
@@ -968,7 +966,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
           a[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + from);
           o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (from * (D / 4) + u));
         }
-        float mm = -INFINITY, ll = 0.f;
+        float mm = kNoScore, ll = 0.f;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
           if (i <= mine.others) mm = fmaxf(mm, a[i].x);
@@ -994,7 +992,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     const int wide = rows * 32 <= kThreads ? 32 : 8;
     for (int r0 = 0; r0 < rows; r0 += kThreads / wide) {
       const int r = min(r0 + tid / wide, rows - 1);
-      float mm = -INFINITY, ll = 0.f;
+      float mm = kNoScore, ll = 0.f;
 #pragma unroll 4
       for (int i = tid % wide; i <= mine.others; i += wide) {
         const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part(i, r));

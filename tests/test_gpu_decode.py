@@ -196,6 +196,28 @@ def test_extreme_scores():
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("bf16", 128)])
+@pytest.mark.parametrize("num_ctas", [0, 3])
+def test_scores_of_minus_infinity(dtype, D, num_ctas):
+    """A bias that takes all but a request's last two keys below float32: the last key has all the weight."""
+    lens = [1000, 17, 1, 300, 2, 0]
+    c = _case(lens, 8, 2, D, dtype, 16, 73)
+    slopes = torch.full((8,), 2e38, device="cuda")
+    out, lse = _run(c, slopes=slopes, num_ctas=num_ctas)
+    q, k = (to_np(c[n]).astype(np.float64) for n in "qk")
+    for b, L in enumerate(lens):
+        if L == 0:
+            assert (out[b] == 0).all() and (lse[b] == -np.inf).all()
+            continue
+        blk, slot = int(c["table"][b, (L - 1) // 16]), (L - 1) % 16
+        assert torch.equal(out[b], c["v"][blk, :, slot].repeat_interleave(4, 0))
+        key = k[blk, :, slot].repeat(4, 0)
+        s = (q[b] * key).sum(-1) / np.sqrt(D)
+        # the float32 sum of D products and the roundings through scale and log2 e
+        size = np.linalg.norm(q[b], axis=-1) * np.linalg.norm(key, axis=-1) / np.sqrt(D)
+        assert (np.abs(to_np(lse)[b] - s) <= (D + 16) * 2.0 ** -24 * size).all()
+
+
 def test_strided_queries_and_a_given_output():
     c = _case([40, 9, 200], 8, 2, 128, "bf16", 16, 81)
     want, _ = _run(c)
