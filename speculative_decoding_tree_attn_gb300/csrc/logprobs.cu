@@ -171,11 +171,15 @@ __device__ __forceinline__ bool huge(float m) { return fabsf(m) > 1048576.f && m
 __device__ __forceinline__ float distance(float x, float m) {
   return huge(m) ? (x - m) * kLog2e : __fmaf_rn(x, kLog2e, -reference(m));
 }
+// From m's reference to m2's: both rounded, one exact, or both exact.
+__device__ __forceinline__ float step(float m, float m2) {
+  if (!huge(m)) return huge(m2) ? __fmaf_rn(-m2, kLog2e, reference(m)) : reference(m) - reference(m2);
+  return distance(m, m2);
+}
 struct Sums {
   float m, s, t;
   __device__ __forceinline__ void raise(float m2) {  // to a larger maximum
-    const float d = m == -INFINITY ? kFar
-                                   : fmaxf(huge(m) || huge(m2) ? (m - m2) * kLog2e : reference(m) - reference(m2), kFar);
+    const float d = m == -INFINITY ? kFar : fmaxf(step(m, m2), kFar);
     const float c = exp2_approx(d);
     t = c * fmaf(d, s, t);
     s *= c;

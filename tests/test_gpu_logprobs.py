@@ -150,6 +150,27 @@ def test_rows_at_the_ends_of_the_type(dtype):
     assert lp[3] < -1e38 and ent[3] == 0 and ids[3] == [5, 0] and top[3][0] == 0
 
 
+@pytest.mark.parametrize("at", [2.0 ** 20, -2.0 ** 20])
+@pytest.mark.parametrize("V", [40, 5000, 100000])
+def test_logits_about_a_million(at, V):
+    """Rows whose threads' maxima lie on both sides of 2^20, where the sums' reference changes."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = at + torch.randn(1, 3, V, generator=g, device="cuda") * 3
+    x[0, 1, ::2], x[0, 1, 1::2] = at + 1, at - 1
+    x[0, 2] = at + torch.linspace(-9, 9, V, device="cuda")
+    t = x.argmax(-1).to(torch.int32)
+    lp, ent, ids, top = (to_np(y) for y in capi.tv_token_logprobs(x, t, top_k=5))
+    ref = OL.token_logprobs(to_np(x), t.cpu().numpy(), None, 5)
+    np.testing.assert_array_equal(ids, ref[2])
+    # logits are within 2^5 of each other, so their differences are exact: what is left are rel, as in _check with a
+    # spread of 2^5, and the roundings of results under 2^6
+    rel = (V / 256 + 16) * 2.0 ** -24 + 2.0 ** -21 + 2 * 2.0 ** -24 * 32
+    bound = rel + 4 * 2.0 ** -24 * 64
+    assert np.abs(lp - ref[0]).max() <= bound and np.abs(top - ref[3]).max() <= bound
+    assert np.abs(ent - ref[1]).max() <= rel + (2 * rel + 4 * 2.0 ** -24) * 32
+
+
 def test_what_greedy_acceptance_returns():
     """out and path of the greedy walk go straight in; each emitted token is its row's first alternative."""
     w = W.WORKLOADS["gqa_b8_l512_2048_n26"]
