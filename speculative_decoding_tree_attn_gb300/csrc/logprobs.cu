@@ -507,10 +507,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
 
 template <typename T>
 int launch_logprobs(const LogprobParams& p, int sm_count, cudaStream_t stream) {
-  // A cluster per row, doubled while the grid has under 2 CTAs an SM and a CTA at least 16 KB of the row.
-  const int64_t rows = (int64_t)p.B * p.C;
+  // A row's CTAs.  A cluster costs a microsecond and its CTAs' barriers, so a row under 96 KB has one (1-300 rows of
+  // 32-80 KB: 6-9 us, as two 7-11); a longer one is split while there are SMs without a CTA and 24 KB for each (5 rows
+  // of 300 KB: 10.6 us over 8 CTAs, 16.6 in one), and onto a second CTA an SM only where 128 KB are left (120 rows of
+  // 300 KB: 17.7 against 19.0 us; 120 rows of 200 KB 12.0 against 11.8; 150 rows of 128 KB over 4 CTAs 17 against 10).
+  const int64_t rows = (int64_t)p.B * p.C, bytes = (int64_t)p.V * sizeof(T);
   int ctas = 1;
-  while (ctas < 8 && rows * ctas < 2 * sm_count && (int64_t)p.V * sizeof(T) >= 2 * 16384 * ctas) ctas *= 2;
+  if (bytes >= 98304)
+    for (int c = 2; c <= 8 && rows * c <= 2 * sm_count && bytes / c >= (rows * c <= sm_count ? 24576 : 131072); c *= 2) ctas = c;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * ctas));
   cfg.blockDim = dim3(kThreads);

@@ -133,6 +133,22 @@ def test_special_rows(name, dtype, copies):
         np.testing.assert_allclose(to_np(many[0][0, 0]), ref[0][0, 0], rtol=2e-5, atol=2e-5)
 
 
+@pytest.mark.parametrize("name", sorted(_special()))
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_special_rows_over_a_cluster(name, dtype):
+    """Three times each row behind one another: ties and peaks in several of its CTAs."""
+    x = _special()[name].to(DT[dtype]).cuda().repeat(3).view(1, 1, -1)
+    tok = torch.tensor([[71234]], dtype=torch.int32, device="cuda")
+    _check(x, tok, top_k=32)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 19, 20, 38, 39, 76, 77, 152, 153])
+@pytest.mark.parametrize("dtype,V", [("f32", 70003), ("bf16", 50001), ("bf16", 140007)])
+def test_every_split_of_a_row(rows, dtype, V):
+    x, t = _rows(1, rows, V, dtype, rows)
+    _check(x, t, top_k=8)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_at_the_ends_of_the_type(dtype):
     """A row masked to the lowest value throughout is uniform; one logit near the largest value takes everything."""
