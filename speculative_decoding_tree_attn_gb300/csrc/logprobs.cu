@@ -204,6 +204,12 @@ __device__ __forceinline__ Sums warp_join(Sums a) {  // every lane the same resu
   return a;
 }
 
+// n + (a >= b), b > 0, from b's negative: a - b carries out of 32 bits.
+__device__ __forceinline__ uint32_t count_ge(uint32_t n, uint32_t a, uint32_t minus_b) {
+  asm("{\n\t.reg .u32 t;\n\tadd.cc.u32 t, %1, %2;\n\taddc.u32 %0, %0, 0;\n\t}" : "+r"(n) : "r"(a), "r"(minus_b));
+  return n;
+}
+
 // The candidates of a warp: keys above the bar wait in its buffer in shared memory;
 // when there are 32 they are sorted into a list, one key per lane, descending.
 struct Best {
@@ -262,15 +268,17 @@ struct Best {
     if (lane < kTold) *(volatile uint32_t*)(shared + lane) = mine4;
   }
   __device__ __forceinline__ void heed(const uint32_t* shared, int k, int lane) {  // the k-th of all warps'
-    uint32_t v = *(const volatile uint32_t*)(shared + lane);
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(shared);
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + 4 * lane) : "memory");
+    uint32_t reach = 0;
 #pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-      for (int w = size >> 1; w; w >>= 1) {
-        const uint32_t o = __shfl_xor_sync(0xffffffffu, v, w);
-        v = !(lane & size) == !(lane & w) ? max(v, o) : min(v, o);
-      }
-    raise((uint64_t)__shfl_sync(0xffffffffu, v, k - 1) << 32);  // under every index of that value
+    for (int j = 0; j < 32; j += 4) {
+      const uint4 o = lds128(at + 4 * j);
+      reach = count_ge(count_ge(count_ge(count_ge(reach, o.x, -v), o.y, -v), o.z, -v), o.w, -v);
+    }
+    // under every index of that value
+    raise((uint64_t)__reduce_max_sync(0xffffffffu, reach >= (uint32_t)k ? v : 0u) << 32);
   }
 };
 
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
   __shared__ uint64_t s_wait[kWarps][64], s_best[32];
   extern __shared__ __align__(16) char s_ring[];
   uint64_t* s_pool = reinterpret_cast<uint64_t*>(s_ring);  // [kWarps * 64], once the stream is over
-  __shared__ uint32_t s_bar[32];
+  __shared__ __align__(16) uint32_t s_bar[32];
   __shared__ int s_pool_size;
   if (tok < 0 || tok >= p.V || node < 0 || node >= p.N) {  // no entry: the same for the whole cluster
     if (rank == 0) {
@@ -480,26 +488,38 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
   } else {
     __syncthreads();
   }
-  if (rank == 0 && warp == 0) {
-    if (kTop) best.mine = s_best[lane];
+  if (rank == 0 && (warp == 0 || (kTop && ctas > 1))) {
     Sums all = sums;
-    int wrong = any_bad;
+    int wrong = any_bad, place = lane;
+    uint64_t key = kTop ? s_best[lane] : 0;
     if (ctas > 1) {
+      // a warp per CTA's list: a key's place is its own in its list and the number of larger ones in each of the others
+      if (kTop) key = warp < ctas ? *cluster.map_shared_rank(&s_best[lane], warp) : 0;
       all = warp_join(lane < ctas ? *cluster.map_shared_rank(&s_sums[kWarps], lane) : nothing);
       wrong = __any_sync(0xffffffffu, lane < ctas && *cluster.map_shared_rank(&s_bad, lane));
-      if (kTop)
-        for (int r = 1; r < ctas; ++r) best.join(*cluster.map_shared_rank(&s_best[lane], r), lane);
+      if (kTop) {
+        s_pool[tid] = key;
+        __syncthreads();
+        for (int i = 0; i < ctas; ++i) {
+          const uint64_t* list = s_pool + 32 * i;
+          int above = 0;
+#pragma unroll
+          for (int w = 16; w; w >>= 1) above += list[above + w - 1] > key ? w : 0;
+          above += list[above] > key;
+          place += i == warp ? 0 : above;
+        }
+      }
     }
     // a row without a distribution: a NaN or +inf in it, or nothing above -inf
     const float log2_s = wrong || all.m == -INFINITY ? NAN : log2f(all.s);
     const float ln_s = (log2_s - distance(all.m, all.m)) * kLn2;  // ln sum e^(x - m)
-    if (lane == 0) {
+    if (tid == 0) {
       p.logprob[e] = x_tok - all.m - ln_s;
       if (p.entropy) p.entropy[e] = (log2_s - all.t / all.s) * kLn2;
     }
-    if (kTop && lane < p.top_k) {
-      p.top_ids[e * p.top_k + lane] = (int)~(uint32_t)best.mine;
-      p.top_logprobs[e * p.top_k + lane] = key_value(best.mine) - all.m - ln_s;
+    if (kTop && key && place < p.top_k) {
+      p.top_ids[e * p.top_k + place] = (int)~(uint32_t)key;
+      p.top_logprobs[e * p.top_k + place] = key_value(key) - all.m - ln_s;
     }
   }
   if (ctas > 1) cluster.sync();  // its shared memory is read until here
