@@ -527,14 +527,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
 
 template <typename T>
 int launch_logprobs(const LogprobParams& p, int sm_count, cudaStream_t stream) {
-  // A row's CTAs.  A cluster costs a microsecond and its CTAs' barriers, so a row under 96 KB has one (1-300 rows of
-  // 32-80 KB: 6-9 us, as two 7-11); a longer one is split while there are SMs without a CTA and 24 KB for each (5 rows
-  // of 300 KB: 10.6 us over 8 CTAs, 16.6 in one), and onto a second CTA an SM only where 128 KB are left (120 rows of
-  // 300 KB: 17.7 against 19.0 us; 120 rows of 200 KB 12.0 against 11.8; 150 rows of 128 KB over 4 CTAs 17 against 10).
+  // A row's CTAs.  A cluster costs most of a microsecond, so it has to save more: 4 or 8 CTAs while no SM gets two, of
+  // 6144 logits at least (5 rows of 32,000 bf16 and 5 alternatives: 6.8 us by four, 7.4 in one; of 16,000 both 6.7 and
+  // 6.2), 2 with 48 KB each (76 rows of 100 KB: 9.1 against 10.1, of 64 KB 8.1 and 8.0), and on SMs with a CTA already
+  // 128 KB each (120 rows of 300 KB: 17.0 against 18.0, of 200 KB 11.7 and 10.7; 152 of 100 KB by four 17 and 10).
   const int64_t rows = (int64_t)p.B * p.C, bytes = (int64_t)p.V * sizeof(T);
   int ctas = 1;
-  if (bytes >= 98304)
-    for (int c = 2; c <= 8 && rows * c <= 2 * sm_count && bytes / c >= (rows * c <= sm_count ? 24576 : 131072); c *= 2) ctas = c;
+  for (int c = 2; c <= 8 && rows * c <= 2 * sm_count; c *= 2) {
+    const int64_t least = rows * c > sm_count ? 131072 : c == 2 ? 49152 : 6144 * (int)sizeof(T);
+    if (bytes / c >= least) ctas = c;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * ctas));
   cfg.blockDim = dim3(kThreads);
