@@ -627,8 +627,9 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     else:
         op = _arg(out, "out", dt, (B, Hq, D), dev)
     if workspace is None:
-        workspace = alloc_workspace(tv_decode_attn_workspace_size(Hq, Hkv, D, dt, num_ctas), q.device)
-        flags |= TV_ATTN_WORKSPACE_ZEROED
+        # the call clears the counters, the first 16 KiB of up to 16 MiB
+        workspace = torch.empty(tv_decode_attn_workspace_size(Hq, Hkv, D, dt, num_ctas), dtype=torch.uint8, device=q.device)
+        flags &= ~TV_ATTN_WORKSPACE_ZEROED
     n_ws = workspace.numel()
     code = lib().tv_decode_attn(qp, q_stride, kc, vc, num_blocks, bs, table, width, lens, B, Hq, Hkv, D,
                                 TV_F32 if dt is torch.float32 else TV_BF16,
