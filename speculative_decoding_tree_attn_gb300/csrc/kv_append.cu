@@ -204,10 +204,122 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   }
 }
 
+// Many tokens of few heads (all of them in one or two rounds of a warp): a token's chain of lookups is longer than its
+// copies, so a warp takes 8 tokens, finds their places with a lane each and copies two rounds at a time.  64 prompts of
+// up to 2000 tokens, 4/1 heads of 64, bf16: 30 us, a warp per token 58; one round at a time 28 there, but 46 against
+// 43 of 2/1 heads of 256; four rounds 36.
+constexpr int kTokens = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) kv_append_narrow_kernel(AppendParams p) {
+  constexpr int kChunks = D / 16, kHeads = 32 / kChunks;
+  constexpr int kVec = 8 * (int)sizeof(T) / 16;
+  constexpr int kRow = D * (int)sizeof(T);
+  constexpr int kUnroll = 2;
+  const int lane = threadIdx.x % 32;
+  const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const int64_t token_warps = ((int64_t)p.T + kTokens - 1) / kTokens;
+  if (w >= token_warps) {
+    if (w - token_warps < p.B) count_request(p, (int)(w - token_warps), lane);
+    return;
+  }
+  const int t0 = (int)(w * kTokens);
+  int my_pos = -1;       // of token t0 + lane; -1: none
+  int64_t my_row = -1;   // its row in the cache for KV head 0; -1: not stored
+  if (lane < kTokens && (int64_t)t0 + lane < p.T) {
+    const int t = t0 + lane;
+    int b = 0, j = t;
+    bool here = true;
+    if (p.cu) {
+      for (int hi = p.B; hi - b > 1;) {  // largest b with cu[b] <= t
+        const int mid = b + (hi - b) / 2;
+        if (__ldg(p.cu + mid) <= t) b = mid; else hi = mid;
+      }
+      const int s0 = __ldg(p.cu + b), s1 = __ldg(p.cu + b + 1);
+      j = t - s0;
+      here = s0 >= 0 && s0 <= t && t < s1 && s1 <= p.T;
+    } else {
+      const int per = p.T / p.B;
+      b = t / per;
+      j = t - b * per;
+    }
+    const int L = __ldg(p.seq_lens + b);
+    const int64_t pos = (int64_t)L + j;
+    if (here && L >= 0 && pos < p.max_pos) {
+      my_pos = (int)pos;
+      const int64_t col = pos / p.block_size;
+      const int64_t blk = col < p.max_blocks ? __ldg(p.table + (int64_t)b * p.max_blocks + col) : -1;
+      if (blk >= 0 && blk < p.num_blocks) my_row = blk * p.Hkv * p.block_size + (pos - col * p.block_size);
+    }
+  }
+  const int c = lane % kChunks;
+  const int64_t lo = c * 8 * sizeof(T), hi = lo + kRow / 2;
+  const int Hq = p.q ? p.Hq : 0;
+  const int H = Hq + 2 * p.Hkv;
+  const int two = H > kHeads;  // rounds - 1
+#pragma unroll 1
+  for (int x0 = 0; x0 < kTokens << two; x0 += kUnroll) {
+    Raw<kVec> x1[kUnroll], x2[kUnroll];
+    float co[kUnroll][8], si[kUnroll][8];
+    char* dst[kUnroll];  // null: nothing to store
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = (x0 + u) >> two;
+      const int h = lane / kChunks + ((x0 + u) & two) * kHeads;
+      const int pos = __shfl_sync(0xffffffffu, my_pos, i);
+      const int64_t row = __shfl_sync(0xffffffffu, my_row, i);
+      const int64_t t = (int64_t)t0 + i;
+      dst[u] = nullptr;
+      if (pos < 0 || h >= H) continue;
+      const char* src;
+      if (h < Hq) {
+        src = p.q + t * p.q_stride + (int64_t)h * kRow;
+        dst[u] = p.q_out + t * p.q_out_stride + (int64_t)h * kRow;
+      } else {
+        if (row < 0) continue;
+        const bool is_k = h < Hq + p.Hkv;
+        const int kh = h - Hq - (is_k ? 0 : p.Hkv);
+        src = (is_k ? p.k + t * p.k_stride : p.v + t * p.v_stride) + (int64_t)kh * kRow;
+        dst[u] = (is_k ? p.k_cache : p.v_cache) + (row + (int64_t)kh * p.block_size) * kRow;
+      }
+      x1[u] = *reinterpret_cast<const Raw<kVec>*>(src + lo);
+      x2[u] = *reinterpret_cast<const Raw<kVec>*>(src + hi);
+      if (p.cs && h < Hq + p.Hkv) {
+        const float* cs = p.cs + (int64_t)pos * D + c * 8;
+        Vec8<float>::load(cs, co[u]);
+        Vec8<float>::load(cs + D / 2, si[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (!dst[u]) continue;
+      if (p.cs && lane / kChunks + ((x0 + u) & two) * kHeads < Hq + p.Hkv) {
+        float a[8], d[8], y1[8], y2[8];
+        Vec8<T>::load(reinterpret_cast<const T*>(&x1[u]), a);
+        Vec8<T>::load(reinterpret_cast<const T*>(&x2[u]), d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rope_pair(a[e], d[e], co[u][e], si[u][e], y1[e], y2[e]);
+        Vec8<T>::store(reinterpret_cast<T*>(dst[u] + lo), y1);
+        Vec8<T>::store(reinterpret_cast<T*>(dst[u] + hi), y2);
+      } else {
+        *reinterpret_cast<Raw<kVec>*>(dst[u] + lo) = x1[u];
+        *reinterpret_cast<Raw<kVec>*>(dst[u] + hi) = x2[u];
+      }
+    }
+  }
+}
+
 template <typename T, int D>
 void launch_append(AppendParams p, int sm_count, cudaStream_t stream) {
   constexpr int kHeads = 32 / (D / 16);
-  const int rounds = ((p.q ? p.Hq : 0) + 2 * p.Hkv + kHeads - 1) / kHeads;
+  const int H = (p.q ? p.Hq : 0) + 2 * p.Hkv;
+  const int rounds = (H + kHeads - 1) / kHeads;
+  // 10,000 tokens of one round 6.5 us, 8.1 a warp each, 5000 6.0 and 4.8; of two rounds 10,000 12.4 and 11.1, 19,000 16
+  // and 21.  A token of 4 KB fills its warp's copies: 85 us, 82 a warp each.
+  if (rounds <= 2 && H * D * (int)sizeof(T) < 4096 && p.T >= 48 * rounds * sm_count) {
+    const int64_t warps = ((int64_t)p.T + kTokens - 1) / kTokens + p.B;
+    kv_append_narrow_kernel<T, D><<<(unsigned)tv::ceil_div(warps, kThreads / 32), kThreads, 0, stream>>>(p);
+    return;
+  }
   // few tokens: several warps share one, so that a step's tokens reach every SM
   const int64_t want = (int64_t)sm_count * 8;
   p.slices = (int)std::max<int64_t>(1, std::min<int64_t>(rounds, want / std::max(1, p.T)));

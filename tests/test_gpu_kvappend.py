@@ -132,6 +132,70 @@ def test_in_place_queries_and_offsets_agree():
     assert torch.equal(q, q2) and torch.equal(kc, kc2) and torch.equal(vc, vc2) and torch.equal(lens, lens2)
 
 
+def _one_by_one(c, cs, q_out, status, skip=()):
+    """The same appends a request at a time, from contiguous rows."""
+    kc, vc, lens = c["k_cache"].clone(), c["v_cache"].clone(), c["lens"].clone()
+    at = 0
+    for b, n in enumerate(c["counts"]):
+        rows = slice(at, at + int(n))
+        at += int(n)
+        if n == 0 or b in skip:
+            continue
+        lens[b] = capi.tv_kv_append(c["k"][rows], c["v"][rows], kc, vc, c["table"][b:b + 1].contiguous(),
+                                    c["lens"][b:b + 1].contiguous(), cos_sin=cs, q=None if q_out is None else c["q"][rows],
+                                    q_out=None if q_out is None else q_out[rows], status=status)[1][0]
+    return kc, vc, lens
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,bs", [(4, 1, 64, "bf16", 24), (4, 1, 128, "bf16", 16), (2, 1, 256, "bf16", 64),
+                                               (2, 1, 64, "f32", 16), (8, 2, 64, "f32", 1), (16, 8, 16, "bf16", 16),
+                                               (1, 1, 32, "f32", 7), (1, 1, 256, "f32", 16)])
+@pytest.mark.parametrize("rope", ["q and k", "k", "none"])
+def test_long_prompts_of_few_heads(Hq, Hkv, D, dtype, bs, rope):
+    """Tens of thousands of tokens in one call have the bits of a call per request."""
+    rng = np.random.default_rng(D + Hq)
+    counts = rng.integers(0, 1500, 40)
+    counts[[3, 17]] = 0, 1
+    c = _case(rng.integers(0, 300, 40), counts, Hq, Hkv, D, dtype, bs, 31, pad=5)
+    cs = None if rope == "none" else c["cs"]
+    outs = [torch.full((c["q"].shape[0], Hq, D), 7.0, device="cuda", dtype=DT[dtype]) for _ in range(2)]
+    if rope != "q and k":
+        outs = [None, None]
+    kc, vc = c["k_cache"].clone(), c["v_cache"].clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _, lens = capi.tv_kv_append(c["k"], c["v"], kc, vc, c["table"], c["lens"], cos_sin=cs, cu_new=c["cu"],
+                                q=None if outs[0] is None else c["q"], q_out=outs[0], status=status)
+    kc1, vc1, lens1 = _one_by_one(c, cs, outs[1], status)
+    assert torch.equal(kc, kc1) and torch.equal(vc, vc1) and torch.equal(lens, lens1) and int(status.item()) == 0
+    assert outs[0] is None or torch.equal(*outs)
+    if rope == "q and k":
+        _check(c, kc, vc, lens, outs[0])
+
+
+def test_long_prompts_with_faults_and_without_offsets():
+    c = _case([9, 0, 1000, 30, 3], [4000] * 5, 4, 1, 64, "bf16", 16, 37, max_pos=4600)
+    c["table"][0, 100] = -1
+    c["table"][3, 7] = c["k_cache"].shape[0]
+    c["lens"][4] = -2
+    outs = [torch.full((c["q"].shape[0], 4, 64), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    seen = torch.zeros(3, dtype=torch.int32, device="cuda")
+    want = _one_by_one(c, c["cs"], outs[1], seen[2:])
+    for i, cu in enumerate((c["cu"], None)):
+        kc, vc = c["k_cache"].clone(), c["v_cache"].clone()
+        outs[0].fill_(7.0)
+        _, lens = capi.tv_kv_append(c["k"], c["v"], kc, vc, c["table"], c["lens"], cos_sin=c["cs"], cu_new=cu, q=c["q"],
+                                    q_out=outs[0], status=seen[i:i + 1])
+        assert torch.equal(kc, want[0]) and torch.equal(vc, want[1]) and torch.equal(lens, want[2]) and torch.equal(*outs)
+    assert seen.tolist() == [capi.TV_DEV_BAD_POSITION | capi.TV_DEV_OUT_OVERFLOW] * 3
+    c["cu"][5] += 1  # past the rows: the last request gets nothing, the others as before
+    c["lens"][4] = 3
+    kc, vc = c["k_cache"].clone(), c["v_cache"].clone()
+    _, lens = capi.tv_kv_append(c["k"], c["v"], kc, vc, c["table"], c["lens"], cos_sin=c["cs"], cu_new=c["cu"], q=c["q"],
+                                status=seen[:1])
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1]) and torch.equal(lens[:4], want[2][:4]) and int(lens[4]) == 3
+    assert int(seen[0]) & capi.TV_DEV_BAD_OFFSETS
+
+
 def test_tokens_that_cannot_be_placed_end_the_length():
     """A short table row, a bad entry, a position past the rotary table, a negative length, bad offsets."""
     bs = 16
