@@ -29,7 +29,8 @@
 // - Online softmax per warp in the log2 domain, sums in float32; warps that share
 //   a unit meet in shared memory at its end.  A team cut by a CTA's boundary
 //   leaves (max, sum, output) of each piece in the workspace; the CTA whose piece
-//   arrives last joins them in order, so results do not depend on timing.
+//   arrives last joins them in order, so results do not depend on timing (many
+//   pieces in two steps).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -46,6 +47,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 4096;
 constexpr int64_t kCounterBytes = 4 * kMaxCtas;  // arrival counters by a cut team's first CTA: first in the workspace
 constexpr float kNoScore = -FLT_MAX;  // maximum of no scores, and of -inf alone: finite, so that -inf weighs 0 against it
+constexpr int kOneStep = 24;  // pieces that are joined at once
 constexpr int kZeros = -1;    // cache row of a key that is not read
 constexpr int kNoGroup = -2;  // of a warp without a group in the tile
 
@@ -105,11 +107,27 @@ __device__ __forceinline__ float scaled(float x, float m, float top) { return x 
 
 // Counts an arrival; releases what the CTA wrote before its last barrier and
 // acquires what the earlier arrivals released.
-__device__ __forceinline__ uint32_t arrive(uint32_t* counter) {
+__device__ __forceinline__ uint32_t arrive(uint32_t* counter, uint32_t one) {
   uint32_t before;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(counter), "r"(one) : "memory");
   return before;
 }
+
+// Joins of n pieces: more than 24 in runs, each joined into its first piece by its last arrival, and then the runs, as
+// one CTA reads all of them slowly (one request of 16,000 tokens, 16/1 heads of 128, 152 pieces: 19 us, 37 in one
+// step; 8/1 heads of 256: 27 and 83).  A run counts in the lower half of the counter of its first CTA, which no other
+// team starts in; the runs of a team in the upper half of the team's.
+struct Runs {
+  int size, count;
+  __device__ __forceinline__ explicit Runs(int n) : size(n), count(1) {
+    if (n > kOneStep) {
+      size = 5 << (n > 64) + (n > 512);  // about the root of n
+      count = n / size;
+    }
+  }
+  __device__ __forceinline__ int of(int i) const { return count == 1 ? 0 : min(i / size, count - 1); }
+  __device__ __forceinline__ int pieces(int run, int n) const { return run == count - 1 ? n - run * size : size; }
+};
 
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, float32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -219,22 +237,38 @@ struct Bf16Math {
   static constexpr int kKeys = 16;
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kWarpScratch = 0;
-  uint4 q[NB][D / 32];
+  // Q of 16 heads of 256 does not fit beside their sums in registers: each lane's part is in its warp's place of the
+  // merge buffer, which holds no sums while keys are read.
+  static constexpr bool kQShared = D == 256 && NB == 2;
+  static constexpr int kQ = D / 32;
+  uint4 q[kQShared ? 1 : NB][kQShared ? 1 : kQ];
+  uint32_t q_at;
   float o[NB][D / 16][4];
   float m[NB][2], l[NB][2], slope[NB][2];
 
   // 16-byte piece c of row r within a group's K or V tile.
   static __device__ __forceinline__ int piece(int r, int c) { return r * kRowBytes + ((c ^ (r & 7)) << 4); }
 
-  __device__ __forceinline__ void begin(const DecodeParams& p, const char* qrow, int h0, int nh, int lane) {
+  __device__ __forceinline__ uint4 query(int n, int i) const {
+    if constexpr (kQShared) return lds128(q_at + 512 * (n * kQ + i));
+    else return q[n][i];
+  }
+  __device__ __forceinline__ void begin(const DecodeParams& p, const char* qrow, int h0, int nh, int lane, uint32_t room) {
     const int g = lane >> 2, t = lane & 3;
+    q_at = room + 16 * lane;
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int h = 8 * n + g;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < kQ; ++i) {
         const int c = 2 * t + (i & 1) + 8 * (i >> 1);
-        q[n][i] = h < nh ? __ldg(reinterpret_cast<const uint4*>(qrow + h * kRowBytes + 16 * c)) : make_uint4(0, 0, 0, 0);
+        const uint4 x = h < nh ? __ldg(reinterpret_cast<const uint4*>(qrow + h * kRowBytes + 16 * c)) : make_uint4(0, 0, 0, 0);
+        if constexpr (kQShared)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + 512 * (n * kQ + i)), "r"(x.x), "r"(x.y),
+                       "r"(x.z), "r"(x.w)
+                       : "memory");
+        else
+          q[n][i] = x;
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
@@ -260,8 +294,9 @@ struct Bf16Math {
       const uint4 a = lds128(kt + piece(g, c)), b = lds128(kt + piece(g + 8, c));
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        mma(s[n], a.x, b.x, a.y, b.y, q[n][i].x, q[n][i].y);
-        mma(s[n], a.z, b.z, a.w, b.w, q[n][i].z, q[n][i].w);
+        const uint4 x = query(n, i);
+        mma(s[n], a.x, b.x, a.y, b.y, x.x, x.y);
+        mma(s[n], a.z, b.z, a.w, b.w, x.z, x.w);
       }
     }
     const bool edge = key + kKeys > sp.L || key < sp.first;
@@ -445,6 +480,7 @@ struct F32Math {
   static constexpr int kKeys = 1024 / D;  // 8 KB of K and V
   static constexpr int kRowBytes = 4 * D;
   static constexpr int kWarpScratch = kKeys * NH * 4;  // the group's weights [key][head]
+  static constexpr bool kQShared = false;
   static constexpr int kE = D / 32;
   static constexpr int kVec = kE < 4 ? kE : 4;                      // consecutive dimensions of a lane
   static constexpr int kPairs = kKeys * NH < 32 ? kKeys * NH : 32;  // (key, head) pairs summed at once
@@ -467,7 +503,7 @@ struct F32Math {
     }
   }
 
-  __device__ __forceinline__ void begin(const DecodeParams& p, const char* qrow, int h0, int nh, int lane) {
+  __device__ __forceinline__ void begin(const DecodeParams& p, const char* qrow, int h0, int nh, int lane, uint32_t) {
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -645,14 +681,15 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   extern __shared__ __align__(128) char smem[];
   struct Piece {  // this CTA's piece of a cut team
     int c0;       // the team's first CTA
-    int others;   // its other pieces; -1: no such team
+    int others;   // its other pieces
     int b, block;
   };
   __shared__ Piece s_piece[2];  // of the team that the slice's start cuts, of the one that its end cuts
   __shared__ int s_sum[kWarps][kLogWarps + 2];
-  __shared__ bool s_last[2];
+  __shared__ bool s_last[2], s_top;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kStage;
+  const uint32_t ring_end = (uint32_t)__cvta_generic_to_shared(smem) + S::kRing;
   float* merge = reinterpret_cast<float*>(smem + S::kRing);
   float* merge_ml = reinterpret_cast<float*>(smem + S::kRing + S::kMerge);  // [warp][8][2]
   float* scratch = merge_ml + kWarps * 16 + warp * (Math::kWarpScratch / 4);
@@ -672,7 +709,6 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
   for (int k = 0; k <= kLogWarps; ++k) sums[k] = __reduce_add_sync(0xffffffffu, sums[k]);
-  if (tid == 0) s_piece[0].others = s_piece[1].others = -1;
   if (!few) {
     if (lane == 0) {
 #pragma unroll
@@ -837,13 +873,13 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   // ---- the slice's teams ----
   const Scorer score(p);
   int stage = 0;
-  uint32_t before[2] = {0, 0};  // pieces that arrived before this CTA's (thread 0)
+  bool last[2] = {false, false};  // this CTA's piece was its run's last (thread 0)
   bool cut = false;
   Math math;
   while (t < t1) {
     const Unit unit = unit_of(at.block, member);
     const int tile1 = min(at.tiles, at.tile + (t1 - t));
-    math.begin(p, query(at.b, unit), unit.h0, unit.nh, lane);
+    math.begin(p, query(at.b, unit), unit.h0, unit.nh, lane, ring_end + warp * Math::kFlush * D * 4);
     if (t + tile1 - at.tile < t1) {
       const bool same = at.block + 1 < blocks;
       touch_queries(same ? at.b : at.b + 1, same ? at.block + 1 : 0);
@@ -909,14 +945,18 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
         }
       }
     }
+    if (Math::kQShared && share_log > 0) __syncthreads();  // the buffer is read: the next queries may be written
     if (!whole) {
       cut = true;
       __syncthreads();  // the piece is written; thread 0's release covers it
       if (tid == 0) {
         const int c0 = cta_of(t - at.tile, T, P), c1 = cta_of(t - at.tile + at.tiles - 1, T, P);
         s_piece[at.tile == 0 ? 1 : 0] = {c0, c1 - c0, at.b, at.block};
-        const uint32_t n = arrive(p.arrive + c0);
-        if (at.tile == 0) before[1] = n; else before[0] = n;
+        const int n = c1 - c0 + 1;
+        const Runs runs(n);
+        const int run = runs.of(blockIdx.x - c0);
+        const bool end = (int)(arrive(p.arrive + c0 + run * runs.size, 1) & 0xffff) == runs.pieces(run, n) - 1;
+        if (at.tile == 0) last[1] = end; else last[0] = end;
       }
     }
     t += tile1 - at.tile;
@@ -929,10 +969,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
   // ---- joins of the teams that the slice's ends cut, where this CTA's piece came last ----
   if (tid == 0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      s_last[k] = s_piece[k].others >= 0 && before[k] == (uint32_t)s_piece[k].others;
-      if (s_last[k]) p.arrive[s_piece[k].c0] = 0;  // every piece is here
-    }
+    for (int k = 0; k < 2; ++k) s_last[k] = last[k];
   }
   __syncthreads();
 #pragma unroll 1
@@ -942,7 +979,6 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     // row of piece i in the workspace (at most 4096 CTAs, 2 pieces, 64 KB of outputs: under 2^31 floats)
     const int step = (int)part_row(1, false, 0);
     const int first = (int)part_row(mine.c0, true, 0), other = (int)part_row(mine.c0, false, 0);
-    auto part = [&](int i, int row) { return (i ? other + i * step : first) + row; };
     auto to_row = [&](int r, bool& here) {  // output row of the pieces' row r
       const Unit unit = unit_of(mine.block, r / p.rows);
       here = r % p.rows < unit.nh;
@@ -955,6 +991,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     const int items = rows * (D / 4);
     constexpr int kBatch = kThreads > 256 ? 4 : 8;  // pieces that a thread has on their way at once (registers)
     if (mine.others < kBatch) {  // all of them: one trip to L2
+      if (tid == 0) p.arrive[mine.c0] = 0;
       for (int x = tid; x < items; x += kThreads) {
         const int r = x / (D / 4), u = x % (D / 4);
         float4 o[kBatch];
@@ -962,7 +999,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           if (i > mine.others) continue;
-          const uint32_t from = (uint32_t)part(i, r);
+          const uint32_t from = (uint32_t)(i ? other + i * step : first) + r;
           a[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + from);
           o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (from * (D / 4) + u));
         }
@@ -986,78 +1023,113 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
       }
       continue;
     }
-    // every row's maximum and sum: 8 or 32 lanes a row, a piece each in turn
-    float* row_max = merge;
-    float* row_inv = merge + rows;
-    const int wide = rows * 32 <= kThreads ? 32 : 8;
-    for (int r0 = 0; r0 < rows; r0 += kThreads / wide) {
-      const int r = min(r0 + tid / wide, rows - 1);
-      float mm = kNoScore, ll = 0.f;
-#pragma unroll 4
-      for (int i = tid % wide; i <= mine.others; i += wide) {
-        const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part(i, r));
-        const float m2 = fmaxf(mm, a.x);
-        ll = scaled(ll, mm, m2) + scaled(a.y, a.x, m2);
-        mm = m2;
-      }
-      for (int w = 1; w < wide; w <<= 1) {
-        const float m1 = __shfl_xor_sync(0xffffffffu, mm, w), l1 = __shfl_xor_sync(0xffffffffu, ll, w);
-        const float m2 = fmaxf(mm, m1);
-        ll = scaled(ll, mm, m2) + scaled(l1, m1, m2);
-        mm = m2;
-      }
-      if (tid % wide == 0) {
-        row_max[r] = mm;
-        row_inv[r] = 1.f / ll;
-        bool here;
-        const int64_t row = to_row(r, here);
-        if (p.lse && here) p.lse[row] = (mm + log2f(ll)) * kLn2;
-      }
+    const int n = mine.others + 1;
+    const Runs runs(n);
+    const int run = runs.of(blockIdx.x - mine.c0);
+    if (tid == 0) {  // every piece of the run is here; the others' may be counted in the same word
+      if (run == 0 && runs.count > 1)
+        arrive(p.arrive + mine.c0, -(uint32_t)runs.pieces(0, n));
+      else
+        p.arrive[mine.c0 + run * runs.size] = 0;
     }
-    __syncthreads();
-    // the outputs: some of a thread's and some pieces at a time, as each step is a trip to L2
-    auto sum_up = [&](auto results, auto pieces) {
-      constexpr int kAtOnce = decltype(results)::value, kPieces = decltype(pieces)::value;
-      for (int x0 = tid; x0 < items; x0 += kThreads * kAtOnce) {
-        float4 v[kAtOnce];
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int i0 = 0; i0 <= mine.others; i0 += kPieces)
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) {
-            const int x = x0 + j * kThreads;
-            if (x >= items) continue;
-            const int r = x / (D / 4);
-            const float top = row_max[r];
-            float4 o[kPieces];
-            float w[kPieces];
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-              if (i0 + k > mine.others) continue;
-              const uint32_t at_row = (uint32_t)part(i0 + k, r);
-              w[k] = __ldcg(p.part_ml + at_row * 2);
-              o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at_row * (D / 4) + x % (D / 4)));
-            }
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k)
-              if (i0 + k <= mine.others) add(v[j], o[k], scaled(1.f, w[k], top));
-          }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int x = x0 + j * kThreads, r = x / (D / 4);
-          if (x >= items) continue;
+    int base = run * runs.size, count = runs.pieces(run, n), stride = 1;  // pieces base, base + stride, ..
+    bool final = runs.count == 1;
+    auto part = [&](int i, int row) {
+      const int x = base + i * stride;
+      return (x ? other + x * step : first) + row;
+    };
+    for (;;) {
+      // every row's maximum and sum: 8 or 32 lanes a row, a piece each in turn
+      float* row_max = merge;
+      float* row_inv = merge + rows;
+      const int wide = rows * 32 <= kThreads ? 32 : 8;
+      for (int r0 = 0; r0 < rows; r0 += kThreads / wide) {
+        const int r = min(r0 + tid / wide, rows - 1);
+        float mm = kNoScore, ll = 0.f;
+#pragma unroll 4
+        for (int i = tid % wide; i < count; i += wide) {
+          const float2 a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part(i, r));
+          const float m2 = fmaxf(mm, a.x);
+          ll = scaled(ll, mm, m2) + scaled(a.y, a.x, m2);
+          mm = m2;
+        }
+        for (int w = 1; w < wide; w <<= 1) {
+          const float m1 = __shfl_xor_sync(0xffffffffu, mm, w), l1 = __shfl_xor_sync(0xffffffffu, ll, w);
+          const float m2 = fmaxf(mm, m1);
+          ll = scaled(ll, mm, m2) + scaled(l1, m1, m2);
+          mm = m2;
+        }
+        if (tid % wide == 0) {
+          row_max[r] = mm;
+          row_inv[r] = final ? 1.f / ll : ll;
           bool here;
           const int64_t row = to_row(r, here);
-          if (here) put(row, x % (D / 4), v[j], row_inv[r]);
+          if (p.lse && here && final) p.lse[row] = (mm + log2f(ll)) * kLn2;
         }
       }
-    };
-    if (items <= kThreads)
-      sum_up(std::integral_constant<int, 1>{}, std::integral_constant<int, 2 * kBatch>{});
-    else
-      sum_up(std::integral_constant<int, 4>{}, std::integral_constant<int, kBatch>{});
-    __syncthreads();  // row_max is read; the next join writes it
+      __syncthreads();
+      // the outputs: some of a thread's and some pieces at a time, as each step is a trip to L2
+      auto sum_up = [&](auto results, auto pieces) {
+        constexpr int kAtOnce = decltype(results)::value, kPieces = decltype(pieces)::value;
+        for (int x0 = tid; x0 < items; x0 += kThreads * kAtOnce) {
+          float4 v[kAtOnce];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int i0 = 0; i0 < count; i0 += kPieces)
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              const int x = x0 + j * kThreads;
+              if (x >= items) continue;
+              const int r = x / (D / 4);
+              const float top = row_max[r];
+              float4 o[kPieces];
+              float w[kPieces];
+#pragma unroll
+              for (int k = 0; k < kPieces; ++k) {
+                if (i0 + k >= count) continue;
+                const uint32_t at_row = (uint32_t)part(i0 + k, r);
+                w[k] = __ldcg(p.part_ml + at_row * 2);
+                o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at_row * (D / 4) + x % (D / 4)));
+              }
+#pragma unroll
+              for (int k = 0; k < kPieces; ++k)
+                if (i0 + k < count) add(v[j], o[k], scaled(1.f, w[k], top));
+            }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int x = x0 + j * kThreads, r = x / (D / 4);
+            if (x >= items) continue;
+            if (!final) {
+              __stcg(reinterpret_cast<float4*>(p.part_o) + ((uint32_t)part(0, r) * (D / 4) + x % (D / 4)), v[j]);
+              continue;
+            }
+            bool here;
+            const int64_t row = to_row(r, here);
+            if (here) put(row, x % (D / 4), v[j], row_inv[r]);
+          }
+        }
+      };
+      if (items <= kThreads)
+        sum_up(std::integral_constant<int, 1>{}, std::integral_constant<int, 2 * kBatch>{});
+      else
+        sum_up(std::integral_constant<int, 4>{}, std::integral_constant<int, kBatch>{});
+      __syncthreads();  // row_max is read; the next join writes it
+      if (final) break;
+      for (int r = tid; r < rows; r += kThreads)
+        __stcg(reinterpret_cast<float2*>(p.part_ml) + part(0, r), make_float2(row_max[r], row_inv[r]));
+      __syncthreads();  // the run's piece is written; thread 0's release covers it
+      if (tid == 0) {
+        s_top = arrive(p.arrive + mine.c0, 0x10000) >> 16 == (uint32_t)runs.count - 1;
+        if (s_top) p.arrive[mine.c0] = 0;  // every run is here
+      }
+      __syncthreads();
+      if (!s_top) break;
+      base = 0;
+      count = runs.count;
+      stride = runs.size;
+      final = true;
+    }
   }
 }
 
@@ -1120,13 +1192,23 @@ int call_decode(const Call& c, int Hkv, int G) {
 }
 
 // Query heads of a unit.  bf16: 8, or 16 where a KV head serves more than 8 (two
-// 8-column products share a key's loads), except where their sums would not fit in
-// registers.  float32: as many as the KV head serves, 8 at most.
+// 8-column products share a key's loads), rows of 256 only where the units are a
+// quarter of the CTAs, as their pieces are twice as large (60 requests of 2k-8.7k,
+// 32/2 heads: 147 us, 8 heads a unit 203; 8 of 500-2000: 35 and 21).  float32: as
+// many as the KV head serves, 8 at most.
 template <int D>
 int dispatch_heads(const Call& c, int dtype, int Hkv, int G) {
   if (dtype == TV_BF16) {
-    if constexpr (D <= 128)
-      if (G > 8) return call_decode<Bf16Math<D, 2>, D>(c, Hkv, G);
+    if (G > 8 && (D < 256 || c.room || 4 * (int64_t)c.p->B * Hkv >= c.ctas)) {
+      if (D == 256 && c.room) {  // the room that either needs
+        if (int rc = call_decode<Bf16Math<D, 1>, D>(c, Hkv, G)) return rc;
+        const Room one = *c.room;
+        if (int rc = call_decode<Bf16Math<D, 2>, D>(c, Hkv, G)) return rc;
+        c.room->bytes = std::max(c.room->bytes, one.bytes);
+        return TV_OK;
+      }
+      return call_decode<Bf16Math<D, 2>, D>(c, Hkv, G);
+    }
     return call_decode<Bf16Math<D, 1>, D>(c, Hkv, G);
   }
   if (G == 1) return call_decode<F32Math<D, 1>, D>(c, Hkv, G);

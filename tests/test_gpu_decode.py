@@ -125,6 +125,16 @@ def test_heads_read_together(G, D, dtype, num_ctas):
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("G,Hkv", [(16, 1), (9, 2), (16, 3), (12, 8), (40, 4)])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("num_ctas", [0, 1, 6, 33])
+def test_many_heads_on_one(G, Hkv, D, num_ctas):
+    """KV heads with more than 8 query heads, requests whole, cut and shared by warps, one after another in a CTA."""
+    c = _case([700, 0, 3000, 33, 1, 16, 500], G * Hkv, Hkv, D, "bf16", 16, 2600 + G + D)
+    out, lse = _run(c, num_ctas=num_ctas)
+    _check(c, out, lse)
+
+
 OPTIONS = [
     dict(softcap=5.0), dict(softcap=30.0, scale=0.7), dict(window=1), dict(window=100), dict(window=128, n_sink=4),
     dict(window=33, n_sink=17), dict(window=1000, n_sink=50), dict(window=5, n_sink=100000), dict(n_sink=4),
