@@ -283,6 +283,21 @@ def test_workspace_serves_calls_of_every_size():
         ws.random_(0, 256)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,num_ctas", [(8, 1, 256, "bf16", 0), (16, 1, 128, "bf16", 0), (2, 2, 64, "f32", 0),
+                                                      (4, 1, 128, "f32", 700), (12, 1, 64, "bf16", 25), (1, 1, 64, "f32", 65)])
+def test_requests_in_many_pieces(Hq, Hkv, D, dtype, num_ctas):
+    """Long requests cut into up to hundreds of pieces: the same bits each time, and the counters zero after each call."""
+    c = _case([9000, 5, 20000], Hq, Hkv, D, dtype, 16, 2700 + D)
+    nbytes = capi.tv_decode_attn_workspace_size(Hq, Hkv, D, DT[dtype], num_ctas)
+    ws = capi.alloc_workspace(nbytes)
+    runs = []
+    for _ in range(3):
+        runs.append(_run(c, workspace=ws, num_ctas=num_ctas, flags=capi.TV_ATTN_WORKSPACE_ZEROED))
+        assert int(ws[:16384].max()) == 0
+    _check(c, *runs[0])
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+
+
 def test_captured_calls_follow_their_inputs():
     """Graph replays with lengths and tables changed in place; two graphs share a workspace in turn."""
     lens = [900, 33, 0, 2000]
