@@ -650,8 +650,10 @@ int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cache, const v
  * tokens    device int32 [B, C]: the token of each entry, -1 = no entry.
  * node      device int32 [B, C] (nullable: entry c reads row c, C <= N): the row
  *           each entry reads, -1 = no entry.  Rows may repeat.
- * logprob   device float32 [B, C] out: x[token] - log sum exp(x); 0 for no entry.
- * entropy   device float32 [B, C] out (nullable): -sum p ln p; 0 for no entry.
+ * logprob   device float32 [B, C] out: x[token] - log sum exp(x), never above 0; 0 for
+ *           no entry.
+ * entropy   device float32 [B, C] out (nullable): -sum p ln p, never below 0; 0 for no
+ *           entry.
  * top_k     0 .. TV_MAX_TOP_K, at most V: alternatives per entry.
  * top_ids   device int32 [B, C, top_k] out: the largest logits' indices, largest
  *           first, equal ones by ascending index; -1 for no entry.

@@ -513,13 +513,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
     // a row without a distribution: a NaN or +inf in it, or nothing above -inf
     const float log2_s = wrong || all.m == -INFINITY ? NAN : log2f(all.s);
     const float ln_s = (log2_s - distance(all.m, all.m)) * kLn2;  // ln sum e^(x - m)
+    // A row that one token has to itself: the reference's rounding is in S and taken away again, which leaves a few
+    // 2^-24 of either sign.  ln p <= 0 <= H; a NaN stays one.
+    auto ln_p = [&](float x) {
+      const float y = x - all.m - ln_s;
+      return y > 0.f ? 0.f : y;
+    };
     if (tid == 0) {
-      p.logprob[e] = x_tok - all.m - ln_s;
-      if (p.entropy) p.entropy[e] = (log2_s - all.t / all.s) * kLn2;
+      p.logprob[e] = ln_p(x_tok);
+      const float h = (log2_s - all.t / all.s) * kLn2;
+      if (p.entropy) p.entropy[e] = h < 0.f ? 0.f : h;
     }
     if (kTop && key && place < p.top_k) {
       p.top_ids[e * p.top_k + place] = (int)~(uint32_t)key;
-      p.top_logprobs[e * p.top_k + place] = key_value(key) - all.m - ln_s;
+      p.top_logprobs[e * p.top_k + place] = ln_p(key_value(key));
     }
   }
   if (ctas > 1) cluster.sync();  // its shared memory is read until here

@@ -331,3 +331,29 @@ def test_a_plain_step_then_a_tree_step(captured):
     out = capi.tv_tree_attn_verify(q_rot, kc, vc, table, lens[3], kt_rot, vt, mask)
     ref, _ = OA.tree_attention(to_np(q), okc, ovc, table_np, olen, to_np(kt), to_np(vt), parent)
     assert np.abs(to_np(out) - ref).max() <= 2e-2
+
+
+def _signs(got):
+    lp, ent, ids, top = got
+    assert not (lp > 0).any() and not (ent < 0).any() and not (top > 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(2000, 64), (500, 9000), (4, 100000)])
+def test_confident_rows_keep_their_signs(dtype, rows, V):
+    """A log probability is never above 0 and an entropy never below: rows that one token has to itself, nearly to
+    itself, and shares, at many sizes of its logit; a row over one CTA and over several."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    t = torch.randint(0, V, (1, rows), generator=g, device="cuda", dtype=torch.int32)
+    best = torch.rand(1, rows, 1, generator=g, device="cuda") * 80 - 40
+    for rest in (-float("inf"), -60.0, -30.0, -17.0, -12.0):
+        x = (best + rest).expand(1, rows, V).clone()
+        x.scatter_(2, t[..., None].long(), best)
+        x = x.to(DT[dtype])
+        got = _check(x, t, top_k=3)
+        _signs(got)
+        if rest == -float("inf"):  # the rounding of a sum of one term, taken away again
+            assert (got[0].abs() <= 2.0 ** -20).all() and (got[1] <= 2.0 ** -20).all()
+    x = (torch.randn(1, rows, V, generator=g, device="cuda") * 6 + best).to(DT[dtype])
+    _signs(_check(x, t, top_k=3))
