@@ -596,8 +596,9 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * is softmax(s) V over the visible keys t of request b, KV head h / (Hq/Hkv),
  *   s_t = cap(scale * q . k_t) + slopes[h] * (t - (L_b - 1)),
  *   cap(x) = softcap * tanh(x / softcap), or x when softcap is 0.
- * A request without a visible key (L_b = 0) gets a zero row with lse = -inf; a
- * score of -inf (float32) has no weight.  Visible values are finite.
+ * A score of -inf (a product past float32, say) has no weight.  A row without
+ * any weight -- no visible key (L_b = 0), or every score -inf -- is zero with
+ * lse = -inf.  Visible values are finite.
  * No page defines the call: it is the N = 1 case of "Tree Verification", "Tree
  * Attention", with the token's K/V in the cache.
  *

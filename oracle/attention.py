@@ -190,7 +190,8 @@ def decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, sof
     Row (b, h) sees keys t < L_b, with a ``window`` only t >= L_b - window or
     t < n_sink; its scores are scale * q . k_t, capped to
     softcap * tanh(x / softcap) when softcap > 0, plus
-    slopes[h] * (t - (L_b - 1)).  No visible key: a zero row, lse -inf.
+    slopes[h] * (t - (L_b - 1)).  No visible key, or only scores of
+    -inf: a zero row, lse -inf.
     """
     q = np.asarray(q, dtype=np.float64)
     Bn, Hq, D = q.shape
@@ -214,6 +215,8 @@ def decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, sof
             if slopes is not None:
                 s = s + float(slopes[h]) * (t - (L - 1))
             m = s.max()
+            if m == -np.inf:
+                continue
             w = np.exp(s - m)
             out[b, h] = w @ values[:, h // (Hq // Hkv)] / w.sum()
             lse[b, h] = m + np.log(w.sum())

@@ -102,6 +102,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// What a row is multiplied with: 1 over its weights' sum.  Without any weight (no visible key, or only scores of -inf)
+// the row is zero, and its m + log2 of the sum is -inf by itself; a NaN stays one.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+
 // A sum against m as one against top.
 __device__ __forceinline__ float scaled(float x, float m, float top) { return x * exp2_approx(m - top); }
 
@@ -399,7 +403,7 @@ struct Bf16Math {
         for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
   }
   // The finished rows of a unit that this warp had alone.
-  __device__ __forceinline__ void write_out(Out* out, float* lse, int nh, bool any, int lane) {
+  __device__ __forceinline__ void write_out(Out* out, float* lse, int nh, int lane) {
     const int g = lane >> 2, t = lane & 3;
     sum_up();
 #pragma unroll
@@ -408,8 +412,8 @@ struct Bf16Math {
       for (int e = 0; e < 2; ++e) {
         const int h = 8 * n + 2 * t + e;
         if (h >= nh) continue;
-        const float r = any ? 1.f / l[n][e] : 0.f;
-        if (lse && g == 0) lse[h] = any ? (m[n][e] + log2f(l[n][e])) * kLn2 : -INFINITY;
+        const float r = inverse(l[n][e]);
+        if (lse && g == 0) lse[h] = (m[n][e] + log2f(l[n][e])) * kLn2;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           const float4 a = four(n, e, i, 0), b = four(n, e, i, 1);
@@ -606,10 +610,10 @@ struct F32Math {
       else
         __stcg(reinterpret_cast<float2*>(to + dim(lane, e)), make_float2(x[e] * r, x[e + 1] * r));
   }
-  __device__ __forceinline__ void write_out(Out* out, float* lse, int nh, bool any, int lane) {
+  __device__ __forceinline__ void write_out(Out* out, float* lse, int nh, int lane) {
     const float v = sum_up();
-    if (lse && lane < nh) lse[lane] = any ? (m + log2f(v)) * kLn2 : -INFINITY;
-    const float r = any ? 1.f / v : 0.f;
+    if (lse && lane < nh) lse[lane] = (m + log2f(v)) * kLn2;
+    const float r = inverse(v);
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       const float rh = __shfl_sync(0xffffffffu, r, h);
@@ -898,12 +902,11 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
     }
 
     const bool whole = at.tile == 0 && tile1 == at.tiles;
-    const bool any = at.span.groups > 0;
     if (share_log == 0) {
       if (whole) {
         const int64_t out_row = (int64_t)at.b * p.Hq + unit.h0;
         math.write_out(reinterpret_cast<typename Math::Out*>(p.out) + out_row * D, p.lse ? p.lse + out_row : nullptr,
-                       unit.nh, any, lane);
+                       unit.nh, lane);
       } else {
         const int64_t to = part_row(blockIdx.x, at.tile == 0, member);
         math.write_piece(p.part_o + to * D, p.part_ml + to * 2, unit.nh, lane);
@@ -932,11 +935,11 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
             add(v, o, c);
           }
           if (whole) {
-            const float r = any ? 1.f / ll : 0.f;
+            const float r = inverse(ll);
             const int64_t out_row = (int64_t)at.b * p.Hq + of.h0 + hh;
             store4(reinterpret_cast<typename Math::Out*>(p.out) + out_row * D + 4 * u,
                    make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
-            if (p.lse && u == 0) p.lse[out_row] = any ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            if (p.lse && u == 0) p.lse[out_row] = (mm + log2f(ll)) * kLn2;
           } else {
             const int64_t to = part_row(blockIdx.x, at.tile == 0, who) + hh;
             __stcg(reinterpret_cast<float4*>(p.part_o + to * D + 4 * u), v);
@@ -1018,7 +1021,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
         bool here;
         const int64_t row = to_row(r, here);
         if (!here) continue;
-        put(row, u, v, 1.f / ll);
+        put(row, u, v, inverse(ll));
         if (p.lse && u == 0) p.lse[row] = (mm + log2f(ll)) * kLn2;
       }
       continue;
@@ -1061,7 +1064,7 @@ __global__ void __launch_bounds__(Shape<Math, D>::kWarps * 32, 1) decode_kernel(
         }
         if (tid % wide == 0) {
           row_max[r] = mm;
-          row_inv[r] = final ? 1.f / ll : ll;
+          row_inv[r] = final ? inverse(ll) : ll;
           bool here;
           const int64_t row = to_row(r, here);
           if (p.lse && here && final) p.lse[row] = (mm + log2f(ll)) * kLn2;

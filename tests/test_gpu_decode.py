@@ -426,3 +426,26 @@ def test_binding_checks_every_argument():
         capi.tv_decode_attn(**{**good, "k_cache": c["k"].cpu()})
     with pytest.raises(capi.TVError, match="workspace"):
         capi.tv_decode_attn(**good, workspace=torch.zeros(100, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(8, 2, 128, "bf16"), (16, 1, 256, "bf16"), (8, 8, 64, "bf16"), (4, 1, 64, "f32"),
+                                            (8, 1, 256, "f32"), (2, 2, 128, "f32")])
+@pytest.mark.parametrize("num_ctas", [0, 1, 3, 40])
+def test_no_score_above_minus_infinity(Hq, Hkv, D, dtype, num_ctas):
+    """Requests whose scores are all -inf (a product past float32, keys of -inf) have no weight anywhere: a zero row with
+    lse -inf, as without a visible key; requests whole, cut in few and many pieces, and shared by warps.  The others are
+    as they were."""
+    lens = [700, 5000, 1, 20, 16, 3, 300]
+    c = _case(lens, Hq, Hkv, D, dtype, 16, 77)
+    want, wlse = _run(c, num_ctas=num_ctas)
+    gone = [1, 3, 5, 6]
+    c["q"][gone] = 1e20
+    table = c["table"].cpu().numpy()
+    for b in gone:
+        for i in range((lens[b] + 15) // 16):
+            n = min(16, lens[b] - 16 * i)
+            c["k"][table[b, i], :, :n] = -float("inf") if b == 6 else -1e20
+    out, lse = _run(c, num_ctas=num_ctas)
+    assert (out[gone] == 0).all() and (lse[gone] == -np.inf).all()
+    rest = [0, 2, 4]
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], wlse[rest])

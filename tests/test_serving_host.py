@@ -200,3 +200,12 @@ def test_binding_names_what_it_refuses():
                  lambda: capi.tv_token_logprobs(None, lens[:, None])):
         with pytest.raises(ValueError, match="must be a CUDA tensor"):
             call()
+
+
+def test_decode_oracle_without_any_weight():
+    """Keys of -inf under positive queries: every score is -inf, a zero row as for an empty request."""
+    k, v = np.full((2, 1, 16, 8), -np.inf), np.ones((2, 1, 16, 8))
+    k[1] = 1.0
+    out, lse = OA.decode_attention(np.ones((2, 2, 8)), k, v, np.array([[0], [1]]), [5, 5])
+    assert (out[0] == 0).all() and (lse[0] == -np.inf).all()
+    np.testing.assert_allclose(out[1], 1.0, atol=1e-15)
