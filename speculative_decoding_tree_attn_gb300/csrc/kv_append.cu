@@ -102,7 +102,7 @@ __device__ void count_request(const AppendParams& p, int b, int lane) {
       const unsigned m = __ballot_sync(0xffffffffu, miss);
       if (m) {
         n = (int)max((int64_t)0, (c0 + __ffs(m) - 1) * p.block_size - L);
-        bad = TV_DEV_OUT_OVERFLOW;  // reached before any position past the table
+        bad |= TV_DEV_OUT_OVERFLOW;  // beside positions past the table: their queries are not written
         break;
       }
     }

@@ -331,3 +331,19 @@ def test_binding_checks_every_argument():
         capi.tv_kv_append(**{**good, "cos_sin": None})
     with pytest.raises(capi.TVError, match="alias"):
         capi.tv_kv_append(**good, new_seq_lens=c["lens"])
+
+
+def test_a_bad_block_before_the_end_of_the_table():
+    """One request with a missing block and, behind it, positions past the rotary table: both are reported, and the
+    queries past the table are left as they were."""
+    c = _case([10], [60], 2, 1, 64, "f32", 16, 41, max_pos=50)
+    c["table"][0, 1] = -1
+    q_out = torch.full((60, 2, 64), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kc, vc, lens, q = _append(c, status=status, q_out=q_out)
+    assert int(status.item()) == capi.TV_DEV_OUT_OVERFLOW | capi.TV_DEV_BAD_POSITION
+    assert lens.tolist() == [16]
+    assert (q[40:] == 7.0).all() and (q[:40] != 7.0).any(-1).all()
+    okc, ovc, olens, _ = _oracle(c, max_pos=50)
+    np.testing.assert_array_equal(to_np(vc), ovc)
+    np.testing.assert_array_equal(olens, [16])
