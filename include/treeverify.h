@@ -54,8 +54,8 @@ extern "C" {
 #define TV_DEV_TIMEOUT 16       /* a pipeline wait in a kernel exceeded 2 s     */
 #define TV_DEV_BAD_BLOCK 32     /* a block-table entry a prefix position uses is outside
                                    [0, num_blocks): those keys and values read as zeros */
-#define TV_DEV_BAD_OFFSETS 64   /* token offsets that decrease or leave [0, T]: that
-                                   request gets no tokens                        */
+#define TV_DEV_BAD_OFFSETS 64   /* token offsets that decrease or leave [0, T]: a
+                                   request that they touch gets no tokens        */
 
 /* ---- element types ------------------------------------------------------ */
 #define TV_F32 0
@@ -563,8 +563,10 @@ int tv_kv_commit(void* k_cache, void* v_cache, int64_t num_blocks, int32_t block
  * cos_sin   device float32 [max_pos, 2, head_dim/2] from tv_rope_table (nullable:
  *           keys are stored as given).
  * A request with bad offsets (TV_DEV_BAD_OFFSETS) or L_b < 0
- * (TV_DEV_BAD_POSITION) gets no tokens; a row that out-of-order offsets give to
- * two others goes to one of them.  A token whose position is outside the rotary
+ * (TV_DEV_BAD_POSITION) gets no tokens.  Offsets out of order may also lead rows
+ * of another request elsewhere or nowhere: that request's length stays L_b
+ * (TV_DEV_BAD_OFFSETS), whatever of it is stored past that length, so that a
+ * returned length only counts tokens that are in the cache.  A token whose position is outside the rotary
  * table (TV_DEV_BAD_POSITION) or has no valid block in the table
  * (TV_DEV_OUT_OVERFLOW) is not stored and ends the returned length there;
  * a later token whose own block is valid may be stored past that length.

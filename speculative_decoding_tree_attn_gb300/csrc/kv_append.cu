@@ -45,8 +45,36 @@ struct AppendParams {
   int32_t* status;
 };
 
-// Request and index within it of packed row t (every lane the same); false
-// for a row of no request.  Largest b with cu[b] <= t, 32 probes a round.
+// Largest b with cu[b] <= t.  A search takes the same turns for all rows between two that it leads to b (a turn asks
+// whether cu[i] <= t), so a request's first and last row tell whether it finds all of them, in order or not.
+// Every lane the same row, 32 probes a round:
+struct WarpSearch {
+  static __device__ __forceinline__ int request(const AppendParams& p, int t, int lane) {
+    int lo = 0, hi = p.B;  // the answer is in [lo, hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int64_t i = (int64_t)lo + (int64_t)step * lane;
+      const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldg(p.cu + i) <= t);
+      lo += step * (le ? 31 - __clz(le) : 0);
+      hi = min(hi, lo + step);
+    }
+    return lo;
+  }
+};
+// a row a lane:
+struct LaneSearch {
+  static __device__ __forceinline__ int request(const AppendParams& p, int t, int) {
+    int lo = 0;
+    for (int hi = p.B; hi - lo > 1;) {
+      const int mid = lo + (hi - lo) / 2;
+      if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+};
+
+// Request and index within it of packed row t; false for a row of no request.
+template <class Search>
 __device__ __forceinline__ bool find_request(const AppendParams& p, int t, int lane, int& b, int& j) {
   if (!p.cu) {
     const int per = p.T / p.B;
@@ -54,21 +82,14 @@ __device__ __forceinline__ bool find_request(const AppendParams& p, int t, int l
     j = t - b * per;
     return true;
   }
-  int lo = 0, hi = p.B;  // the answer is in [lo, hi)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int64_t i = (int64_t)lo + (int64_t)step * lane;
-    const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldg(p.cu + i) <= t);
-    lo += step * (le ? 31 - __clz(le) : 0);
-    hi = min(hi, lo + step);
-  }
-  b = lo;
+  b = Search::request(p, t, lane);
   const int s0 = __ldg(p.cu + b), s1 = __ldg(p.cu + b + 1);
   j = t - s0;
   return s0 >= 0 && s0 <= t && t < s1 && s1 <= p.T;
 }
 
-// New length of request b: the tokens before the first that cannot be placed.
+// New length of request b: the tokens before the first that cannot be placed.  Search is the one that the tokens' warps use.
+template <class Search>
 __device__ void count_request(const AppendParams& p, int b, int lane) {
   const int L = p.seq_lens[b];
   int n, bad = 0;
@@ -78,6 +99,14 @@ __device__ void count_request(const AppendParams& p, int b, int lane) {
     if (s0 < 0 || s1 < s0 || s1 > p.T) {
       n = 0;
       bad = TV_DEV_BAD_OFFSETS;
+    }
+    // offsets of others, out of order, may lead some of its rows elsewhere or nowhere
+    if (n > 0) {
+      const int first = Search::request(p, s0, lane), last = Search::request(p, s1 - 1, lane);
+      if (first != b || last != b) {
+        n = 0;
+        bad = TV_DEV_BAD_OFFSETS;
+      }
     }
   } else {
     n = p.T / p.B;
@@ -135,13 +164,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int64_t token_warps = (int64_t)p.T * p.slices;
   if (w >= token_warps) {
-    if (w - token_warps < p.B) count_request(p, (int)(w - token_warps), lane);
+    if (w - token_warps < p.B) count_request<WarpSearch>(p, (int)(w - token_warps), lane);
     return;
   }
   const int t = (int)(w / p.slices);
   const int s = (int)(w - (int64_t)t * p.slices);
   int b, j;
-  if (!find_request(p, t, lane, b, j)) return;
+  if (!find_request<WarpSearch>(p, t, lane, b, j)) return;
   const int L = __ldg(p.seq_lens + b);
   const int64_t pos = (int64_t)L + j;
   if (L < 0 || pos >= p.max_pos) return;
@@ -219,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_narrow_kernel(AppendParams
   const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int64_t token_warps = ((int64_t)p.T + kTokens - 1) / kTokens;
   if (w >= token_warps) {
-    if (w - token_warps < p.B) count_request(p, (int)(w - token_warps), lane);
+    if (w - token_warps < p.B) count_request<LaneSearch>(p, (int)(w - token_warps), lane);
     return;
   }
   const int t0 = (int)(w * kTokens);
@@ -227,21 +256,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_narrow_kernel(AppendParams
   int64_t my_row = -1;   // its row in the cache for KV head 0; -1: not stored
   if (lane < kTokens && (int64_t)t0 + lane < p.T) {
     const int t = t0 + lane;
-    int b = 0, j = t;
-    bool here = true;
-    if (p.cu) {
-      for (int hi = p.B; hi - b > 1;) {  // largest b with cu[b] <= t
-        const int mid = b + (hi - b) / 2;
-        if (__ldg(p.cu + mid) <= t) b = mid; else hi = mid;
-      }
-      const int s0 = __ldg(p.cu + b), s1 = __ldg(p.cu + b + 1);
-      j = t - s0;
-      here = s0 >= 0 && s0 <= t && t < s1 && s1 <= p.T;
-    } else {
-      const int per = p.T / p.B;
-      b = t / per;
-      j = t - b * per;
-    }
+    int b, j;
+    const bool here = find_request<LaneSearch>(p, t, lane, b, j);
     const int L = __ldg(p.seq_lens + b);
     const int64_t pos = (int64_t)L + j;
     if (here && L >= 0 && pos < p.max_pos) {

@@ -347,3 +347,50 @@ def test_a_bad_block_before_the_end_of_the_table():
     okc, ovc, olens, _ = _oracle(c, max_pos=50)
     np.testing.assert_array_equal(to_np(vc), ovc)
     np.testing.assert_array_equal(olens, [16])
+
+
+def _random_offsets(rng, B, T):
+    """Offsets in order, then some of them moved anywhere, a little past [0, T] too."""
+    cu = np.sort(rng.integers(0, T + 1, B + 1))
+    cu[0], cu[-1] = 0, T
+    for i in rng.choice(B + 1, size=int(rng.integers(1, 4)), replace=False):
+        cu[i] = rng.integers(-2, T + 3)
+    return cu.astype(np.int32)
+
+
+@pytest.mark.parametrize("B,T", [(3, 10), (5, 45), (33, 200), (100, 900), (1500, 3000), (40, 9000)])
+def test_offsets_out_of_order_count_no_token_that_is_not_stored(B, T):
+    """Whatever the offsets, a length that is returned covers rows of its request that are in the cache; a batch in
+    order has all of them.  9000 tokens of one head go eight to a warp."""
+    rng = np.random.default_rng(B)
+    bs, Hkv, D = 16, 1, 64
+    lens0 = rng.integers(0, 40, B).astype(np.int32)
+    width = (40 + T) // bs + 2 if B <= 100 else 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    k = torch.randn(T, Hkv, D, generator=g, device="cuda")
+    v = torch.randn(T, Hkv, D, generator=g, device="cuda")
+    table = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width)
+    lens = torch.from_numpy(lens0).cuda()
+    cases = [np.array([0, 10, 5, 8], dtype=np.int32)] if B == 3 else []
+    cases += [_random_offsets(rng, B, T) for _ in range(12)]
+    for cu in cases:
+        kc = torch.full((B * width, Hkv, bs, D), 7.0, device="cuda")
+        vc = kc.clone()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        _, new = capi.tv_kv_append(k, v, kc, vc, table, lens, cu_new=torch.from_numpy(cu).cuda(), status=status)
+        n = (new - lens).cpu().numpy()
+        ordered = (np.diff(cu) >= 0).all() and cu[0] >= 0 and cu[-1] <= T
+        assert (n >= 0).all()
+        if ordered:
+            assert int(status) & capi.TV_DEV_BAD_OFFSETS == 0
+        else:
+            assert int(status) & capi.TV_DEV_BAD_OFFSETS
+        for b in range(B):
+            s0, s1 = int(cu[b]), int(cu[b + 1])
+            room = max(0, min(s1 - s0, width * bs - int(lens0[b])))
+            assert n[b] in ((room,) if ordered else (0, room))
+            if n[b]:
+                at = torch.arange(int(lens0[b]), int(lens0[b]) + int(n[b]), device="cuda")
+                blk = table[b, at // bs].long()
+                assert torch.equal(kc[blk, :, at % bs], k[s0:s0 + n[b]]) and torch.equal(vc[blk, :, at % bs], v[s0:s0 + n[b]])
