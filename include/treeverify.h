@@ -557,7 +557,7 @@ int tv_kv_commit(void* k_cache, void* v_cache, int64_t num_blocks, int32_t block
  * k_cache, v_cache, block_table: as in tv_kv_commit; the caller has placed
  *           blocks for the new positions.  Distinct tokens go to distinct slots.
  * seq_lens  device int32 [B]: L_b before the call (read).
- * new_seq_lens device int32 [B] out (nullable, must not alias seq_lens): L_b +
+ * new_seq_lens device int32 [B] out (nullable, must not overlap seq_lens): L_b +
  *           the request's tokens, or L_b + j when token j is the first that
  *           cannot be placed (below).
  * cos_sin   device float32 [max_pos, 2, head_dim/2] from tv_rope_table (nullable:

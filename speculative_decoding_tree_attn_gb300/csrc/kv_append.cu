@@ -379,8 +379,10 @@ extern "C" int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_
     return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: null pointer");
   if (q && (!cos_sin || !q_out))
     return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: q needs cos_sin and q_out");
-  if (new_seq_lens && new_seq_lens == seq_lens)
-    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: new_seq_lens must not alias seq_lens");
+  // shifted views of one buffer too: lengths are written while other requests' warps read theirs
+  const uintptr_t len0 = reinterpret_cast<uintptr_t>(seq_lens), len1 = reinterpret_cast<uintptr_t>(new_seq_lens);
+  if (new_seq_lens && (len0 > len1 ? len0 - len1 : len1 - len0) < sizeof(int32_t) * (size_t)B)
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_kv_append: new_seq_lens must not alias seq_lens or overlap it");
   const int64_t e = dtype == TV_F32 ? 4 : 2;
   const int64_t kv_row = (int64_t)Hkv * head_dim, q_row = (int64_t)Hq * head_dim;
   const bool many = T > 1;  // one token's strides do not matter

@@ -50,6 +50,13 @@ def test_append_refuses_on_the_host(change, code, text):
     assert text in capi.lib().tv_last_error()
 
 
+@pytest.mark.parametrize("at", [4096 - 8, 4096 - 4, 4096 + 4, 4096 + 8])
+def test_append_refuses_lengths_that_overlap(at):
+    """Shifted views of one buffer: a request's new length would land where another's old one is read."""
+    assert _call("tv_kv_append", APPEND, new_lens=ctypes.c_void_p(at)) == -1
+    assert b"overlap" in capi.lib().tv_last_error()
+
+
 def test_append_of_an_empty_batch_does_nothing():
     assert _call("tv_kv_append", APPEND, B=0, T=0) == 0
 
