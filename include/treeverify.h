@@ -610,7 +610,9 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  *            slots and blocks that hold no visible key are never read.
  * seq_lens   device int32 [B]: L_b, the new token included; values outside
  *            [0, max_blocks * block_size] (or past 2^31 - 64) are clamped.
- * scale      softmax scale; softcap >= 0, finite.
+ * scale      softmax scale, finite; softcap >= 0, finite; both at most 2.3e38 in
+ *            size.  A cap past 2^126 |scale| is left out (it would first
+ *            change a score at |q . k| of 2^114).
  * window     0: every key is visible.  Else t is visible when t >= L_b - window
  *            or t < n_sink (the first n_sink keys stay visible; n_sink is
  *            ignored without a window).

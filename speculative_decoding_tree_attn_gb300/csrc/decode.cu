@@ -214,6 +214,12 @@ struct Scorer {
   }
 };
 
+// A head's bias in the log2 domain.  A finite one stays finite: the last key's distance is 0 and has to give 0.
+__device__ __forceinline__ float slope_of(const DecodeParams& p, int head) {
+  const float a = __ldg(p.slopes + head), x = a * kLog2e;
+  return fabsf(x) > FLT_MAX && fabsf(a) <= FLT_MAX ? copysignf(FLT_MAX, a) : x;
+}
+
 // Position of 16-byte unit u of a head's row in the merge buffer: spreads the
 // heads that a warp writes at once over the banks.
 __device__ __forceinline__ int merge_unit(int head, int u) {
@@ -281,7 +287,7 @@ struct Bf16Math {
         const int hc = 8 * n + 2 * t + e;
         m[n][e] = kNoScore;
         l[n][e] = 0.f;
-        slope[n][e] = p.slopes && hc < nh ? __ldg(p.slopes + h0 + hc) * kLog2e : 0.f;
+        slope[n][e] = p.slopes && hc < nh ? slope_of(p, h0 + hc) : 0.f;
       }
     }
   }
@@ -517,7 +523,7 @@ struct F32Math {
       }
     m = kNoScore;
     l = 0.f;
-    slope = p.slopes && lane % NH < nh ? __ldg(p.slopes + h0 + lane % NH) * kLog2e : 0.f;
+    slope = p.slopes && lane % NH < nh ? slope_of(p, h0 + lane % NH) : 0.f;
   }
 
   __device__ __forceinline__ void group(const DecodeParams& p, const Scorer& score, const Span& sp, int key, uint32_t kt,
@@ -1272,8 +1278,10 @@ extern "C" int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cac
   if (int rc = check_shape("tv_decode_attn", Hq, Hkv, head_dim, dtype, num_ctas)) return rc;
   if (B < 0 || num_blocks < 1 || block_size < 1 || max_blocks < 1 || window < 0 || n_sink < 0)
     return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: bad sizes");
-  if (!std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
-    return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: scale must be finite, softcap finite and not negative");
+  // scores are kept in the log2 domain: their factors are held there too
+  if (!std::isfinite(scale * kLog2e) || !(softcap >= 0.f) || !std::isfinite(softcap * kLog2e))
+    return tv::fail(TV_ERR_INVALID_ARG,
+                    "tv_decode_attn: scale must be finite, softcap finite and not negative, both within 2.3e38");
   if (flags & ~TV_ATTN_WORKSPACE_ZEROED) return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: unknown flags %d", flags);
   if (B == 0) return TV_OK;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out)
@@ -1306,7 +1314,9 @@ extern "C" int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cac
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.scale = scale;
-  p.softcap = softcap;
+  // tanh x is x to float32 for |x| < 2^-12: a factor below the normal numbers would lose bits of it, and caps nothing
+  // as long as q . k is below 2^114
+  p.softcap = softcap > 0.f && std::fabs(scale / softcap) < FLT_MIN ? 0.f : softcap;
   p.window = window;
   p.n_sink = n_sink;
   p.slopes = slopes;

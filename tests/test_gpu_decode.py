@@ -449,3 +449,20 @@ def test_no_score_above_minus_infinity(Hq, Hkv, D, dtype, num_ctas):
     assert (out[gone] == 0).all() and (lse[gone] == -np.inf).all()
     rest = [0, 2, 4]
     assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], wlse[rest])
+
+
+def test_the_largest_caps_and_biases():
+    """A cap far above every score changes nothing; a bias near float32's largest value leaves the last key alone."""
+    for dtype in ("f32", "bf16"):
+        c = _case([300, 17, 1], 4, 2, 64, dtype, 16, 79)
+        want, wlse = _run(c)
+        for cap in (1e30, 1e37, 1e38, 2.3e38):
+            out, lse = _run(c, softcap=cap)
+            # the cap's tanh and its two factors: 8 roundings of scores within 2^4
+            assert (lse - wlse).abs().max() <= 8 * 2.0 ** -24 * 16
+            u = torch.finfo(DT[dtype]).eps
+            assert ((out - want).float().abs() <= u * want.float().abs() + 16 * 2.0 ** -24 * 16 * 4).all()
+        out, lse = _run(c, slopes=torch.full((4,), 3.2e38, device="cuda"))
+        for b, L in enumerate([300, 17, 1]):
+            blk, slot = int(c["table"][b, (L - 1) // 16]), (L - 1) % 16
+            assert torch.equal(out[b], c["v"][blk, :, slot].repeat_interleave(2, 0)) and lse[b].isfinite().all()

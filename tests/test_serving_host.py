@@ -108,6 +108,14 @@ def test_decode_refuses_on_the_host(change, code, text):
     assert text in capi.lib().tv_last_error()
 
 
+@pytest.mark.parametrize("change,text", [(dict(softcap=3e38), b"softcap"), (dict(scale=3e38), b"scale"),
+                                         (dict(scale=-3e38), b"scale")])
+def test_decode_refuses_factors_past_the_log2_domain(change, text):
+    """Their product with log2 e is no float32: a score of 0 would come out as NaN."""
+    assert _call("tv_decode_attn", DECODE, **change) == -1
+    assert text in capi.lib().tv_last_error()
+
+
 def test_decode_of_an_empty_batch_does_nothing():
     assert _call("tv_decode_attn", DECODE, B=0) == 0
 
