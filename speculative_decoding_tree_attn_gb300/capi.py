@@ -615,6 +615,8 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
             return tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, scale=scale, softcap=softcap, window=window,
                                   n_sink=n_sink, slopes=slopes, out=out, lse=lse, workspace=workspace,
                                   num_ctas=num_ctas, flags=flags, status=status)
+    if (window | n_sink | num_ctas | flags) >> 31 not in (0, -1):  # ctypes would take them modulo 2^32
+        raise ValueError(f"window {window}, n_sink {n_sink}, num_ctas {num_ctas} or flags {flags} does not fit 32 bits")
     dev, st = _current()
     lens, B = _arg_batch(seq_lens, dev)
     kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
@@ -653,6 +655,8 @@ def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entro
         with torch.cuda.stream(stream):
             return tv_token_logprobs(logits, tokens, node=node, top_k=top_k, logprob=logprob, entropy=entropy,
                                      top_ids=top_ids, top_logprobs=top_logprobs, status=status)
+    if top_k >> 31 not in (0, -1):
+        raise ValueError(f"top_k {top_k} does not fit 32 bits")
     dev, st = _current()
     if not isinstance(logits, torch.Tensor) or logits.dim() != 3 or logits.dtype not in (torch.float32, torch.bfloat16):
         _refuse(logits, "logits", "float32 or bfloat16", (None,) * 3, dev)

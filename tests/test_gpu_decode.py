@@ -466,3 +466,15 @@ def test_the_largest_caps_and_biases():
         for b, L in enumerate([300, 17, 1]):
             blk, slot = int(c["table"][b, (L - 1) // 16]), (L - 1) % 16
             assert torch.equal(out[b], c["v"][blk, :, slot].repeat_interleave(2, 0)) and lse[b].isfinite().all()
+
+
+def test_numbers_past_32_bits_are_refused():
+    """None of them is taken modulo 2^32; negative ones are the library's to refuse, as before."""
+    c = _case([40, 9], 4, 2, 64, "bf16", 16, 173)
+    for name in ("window", "n_sink", "num_ctas", "flags"):
+        with pytest.raises(capi.TVError):
+            capi.tv_decode_attn(c["q"], c["k"], c["v"], c["table"], c["lens"], **{name: -1})
+    for name in ("window", "n_sink", "num_ctas", "flags"):
+        for x in (1 << 32, (1 << 32) + 5, 1 << 31, -(1 << 32)):
+            with pytest.raises((ValueError, capi.TVError), match=name):
+                capi.tv_decode_attn(c["q"], c["k"], c["v"], c["table"], c["lens"], **{name: x})

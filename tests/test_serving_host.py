@@ -224,3 +224,15 @@ def test_decode_oracle_without_any_weight():
     out, lse = OA.decode_attention(np.ones((2, 2, 8)), k, v, np.array([[0], [1]]), [5, 5])
     assert (out[0] == 0).all() and (lse[0] == -np.inf).all()
     np.testing.assert_allclose(out[1], 1.0, atol=1e-15)
+
+
+@pytest.mark.parametrize("name", ["window", "n_sink", "num_ctas", "flags"])
+@pytest.mark.parametrize("x", [1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 31) - 1, -(1 << 32)])
+def test_binding_refuses_numbers_past_32_bits(name, x):
+    lens, table = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    cache, q = torch.zeros(3, 1, 16, 64), torch.zeros(2, 4, 64)
+    with pytest.raises(ValueError, match=name + f" {x}"):
+        capi.tv_decode_attn(q, cache, cache, table, lens, **{name: x})
+    if name == "window":
+        with pytest.raises(ValueError, match=f"top_k {x}"):
+            capi.tv_token_logprobs(torch.zeros(2, 3, 10), lens[:, None], top_k=x)
