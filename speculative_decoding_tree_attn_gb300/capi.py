@@ -126,13 +126,19 @@ def _dev(t, name, dtypes):
     return t
 
 
+# torch's own raw calls, without the objects that torch.cuda makes (8 us of a call's 20); a torch that lacks the names
+# has the public ones
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_stream_now = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+
+
 def _current():
-    """Current device and its current stream's handle, without the objects that torch.cuda makes for them
-    (8 us of a call's 20); no tensor is on device -2."""
+    """Current device and its current stream's handle; no tensor is on device -2."""
     if not torch.cuda.is_initialized():
         return -2, 0
-    dev = torch._C._cuda_getDevice()
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
+    dev = _device_now()
+    return dev, _stream_now(dev)
 
 
 def _refuse(t, name, dtype, shape, dev):

@@ -3,7 +3,9 @@ probabilities) that need no GPU: argument errors are reported before anything
 is launched, and the oracle's definitions agree with independent ones."""
 
 import ctypes
+import importlib.util
 import os
+import types
 
 import numpy as np
 import pytest
@@ -236,3 +238,16 @@ def test_binding_refuses_numbers_past_32_bits(name, x):
     if name == "window":
         with pytest.raises(ValueError, match=f"top_k {x}"):
             capi.tv_token_logprobs(torch.zeros(2, 3, 10), lens[:, None], top_k=x)
+
+
+def test_binding_without_torchs_raw_calls(monkeypatch):
+    """A torch without the two private names: the public calls give device and stream."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("capi_public", capi.__file__)
+    copy = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(copy)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: types.SimpleNamespace(cuda_stream=70 + dev))
+    assert copy._current() == (3, 73)
