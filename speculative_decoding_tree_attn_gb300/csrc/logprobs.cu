@@ -512,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
     }
     // a row without a distribution: a NaN or +inf in it, or nothing above -inf
     const float log2_s = wrong || all.m == -INFINITY ? NAN : log2f(all.s);
-    const float ln_s = (log2_s - distance(all.m, all.m)) * kLn2;  // ln sum e^(x - m)
+    const float log2_sum = log2_s - distance(all.m, all.m);  // log2 sum e^(x - m)
     // A row that one token has to itself: the reference's rounding is in S and taken away again, which leaves a few
     // 2^-24 of either sign.  ln p <= 0 <= H; a NaN stays one.
     auto ln_p = [&](float x) {
-      const float y = x - all.m - ln_s;
+      const float y = __fmaf_rn(log2_sum, -kLn2, x - all.m);
       return y > 0.f ? 0.f : y;
     };
     if (tid == 0) {
