@@ -267,14 +267,22 @@ struct Best {
     }
     if (lane < kTold) *(volatile uint32_t*)(shared + lane) = mine4;
   }
-  __device__ __forceinline__ void heed(const uint32_t* shared, int k, int lane) {  // the k-th of all warps'
+  // The k-th of all warps'.  Others may write theirs meanwhile (volatile on both sides: every number is one that its
+  // warp told, though four need not be of one time).  A warp's j-th number only grows, as its lanes' maxima do, so a mix
+  // of times is nowhere above the latest numbers: no fewer than k elements reach the bar.  (A lane that meets a NaN tells
+  // less from then on; the element behind what it told before is still there.)
+  __device__ __forceinline__ void heed(const uint32_t* shared, int k, int lane) {
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(shared);
     uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + 4 * lane) : "memory");
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + 4 * lane) : "memory");
     uint32_t reach = 0;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      const uint4 o = lds128(at + 4 * j);
+      uint4 o;
+      asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                   : "r"(at + 4 * j)
+                   : "memory");
       reach = count_ge(count_ge(count_ge(count_ge(reach, o.x, -v), o.y, -v), o.z, -v), o.w, -v);
     }
     // under every index of that value
