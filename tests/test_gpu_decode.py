@@ -478,3 +478,15 @@ def test_numbers_past_32_bits_are_refused():
         for x in (1 << 32, (1 << 32) + 5, 1 << 31, -(1 << 32)):
             with pytest.raises((ValueError, capi.TVError), match=name):
                 capi.tv_decode_attn(c["q"], c["k"], c["v"], c["table"], c["lens"], **{name: x})
+
+
+def test_a_request_in_hundreds_of_pieces():
+    """More than 512 pieces of one request: joined in runs of 20, the same bits each time, counters left zero."""
+    c = _case([20000, 7], 1, 1, 256, "f32", 16, 2800)
+    ws = capi.alloc_workspace(capi.tv_decode_attn_workspace_size(1, 1, 256, torch.float32, 700))
+    runs = []
+    for _ in range(3):
+        runs.append(_run(c, workspace=ws, num_ctas=700, flags=capi.TV_ATTN_WORKSPACE_ZEROED))
+        assert int(ws[:16384].max()) == 0
+    _check(c, *runs[0])
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))

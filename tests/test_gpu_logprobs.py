@@ -357,3 +357,20 @@ def test_confident_rows_keep_their_signs(dtype, rows, V):
             assert (got[0].abs() <= 2.0 ** -20).all() and (got[1] <= 2.0 ** -20).all()
     x = (torch.randn(1, rows, V, generator=g, device="cuda") * 6 + best).to(DT[dtype])
     _signs(_check(x, t, top_k=3))
+
+
+@pytest.mark.parametrize("name", sorted(_special()))
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_every_copy_of_a_special_row(name, dtype):
+    """400 entries of one row: all four outputs the same in each, the first within the bounds of the oracle."""
+    x = _special()[name].to(DT[dtype]).cuda().view(1, 1, -1)
+    many = capi.tv_token_logprobs(x, torch.full((1, 400), 31234, dtype=torch.int32, device="cuda"),
+                                  node=torch.zeros(1, 400, dtype=torch.int32, device="cuda"), top_k=32)
+    for m in many:
+        bits = m.view(torch.int32)
+        assert torch.equal(bits, bits[:, :1].expand_as(bits))
+    # entries of their own are one CTA each too: the same bits, within the bounds of _check
+    rows = x.expand(1, 160, -1).contiguous()
+    first = _check(rows, torch.full((1, 160), 31234, dtype=torch.int32, device="cuda"), top_k=32)
+    for m, f in zip(many, first):
+        assert torch.equal(m[:, 0].view(torch.int32), f[:, 0].view(torch.int32))
