@@ -616,7 +616,8 @@ int tv_decode_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int
  * window     0: every key is visible.  Else t is visible when t >= L_b - window
  *            or t < n_sink (the first n_sink keys stay visible; n_sink is
  *            ignored without a window).
- * slopes     device float32 [Hq] (nullable): distance bias per query head.
+ * slopes     device float32 [Hq] (nullable): distance bias per query head; one past
+ *            2.3e38 in size counts as that.
  * out        device [B, Hq, head_dim] (dtype) out, contiguous.
  * lse        device float32 [B, Hq] out (nullable): natural-log normaliser.
  * workspace  device buffer of at least tv_decode_attn_workspace_size bytes, 256-

@@ -102,9 +102,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// What a row is multiplied with: 1 over its weights' sum.  Without any weight (no visible key, or only scores of -inf)
-// the row is zero, and its m + log2 of the sum is -inf by itself; a NaN stays one.
-__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+// What a row is multiplied with: 1 over its weights' sum, which is 1 at least where there are any.  Without (no visible
+// key, or only scores of -inf) the row is zero, and its m + log2 of the sum is -inf by itself; NaN outputs stay NaN.
+__device__ __forceinline__ float inverse(float sum) { return 1.f / fmaxf(sum, FLT_MIN); }
 
 // A sum against m as one against top.
 __device__ __forceinline__ float scaled(float x, float m, float top) { return x * exp2_approx(m - top); }
@@ -214,10 +214,11 @@ struct Scorer {
   }
 };
 
-// A head's bias in the log2 domain.  A finite one stays finite: the last key's distance is 0 and has to give 0.
+// A head's bias in the log2 domain, held within float32: the last key's distance is 0 and has to give 0.
 __device__ __forceinline__ float slope_of(const DecodeParams& p, int head) {
-  const float a = __ldg(p.slopes + head), x = a * kLog2e;
-  return fabsf(x) > FLT_MAX && fabsf(a) <= FLT_MAX ? copysignf(FLT_MAX, a) : x;
+  float x = __ldg(p.slopes + head) * kLog2e;
+  asm("{\n\tmin.NaN.f32 %0, %0, 0f7f7fffff;\n\tmax.NaN.f32 %0, %0, 0fff7fffff;\n\t}" : "+f"(x));
+  return x;
 }
 
 // Position of 16-byte unit u of a head's row in the merge buffer: spreads the

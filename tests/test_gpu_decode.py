@@ -490,3 +490,26 @@ def test_a_request_in_hundreds_of_pieces():
         assert int(ws[:16384].max()) == 0
     _check(c, *runs[0])
     assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(8, 2, 128, "bf16"), (16, 1, 256, "bf16"), (8, 8, 64, "bf16"), (4, 1, 64, "f32")])
+@pytest.mark.parametrize("num_ctas", [0, 1, 40])
+def test_nan_reaches_its_own_rows_only(Hq, Hkv, D, dtype, num_ctas):
+    """A NaN among a request's keys, or as a bias, makes its rows NaN; an infinite bias leaves the last key alone."""
+    lens = [700, 5000, 1, 20, 16, 300]
+    c = _case(lens, Hq, Hkv, D, dtype, 16, 78)
+    want, wlse = _run(c, num_ctas=num_ctas)
+    table = c["table"].cpu().numpy()
+    for b, t in ((1, 4000), (3, 19), (4, 0)):
+        c["k"][table[b, t // 16], :, t % 16] = float("nan")
+    out, lse = _run(c, num_ctas=num_ctas)
+    assert out[[1, 3, 4]].isnan().all() and lse[[1, 3, 4]].isnan().all()
+    rest = [0, 2, 5]
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], wlse[rest])
+    slopes = torch.zeros(Hq, device="cuda")
+    slopes[0], slopes[-1] = float("inf"), float("nan")
+    out, lse = _run(c, slopes=slopes, num_ctas=num_ctas)
+    for b in rest:
+        L = lens[b]
+        assert torch.equal(out[b, 0], c["v"][table[b, (L - 1) // 16], 0, (L - 1) % 16]) and lse[b, 0].isfinite()
+        assert out[b, -1].isnan().all() and lse[b, -1].isnan()
