@@ -239,6 +239,8 @@ __device__ __forceinline__ int merge_unit(int head, int u) {
 //   permutes; P^T is S^T's registers with their 8x8 blocks transposed.
 // P is held as two bf16 parts (value and remainder, 16 bits together): the
 // products are far from the limit, and one part alone would add 2^-9 a weight.
+// The sum takes the weight as it was, 2^-17 of it away at most, which is lost in
+// the outputs' own rounding (2^-9).
 // ---------------------------------------------------------------------------
 template <int D, int NB>
 struct Bf16Math {
@@ -668,7 +670,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 
 // A CTA: 8 warps whose rings take 192 KB, so that 128 KB are in flight while a
 // third is computed; 4 warps where a group is 16 KB; 16 where it is 4 KB (twice
-// the instructions a byte).
+// the instructions a byte), which leaves 128 registers a thread: bf16 units of 8
+// and 16 heads spill 20 and 38 bytes there (64 requests of 1k-8k, 32/8 heads: 105
+// us, 0.84 of the copy rate).
 template <class Math, int D>
 struct Shape {
   static constexpr int kTile = Math::kKeys * Math::kRowBytes;  // K or V of a group
@@ -1204,8 +1208,9 @@ int call_decode(const Call& c, int Hkv, int G) {
 // Query heads of a unit.  bf16: 8, or 16 where a KV head serves more than 8 (two
 // 8-column products share a key's loads), rows of 256 only where the units are a
 // quarter of the CTAs, as their pieces are twice as large (60 requests of 2k-8.7k,
-// 32/2 heads: 147 us, 8 heads a unit 203; 8 of 500-2000: 35 and 21).  float32: as
-// many as the KV head serves, 8 at most.
+// 32/2 heads: 138-147 us, 8 heads a unit 203; 8 of 500-2000: 35 and 21).  Units of
+// unused slots and short requests count alike: lengths are known on the device
+// only.  float32: as many as the KV head serves, 8 at most.
 template <int D>
 int dispatch_heads(const Call& c, int dtype, int Hkv, int G) {
   if (dtype == TV_BF16) {

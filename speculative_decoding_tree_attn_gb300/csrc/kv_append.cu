@@ -10,9 +10,9 @@
 //
 // Pure movement: (Hq + 2 Hkv) D elements a token read once and written once;
 // the rotation is 3 flops an element.  Bound by HBM for a prompt (32 prompts of
-// 1-1023 tokens, 32/8 heads of 128, bf16: 65 us, 0.95 of the measured copy rate;
+// 1-1023 tokens, 32/8 heads of 128, bf16: 65 us, 0.96 of the measured copy rate;
 // CTAs of 256 threads 68 us, twice the loads in flight a lane 81 us), by latency
-// for a step's tokens (256 requests: 3.0 us).
+// for a step's tokens (256 requests: 3.3 us).
 #include <algorithm>
 #include <climits>
 
@@ -88,7 +88,9 @@ __device__ __forceinline__ bool find_request(const AppendParams& p, int t, int l
   return s0 >= 0 && s0 <= t && t < s1 && s1 <= p.T;
 }
 
-// New length of request b: the tokens before the first that cannot be placed.  Search is the one that the tokens' warps use.
+// New length of request b: the tokens before the first that cannot be placed.  Search is the one that the tokens' warps
+// use.  Blocks are looked at 32 a trip to L2, behind the copies: one prompt of 32k tokens, 32/8 heads of 128, takes
+// 149 us in blocks of 16 and 638 in blocks of 1, of a floor of 121.
 template <class Search>
 __device__ void count_request(const AppendParams& p, int b, int lane) {
   const int L = p.seq_lens[b];

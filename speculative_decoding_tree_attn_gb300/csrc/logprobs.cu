@@ -11,12 +11,13 @@
 // One pass: a row is read once, by a cluster of 1-8 CTAs (the fewer rows, the
 // more), in 16-byte vectors that each thread copies to its own places in shared
 // memory two batches ahead (no barrier; 32 KB in flight a CTA, 4 CTAs an SM).
-// Bound by HBM for float32, by the issue slots for bf16: an element costs eight
-// instructions (unpacking, its place in the maximum, one exponential, three for the
-// sums), ten with alternatives; 1999 rows of 128,000 bf16 logits take 96 us with 5
-// alternatives (0.78 of the measured copy rate, 78 % of the slots issued), 83 us
-// without.  Everything is summed in the log2 domain against r = fl(m log2 e): with
-// S = sum 2^(x log2 e - r) the rounding of r cancels in x log2 e - r - log2 S, and a
+// Bound by HBM for float32 (1000 rows of 128,000: 82 us, 0.92 of the measured copy
+// rate), by the issue slots for bf16: an element costs eight instructions
+// (unpacking, its place in the maximum, one exponential, three for the sums), ten
+// with alternatives; 1999 rows of 128,000 bf16 logits take 94 us with 5
+// alternatives (0.80 of the copy rate, 78 % of the slots issued), 82 us without.
+// Everything is summed in the log2 domain against r = fl(m log2 e): with S = sum
+// 2^(x log2 e - r) the rounding of r cancels in x log2 e - r - log2 S, and a
 // distance is one FMA.
 //
 // The alternatives cost little beside that.  A thread's maximum is kept anyway, and
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
 
 template <typename T>
 int launch_logprobs(const LogprobParams& p, int sm_count, cudaStream_t stream) {
-  // A row's CTAs.  A cluster costs most of a microsecond, so it has to save more: 4 or 8 CTAs while no SM gets two, of
+  // A row's CTAs; an entry that turns out to be none counts too, as tokens are known on the device only.
+  // A cluster costs most of a microsecond, so it has to save more: 4 or 8 CTAs while no SM gets two, of
   // 6144 logits at least (5 rows of 32,000 bf16 and 5 alternatives: 6.8 us by four, 7.4 in one; of 16,000 both 6.7 and
   // 6.2), 2 with 48 KB each (76 rows of 100 KB: 9.1 against 10.1, of 64 KB 8.1 and 8.0), and on SMs with a CTA already
   // 128 KB each (120 rows of 300 KB: 17.0 against 18.0, of 200 KB 11.7 and 10.7; 152 of 100 KB by four 17 and 10).
