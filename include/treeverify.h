@@ -570,7 +570,8 @@ int tv_kv_commit(void* k_cache, void* v_cache, int64_t num_blocks, int32_t block
  * table (TV_DEV_BAD_POSITION) or has no valid block in the table
  * (TV_DEV_OUT_OVERFLOW) is not stored and ends the returned length there;
  * a later token whose own block is valid may be stored past that length.
- * q_out rows are written for every token whose position is in the rotary table.
+ * q_out rows are written for every token that good offsets, in order, place at a
+ * position in the rotary table.
  * head_dim in {16, 32, 64, 128, 256}; every buffer and token stride a multiple
  * of 16 bytes (else TV_ERR_INVALID_ARG; the strides of a single token are not used).
  */
