@@ -56,6 +56,8 @@ extern "C" {
                                    [0, num_blocks): those keys and values read as zeros */
 #define TV_DEV_BAD_OFFSETS 64   /* token offsets that decrease or leave [0, T]: a
                                    request that they touch gets no tokens        */
+#define TV_DEV_BAD_PARAM 128    /* a temperature that is negative, infinite or NaN:
+                                   its row counts as one without a distribution  */
 
 /* ---- element types ------------------------------------------------------ */
 #define TV_F32 0
@@ -584,6 +586,38 @@ int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_str
                  int32_t head_dim, int32_t dtype, int32_t* status, void* stream);
 
 /*
+ * tv_kv_append_norm -- device, asynchronous.  tv_kv_append with each head of the
+ * keys and queries normalised before its rotation, and with other rotations:
+ *   y = x * weight / sqrt(mean(x^2) + eps), its leading rot_dim elements turned
+ * by the position's angles.  Sums, factors and rotation are float32 and a row is
+ * rounded once; a row whose squares leave float32 follows float32's rules.  Without
+ * weights, interleaving and with rot_dim = head_dim it gives tv_kv_append's bits.
+ *
+ * q_weight  device [head_dim] (dtype), nullable: queries are not normalised.
+ * k_weight  device [head_dim] (dtype), nullable: keys are not normalised.
+ * eps       finite, not negative.
+ * cos_sin   device float32 [max_pos, 2, rot_dim/2], tv_rope_table(max_pos, rot_dim)
+ *           for instance (nullable: nothing is rotated, rot_dim is ignored and
+ *           every position is in range).
+ * rot_dim   a multiple of 16, at most head_dim: the elements that are rotated; the
+ *           others are only normalised.
+ * interleaved 0: element i is paired with element i + rot_dim/2; 1: element 2i
+ *           with element 2i + 1.
+ * Everything else (which tokens are stored, lengths, status bits, strides, head
+ * dimensions) as in tv_kv_append; q may be given without cos_sin.  Weights 16-byte
+ * aligned.
+ */
+int tv_kv_append_norm(const void* q, int64_t q_stride, const void* q_weight, void* q_out,
+                      int64_t q_out_stride, int32_t Hq, const void* k_new, int64_t k_stride,
+                      const void* k_weight, const void* v_new, int64_t v_stride, float eps,
+                      const int32_t* cu_new, int32_t T, void* k_cache, void* v_cache,
+                      int64_t num_blocks, int32_t block_size, const int32_t* block_table,
+                      int32_t max_blocks, const int32_t* seq_lens, int32_t* new_seq_lens,
+                      const float* cos_sin, int32_t max_pos, int32_t rot_dim,
+                      int32_t interleaved, int32_t B, int32_t Hkv, int32_t head_dim,
+                      int32_t dtype, int32_t* status, void* stream);
+
+/*
  * tv_decode_attn_workspace_size -- host (queries the current device).  Bytes of
  * device workspace that tv_decode_attn needs for these heads, type and grid
  * (num_ctas, 0 = one wave of the current device).  Depends on neither the batch
@@ -647,6 +681,71 @@ int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cache, const v
                    int32_t* status, void* stream);
 
 /*
+ * tv_chunk_attn_workspace_size -- host (queries the current device).  Bytes of
+ * device workspace that tv_chunk_attn needs for these heads, type and grid
+ * (num_ctas, 0 = one CTA per SM of the current device).  Depends on neither the
+ * batch nor the lengths; at most 64 MiB with num_ctas = 0.
+ */
+int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t dtype,
+                                 int32_t num_ctas, size_t* bytes);
+
+/*
+ * tv_chunk_attn -- device, asynchronous.  Attention of a chunk of new tokens per
+ * request over the paged cache -- a whole prompt, the next piece of one, or a few
+ * tokens -- which already holds their keys and values (tv_kv_append).  Token j of a
+ * chunk of n sits at position p = L_b - n + j; its output row of head h is
+ * softmax(s) V over the visible keys of KV head h / (Hq/Hkv),
+ *   s_t = cap(scale * q . k_t) + slopes[h] * (t - p),  cap as in tv_decode_attn;
+ * key t is visible when t <= p and, with a window, t > p - window or t < n_sink.
+ * A score of -inf has no weight; a row without any weight (no visible key: its
+ * position is below 0, n being larger than L_b; or every score -inf) is zero with
+ * lse = -inf.  Visible values are finite.
+ * No page defines the call: it is the chain case of "Tree Verification", "Tree
+ * Attention", with the chain's K/V in the cache.
+ *
+ * q          device [T, Hq, head_dim] (dtype), q_stride elements between tokens
+ *            (heads contiguous), rotated (tv_kv_append).
+ * k_cache, v_cache, block_table: as in tv_decode_attn; any block_size >= 1.
+ *            What lies in slots that hold no key visible to the request does not matter.
+ * seq_lens   device int32 [B]: L_b, the chunk's tokens included (tv_kv_append's
+ *            new_seq_lens); values outside [0, max_blocks * block_size] (or past 2^31 -
+ *            1024) are clamped.
+ * cu_new     device int32 [B + 1] (nullable): request b's tokens are the packed rows
+ *            cu_new[b] .. cu_new[b + 1] - 1, as in tv_kv_append.  NULL: T / B rows each.
+ *            A request whose offsets decrease or leave [0, T] has no rows
+ *            (TV_DEV_BAD_OFFSETS); a row that offsets out of order give to two
+ *            requests, or lead past, holds either's result or what it held.  Rows of
+ *            no request are left as they are, in out and lse.
+ * scale, softcap, window, n_sink, slopes: as in tv_decode_attn.
+ * out        device [T, Hq, head_dim] (dtype) out, contiguous.
+ * lse        device float32 [T, Hq] out (nullable): natural-log normaliser.
+ * workspace  device buffer of at least tv_chunk_attn_workspace_size bytes, 256-byte
+ *            aligned; its counters (the first 16 KiB) as in tv_decode_attn: cleared
+ *            first, or taken as zero with TV_ATTN_WORKSPACE_ZEROED and left zero
+ *            by a call that completes (not by one that reports TV_DEV_TIMEOUT).
+ *            Calls that overlap on the GPU need their own.
+ * num_ctas   persistent grid of the tensor-core kernel (0 = one CTA per SM); at most
+ *            4096, the value given to tv_chunk_attn_workspace_size.
+ * flags      TV_ATTN_AUTO, TV_ATTN_SIMT (float32 on CUDA cores, every shape) or
+ *            TV_ATTN_TCGEN05 (TV_ERR_UNSUPPORTED where it cannot run), and
+ *            TV_ATTN_WORKSPACE_ZEROED.
+ * status     device int32 (nullable): TV_DEV_BAD_OFFSETS; TV_DEV_BAD_BLOCK (a visible
+ *            position's block is outside [0, num_blocks): its key and value count
+ *            as zeros); TV_DEV_TIMEOUT.
+ * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, any Hq / Hkv, Hkv <= 65535;
+ * q, out and the caches 16-byte aligned, q_stride a multiple of 16 bytes (unused
+ * for one token).
+ */
+int tv_chunk_attn(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                  int64_t num_blocks, int32_t block_size, const int32_t* block_table,
+                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_new,
+                  int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                  int32_t dtype, float scale, float softcap, int32_t window, int32_t n_sink,
+                  const float* slopes, void* out, float* lse, void* workspace,
+                  size_t workspace_bytes, int32_t num_ctas, int32_t flags, int32_t* status,
+                  void* stream);
+
+/*
  * tv_token_logprobs -- device, asynchronous.  Log probabilities of given tokens
  * under rows of logits, with each row's entropy and its most likely
  * alternatives, from one pass over the row.  Takes what acceptance returns: out
@@ -679,6 +778,44 @@ int tv_token_logprobs(const void* logits, const int32_t* tokens, const int32_t* 
                       int32_t N, int32_t C, int32_t V, int32_t dtype, float* logprob,
                       float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs,
                       int32_t* status, void* stream);
+
+/*
+ * tv_token_sample -- device, asynchronous.  One token per row of logits, drawn with a
+ * given uniform number from the row's processed distribution, and that
+ * distribution: what tv_tree_accept_sample takes as p or, for the rows that
+ * drafted tokens were drawn from, as q ("Implement the lossless speculative
+ * sampling verifier ...", "Details that matter in review").
+ *
+ * With w_i = exp((x_i - max x) / temperature), in this order: the top_k largest
+ * logits are kept (equal ones by ascending index); of these the ones with w_i >=
+ * min_p; of these, in descending order, the shortest run whose sum reaches top_p of
+ * theirs (at least one).  The token is the first index whose running sum over the
+ * kept w exceeds u times their total.  Sums are exact over weights that are good
+ * to 2^-39 of themselves or 2^-44 of the largest, so a token is the one of the
+ * definition in float64 unless u falls on the border of two.
+ *
+ * logits    device [R, V] (dtype), contiguous; -inf: an excluded token.
+ * temperature device float32 [R] (nullable: 1): 0 (or anything below 2^-60): the
+ *           largest logit alone, the first of equal ones; past 2^60 it counts as that.
+ *           Negative, infinite or NaN: TV_DEV_BAD_PARAM, no distribution.
+ * top_k     device int32 [R] (nullable): 0, negative or >= V: no limit.
+ * top_p     device float32 [R] (nullable): 1, more or NaN: no limit; 0 or less: the
+ *           first of the order alone.
+ * min_p     device float32 [R] (nullable): 0, negative or NaN: no limit; more than 1
+ *           counts as 1.
+ * u         device float32 [R] in [0, 1): 1 or more gives the last kept token with any
+ *           weight, less than 0 or NaN the first.
+ * tokens    device int32 [R] out.
+ * probs     device float32 [R, V] out (nullable): w_i / their total, 0 for a token that
+ *           is not kept.
+ * A row that holds a NaN or +inf, or nothing above -inf, has no distribution: its
+ * token is -1, its probabilities are NaN.
+ * logits and probs 16-byte aligned; V <= 1,048,576 (else TV_ERR_UNSUPPORTED).
+ */
+int tv_token_sample(const void* logits, int64_t R, int32_t V, int32_t dtype,
+                    const float* temperature, const int32_t* top_k, const float* top_p,
+                    const float* min_p, const float* u, int32_t* tokens, float* probs,
+                    int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -221,3 +221,23 @@ def decode_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, sof
             out[b, h] = w @ values[:, h // (Hq // Hkv)] / w.sum()
             lse[b, h] = m + np.log(w.sum())
     return out, lse
+
+
+def chunk_attention(q, k_cache, v_cache, block_table, seq_lens, counts, scale=None, softcap=0.0, window=0, n_sink=0,
+                    slopes=None):
+    """Attention of each request's last ``counts[b]`` tokens over its seq_lens[b] cached keys (their own among them):
+    packed q [T, Hq, D] -> (out [T, Hq, D], lse [T, Hq]), float64; rows behind the last request are zero, -inf.
+
+    Token j of request b sits at p = L_b - counts[b] + j and is the one token of a sequence of p + 1 keys.
+    """
+    q = np.asarray(q, dtype=np.float64)
+    out, lse = np.zeros_like(q), np.full(q.shape[:2], -np.inf)
+    t = 0
+    for b, n in enumerate(counts):
+        for j in range(int(n)):
+            length = max(0, int(seq_lens[b]) - int(n) + j + 1)
+            o, l = decode_attention(q[t:t + 1], k_cache, v_cache, block_table[b:b + 1], [length], scale, softcap, window,
+                                    n_sink, slopes)
+            out[t], lse[t] = o[0], l[0]
+            t += 1
+    return out, lse

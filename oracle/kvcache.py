@@ -103,3 +103,40 @@ def append_tokens(k_cache, v_cache, block_table, seq_lens, k_new, v_new, counts,
             t += 1
         lens[b] = L + (int(counts[b]) if done is None else done)
     return kc, vc, lens, qo
+
+
+def norm_rows(x, weight, eps):
+    """Rows x [..., D] divided by their root mean square (eps added to the mean square) and scaled by weight [D]."""
+    x = np.asarray(x, dtype=np.float64)
+    return x / np.sqrt((x * x).mean(axis=-1, keepdims=True) + eps) * np.asarray(weight, dtype=np.float64)
+
+
+def turn_rows(x, table, interleaved=False):
+    """The leading R elements of rows x [T, H, D] turned by the angles' cos and sin, table [T, 2, R/2]: element i with
+    i + R/2 or, interleaved, 2i with 2i + 1."""
+    y = np.array(x, dtype=np.float64)
+    half = table.shape[2]
+    first, second = ((slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved
+                     else (slice(0, half), slice(half, 2 * half)))
+    a, b = np.array(y[..., first]), np.array(y[..., second])
+    c, s = (np.asarray(table, dtype=np.float64)[:, None, i] for i in (0, 1))
+    y[..., first], y[..., second] = a * c - b * s, b * c + a * s
+    return y
+
+
+def append_normed(k_cache, v_cache, block_table, seq_lens, k_new, v_new, counts, q=None, q_weight=None, k_weight=None,
+                  eps=0.0, table=None, interleaved=False):
+    """append_tokens of rows normalised per head (weights given) and turned by the rotary ``table`` [max_pos, 2, R/2]
+    (None: not turned), every position within it.  Returns (k_cache', v_cache', seq_lens', q')."""
+    counts = np.asarray(counts, dtype=np.int64)
+    pos = np.concatenate([np.arange(L, L + n) for L, n in zip(seq_lens, counts)]).astype(np.int64)
+    total = pos.size
+
+    def done(x, weight):
+        y = np.array(x, dtype=np.float64)
+        z = y[:total] if weight is None else norm_rows(y[:total], weight, eps)
+        y[:total] = z if table is None else turn_rows(z, np.asarray(table)[pos], interleaved)
+        return y
+
+    kc, vc, lens, _ = append_tokens(k_cache, v_cache, block_table, seq_lens, done(k_new, k_weight), v_new, counts)
+    return kc, vc, lens, None if q is None else done(q, q_weight)

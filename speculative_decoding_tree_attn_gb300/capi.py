@@ -29,6 +29,7 @@ TV_SAMPLE_AUTO, TV_SAMPLE_CLUSTER, TV_SAMPLE_SINGLE_CTA, TV_SAMPLE_STREAM, TV_SA
 TV_DEV_BAD_TOPOLOGY, TV_DEV_BAD_TOKEN, TV_DEV_OUT_OVERFLOW, TV_DEV_BAD_POSITION, TV_DEV_TIMEOUT = 1, 2, 4, 8, 16
 TV_DEV_BAD_BLOCK = 32
 TV_DEV_BAD_OFFSETS = 64
+TV_DEV_BAD_PARAM = 128
 TV_MAX_TOP_K = 32
 STATUS_NAMES = {0: "TV_OK", -1: "TV_ERR_INVALID_ARG", -2: "TV_ERR_MISSING_PARENT", -3: "TV_ERR_TOO_MANY_NODES",
                 -4: "TV_ERR_UNSUPPORTED", -5: "TV_ERR_WORKSPACE", -6: "TV_ERR_CUDA"}
@@ -64,9 +65,15 @@ SIGNATURES = {
                                     _I32, _I32, _P, _P]),
     "tv_kv_append": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _I64, _I32, _P,
                                     _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "tv_kv_append_norm": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _P, _I64, _P, _P, _I64, _F, _P, _I32, _P, _P, _I64,
+                                         _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "tv_decode_attn_workspace_size": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P]),
     "tv_decode_attn": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F,
                                       _F, _I32, _I32, _P, _P, _P, _P, _SZ, _I32, _I32, _P, _P]),
+    "tv_chunk_attn_workspace_size": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P]),
+    "tv_chunk_attn": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                     _F, _F, _I32, _I32, _P, _P, _P, _P, _SZ, _I32, _I32, _P, _P]),
+    "tv_token_sample": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "tv_token_logprobs": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P]),
 }
 
@@ -603,6 +610,58 @@ def tv_kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, cos_s
     return q_out, new_seq_lens
 
 
+def tv_kv_append_norm(k_new, v_new, k_cache, v_cache, block_table, seq_lens, *, k_weight=None, q=None, q_weight=None,
+                      q_out=None, eps=1e-6, cos_sin=None, interleaved=False, cu_new=None, new_seq_lens=None, status=None,
+                      stream=None):
+    """tv_kv_append with every head of the keys (queries) normalised by its root
+    mean square and scaled by k_weight (q_weight) [D] in the cache's type (None:
+    not normalised) before the rotation, which turns the leading R elements of
+    cos_sin [max_pos, 2, R/2], in halves or, interleaved, in neighbouring pairs.
+    Returns (q_out, new_seq_lens int32 [B])."""
+    if stream is not None:  # under it, so that what the call allocates is ordered and reused with its work
+        with torch.cuda.stream(stream):
+            return tv_kv_append_norm(k_new, v_new, k_cache, v_cache, block_table, seq_lens, k_weight=k_weight, q=q,
+                                     q_weight=q_weight, q_out=q_out, eps=eps, cos_sin=cos_sin, interleaved=interleaved,
+                                     cu_new=cu_new, new_seq_lens=new_seq_lens, status=status)
+    dev, st = _current()
+    lens, B = _arg_batch(seq_lens, dev)
+    kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
+    T = _rows(k_new, "k_new", dev)
+    k, k_stride = _arg_rows(k_new, "k_new", dt, (T, Hkv, D), dev)
+    v, v_stride = _arg_rows(v_new, "v_new", dt, (T, Hkv, D), dev)
+    cs = qp = qo = qw = None
+    Hq = max_pos = rot = q_stride = out_stride = 0
+    if cos_sin is not None:
+        max_pos = _rows(cos_sin, "cos_sin", dev)
+        rot = 2 * cos_sin.shape[2]
+        cs = _arg(cos_sin, "cos_sin", torch.float32, (max_pos, 2, rot // 2), dev)
+    if q is not None:
+        _rows(q, "q", dev)
+        Hq = q.shape[1]
+        qp, q_stride = _arg_rows(q, "q", dt, (T, Hq, D), dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            qo, out_stride = q_out.data_ptr(), Hq * D
+        else:
+            qo, out_stride = _arg_rows(q_out, "q_out", dt, (T, Hq, D), dev)
+    if q_weight is not None:
+        qw = _arg(q_weight, "q_weight", dt, (D,), dev)
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty_like(seq_lens)
+        new = new_seq_lens.data_ptr()
+    else:
+        new = _arg(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev)
+    code = lib().tv_kv_append_norm(qp, q_stride, qw, qo, out_stride, Hq, k, k_stride,
+                                   None if k_weight is None else _arg(k_weight, "k_weight", dt, (D,), dev), v, v_stride,
+                                   eps, None if cu_new is None else _arg(cu_new, "cu_new", torch.int32, (B + 1,), dev), T,
+                                   kc, vc, num_blocks, bs, table, width, lens, new, cs, max_pos, rot,
+                                   1 if interleaved else 0, B, Hkv, D, TV_F32 if dt is torch.float32 else TV_BF16,
+                                   _arg_status(status, dev), st)
+    if code:
+        _check("tv_kv_append_norm", code)
+    return q_out, new_seq_lens
+
+
 def tv_decode_attn_workspace_size(Hq, Hkv, head_dim, dtype, num_ctas=0):
     out = ctypes.c_size_t(0)
     _check("tv_decode_attn_workspace_size",
@@ -651,6 +710,57 @@ def tv_decode_attn(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, so
     return out
 
 
+def tv_chunk_attn_workspace_size(Hq, Hkv, head_dim, dtype, num_ctas=0):
+    out = ctypes.c_size_t(0)
+    _check("tv_chunk_attn_workspace_size",
+           lib().tv_chunk_attn_workspace_size(Hq, Hkv, head_dim, _code(dtype), num_ctas, ctypes.addressof(out)))
+    return out.value
+
+
+def tv_chunk_attn(q, k_cache, v_cache, block_table, seq_lens, *, cu_new=None, scale=None, softcap=0.0, window=0, n_sink=0,
+                  slopes=None, out=None, lse=None, workspace=None, num_ctas=0, flags=0, status=None, stream=None):
+    """Causal attention of each request's chunk of new tokens, the last of its
+    seq_lens, over the paged cache (which holds their K/V already); returns out
+    [T, Hq, D].  q [T, Hq, D] may be strided between tokens; cu_new int32 [B + 1]:
+    packed offsets, None: T / B tokens each; softcap, window / n_sink and slopes
+    as in the header; lse float32 [T, Hq] is filled when given.  Rows of no
+    request are left as they are (undefined in an out that the call makes)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tv_chunk_attn(q, k_cache, v_cache, block_table, seq_lens, cu_new=cu_new, scale=scale, softcap=softcap,
+                                 window=window, n_sink=n_sink, slopes=slopes, out=out, lse=lse, workspace=workspace,
+                                 num_ctas=num_ctas, flags=flags, status=status)
+    if (window | n_sink | num_ctas | flags) >> 31 not in (0, -1):  # ctypes would take them modulo 2^32
+        raise ValueError(f"window {window}, n_sink {n_sink}, num_ctas {num_ctas} or flags {flags} does not fit 32 bits")
+    dev, st = _current()
+    lens, B = _arg_batch(seq_lens, dev)
+    kc, vc, (num_blocks, Hkv, bs, D), dt, table, width = _arg_cache(k_cache, v_cache, block_table, B, dev)
+    T = _rows(q, "q", dev)
+    Hq = q.shape[1]
+    qp, q_stride = _arg_rows(q, "q", dt, (T, Hq, D), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, "out", dt, (T, Hq, D), dev)
+    if workspace is None:
+        # the call clears the counters, the first 16 KiB
+        workspace = torch.empty(tv_chunk_attn_workspace_size(Hq, Hkv, D, dt, num_ctas), dtype=torch.uint8, device=q.device)
+        flags &= ~TV_ATTN_WORKSPACE_ZEROED
+    n_ws = workspace.numel()
+    code = lib().tv_chunk_attn(qp, q_stride, kc, vc, num_blocks, bs, table, width, lens,
+                               None if cu_new is None else _arg(cu_new, "cu_new", torch.int32, (B + 1,), dev), T, B, Hq,
+                               Hkv, D, TV_F32 if dt is torch.float32 else TV_BF16,
+                               1.0 / math.sqrt(D) if scale is None else scale, softcap, window, n_sink,
+                               None if slopes is None else _arg(slopes, "slopes", torch.float32, (Hq,), dev), op,
+                               None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq), dev),
+                               _arg(workspace, "workspace", torch.uint8, (n_ws,), dev), n_ws, num_ctas, flags,
+                               _arg_status(status, dev), st)
+    if code:
+        _check("tv_chunk_attn", code)
+    return out
+
+
 def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entropy=None, top_ids=None,
                       top_logprobs=None, status=None, stream=None):
     """Log probabilities of tokens [B, C] under rows node [B, C] (None: row c) of
@@ -691,3 +801,39 @@ def tv_token_logprobs(logits, tokens, *, node=None, top_k=0, logprob=None, entro
     if code:
         _check("tv_token_logprobs", code)
     return logprob, entropy, top_ids, top_logprobs
+
+
+def tv_token_sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None,
+                    status=None, stream=None):
+    """A token per row of logits [..., V] (float32 or bf16), drawn with u [...]
+    float32 from the row's distribution after temperature, top_k (int32), min_p and
+    top_p, each a tensor of the rows' shape or None; returns tokens int32 [...].
+    probs float32 [..., V] is filled with the processed distributions when given:
+    the p or q rows of tv_tree_accept_sample."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tv_token_sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p,
+                                   tokens=tokens, probs=probs, status=status)
+    dev, st = _current()
+    if not isinstance(logits, torch.Tensor) or logits.dim() < 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        _refuse(logits, "logits", "float32 or bfloat16", (None, None), dev)
+    f32, rows, V = torch.float32, logits.shape[:-1], logits.shape[-1]
+    x = _arg(logits, "logits", logits.dtype, logits.shape, dev)
+
+    def per_row(t, name, dtype):
+        return None if t is None else _arg(t, name, dtype, rows, dev)
+
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        tok = tokens.data_ptr()
+    else:
+        tok = _arg(tokens, "tokens", torch.int32, rows, dev)
+    code = lib().tv_token_sample(x, rows.numel(), V, TV_F32 if logits.dtype is f32 else TV_BF16,
+                                 per_row(temperature, "temperature", f32), per_row(top_k, "top_k", torch.int32),
+                                 per_row(top_p, "top_p", f32), per_row(min_p, "min_p", f32),
+                                 _arg(u, "u", f32, rows, dev), tok,
+                                 None if probs is None else _arg(probs, "probs", f32, logits.shape, dev),
+                                 _arg_status(status, dev), st)
+    if code:
+        _check("tv_token_sample", code)
+    return tokens

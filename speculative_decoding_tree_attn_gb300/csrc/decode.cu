@@ -38,15 +38,13 @@
 
 #include <cuda_bf16.h>
 
+#include "attn_score.cuh"
 #include "common.h"
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCtas = 4096;
 constexpr int64_t kCounterBytes = 4 * kMaxCtas;  // arrival counters by a cut team's first CTA: first in the workspace
-constexpr float kNoScore = -FLT_MAX;  // maximum of no scores, and of -inf alone: finite, so that -inf weighs 0 against it
 constexpr int kOneStep = 24;  // pieces that are joined at once
 constexpr int kZeros = -1;    // cache row of a key that is not read
 constexpr int kNoGroup = -2;  // of a warp without a group in the tile
@@ -90,22 +88,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// What a row is multiplied with: 1 over its weights' sum, which is 1 at least where there are any.  Without (no visible
-// key, or only scores of -inf) the row is zero, and its m + log2 of the sum is -inf by itself; NaN outputs stay NaN.
-__device__ __forceinline__ float inverse(float sum) { return 1.f / fmaxf(sum, FLT_MIN); }
-
 // A sum against m as one against top.
 __device__ __forceinline__ float scaled(float x, float m, float top) { return x * exp2_approx(m - top); }
 
@@ -177,50 +159,6 @@ __device__ __forceinline__ int cta_start(int c, int T, int P) {  // c T / P in 3
 }
 __device__ __forceinline__ int cta_of(int t, int T, int P) { return (int)((((int64_t)t + 1) * P - 1) / T); }
 
-// Score of one (head, key) in the log2 domain from its raw product.
-struct Scorer {
-  float mul, cap2, cap_mul;  // mul: scale log2 e;  cap2: softcap log2 e, 0 without
-  __device__ __forceinline__ explicit Scorer(const DecodeParams& p)
-      : mul(p.scale * kLog2e), cap2(p.softcap * kLog2e), cap_mul(0.f) {
-    // a finite factor for the smallest caps too: 0 has to stay 0
-    if (p.softcap > 0.f) cap_mul = fmaxf(fminf(p.scale / p.softcap, FLT_MAX), -FLT_MAX);
-  }
-  // tanh y within 6 2^-24 of itself: up to 1.25 the seventh convergent of Lambert's continued fraction
-  // y / (1 + y^2 / (3 + y^2 / (5 + ..))), beyond 1 - 2 / (1 + e^2y), which loses its last bits only for small y.
-  // (Both forms for a warp only where one of its scores needs the second.)
-  template <int N>
-  __device__ __forceinline__ void operator()(float (&x)[N]) const {
-    if (cap2 > 0.f) {
-      float z[N], most = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i] *= cap_mul;
-        z[i] = x[i] * x[i];
-        most = fmaxf(most, z[i]);
-      }
-      const bool far = __any_sync(0xffffffffu, most > 1.5625f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float n = fmaf(fmaf(z[i] + 378.f, z[i], 17325.f), z[i], 135135.f);
-        const float d = fmaf(fmaf(fmaf(28.f, z[i], 3150.f), z[i], 62370.f), z[i], 135135.f);
-        float t = x[i] * (n * rcp_approx(d));
-        if (far && !(z[i] <= 1.5625f)) t = 1.f - 2.f * rcp_approx(1.f + exp2_approx(x[i] * (2.f * kLog2e)));
-        x[i] = cap2 * t;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] *= mul;
-    }
-  }
-};
-
-// A head's bias in the log2 domain, held within float32: the last key's distance is 0 and has to give 0.
-__device__ __forceinline__ float slope_of(const DecodeParams& p, int head) {
-  float x = __ldg(p.slopes + head) * kLog2e;
-  asm("{\n\tmin.NaN.f32 %0, %0, 0f7f7fffff;\n\tmax.NaN.f32 %0, %0, 0fff7fffff;\n\t}" : "+f"(x));
-  return x;
-}
-
 // Position of 16-byte unit u of a head's row in the merge buffer: spreads the
 // heads that a warp writes at once over the banks.
 __device__ __forceinline__ int merge_unit(int head, int u) {
@@ -290,7 +228,7 @@ struct Bf16Math {
         const int hc = 8 * n + 2 * t + e;
         m[n][e] = kNoScore;
         l[n][e] = 0.f;
-        slope[n][e] = p.slopes && hc < nh ? slope_of(p, h0 + hc) : 0.f;
+        slope[n][e] = p.slopes && hc < nh ? slope_of(p.slopes, h0 + hc) : 0.f;
       }
     }
   }
@@ -526,7 +464,7 @@ struct F32Math {
       }
     m = kNoScore;
     l = 0.f;
-    slope = p.slopes && lane % NH < nh ? slope_of(p, h0 + lane % NH) : 0.f;
+    slope = p.slopes && lane % NH < nh ? slope_of(p.slopes, h0 + lane % NH) : 0.f;
   }
 
   __device__ __forceinline__ void group(const DecodeParams& p, const Scorer& score, const Span& sp, int key, uint32_t kt,
@@ -1284,8 +1222,7 @@ extern "C" int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cac
   if (int rc = check_shape("tv_decode_attn", Hq, Hkv, head_dim, dtype, num_ctas)) return rc;
   if (B < 0 || num_blocks < 1 || block_size < 1 || max_blocks < 1 || window < 0 || n_sink < 0)
     return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: bad sizes");
-  // scores are kept in the log2 domain: their factors are held there too
-  if (!std::isfinite(scale * kLog2e) || !(softcap >= 0.f) || !std::isfinite(softcap * kLog2e))
+  if (!factors_fit(scale, softcap))
     return tv::fail(TV_ERR_INVALID_ARG,
                     "tv_decode_attn: scale must be finite, softcap finite and not negative, both within 2.3e38");
   if (flags & ~TV_ATTN_WORKSPACE_ZEROED) return tv::fail(TV_ERR_INVALID_ARG, "tv_decode_attn: unknown flags %d", flags);
@@ -1320,9 +1257,7 @@ extern "C" int tv_decode_attn(const void* q, int64_t q_stride, const void* k_cac
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.scale = scale;
-  // tanh x is x to float32 for |x| < 2^-12: a factor below the normal numbers would lose bits of it, and caps nothing
-  // as long as q . k is below 2^114
-  p.softcap = softcap > 0.f && std::fabs(scale / softcap) < FLT_MIN ? 0.f : softcap;
+  p.softcap = cap_that_matters(scale, softcap);
   p.window = window;
   p.n_sink = n_sink;
   p.slopes = slopes;

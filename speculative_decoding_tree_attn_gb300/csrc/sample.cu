@@ -1,0 +1,685 @@
+// Sampling a token from a row of logits with temperature, top-k, min-p and
+// top-p, from a given uniform number.
+//
+// With m = max x and w_i = e^((x_i - m) / T): of the top_k largest logits (equal
+// ones by index), those with w_i >= min_p, and of these in descending order the
+// shortest run that holds top_p of their sum, are kept; the token is the first
+// index whose running sum over the kept ones exceeds u times their total W, and
+// w_i / W are the probabilities.  "Implement the lossless speculative sampling
+// verifier ...", "Details that matter in review": acceptance has to be given the
+// distributions that tokens are drawn from, so both come out of one call.
+//
+// A draw among V tokens goes wrong wherever a running sum is off by as much as u
+// W is away from it, so sums in float32 would give another token in one of a
+// hundred draws over 128,000.  Weights are therefore whole numbers, w 2^43 to
+// about 2^-39 of itself, and their sums exact and independent of order:
+//   w = 2^(n / 64) e^t,  (x - m) log2 e / T = n / 64 + r in two floats, t = r ln 2,
+// with the 64 powers from a table and e^t by its series (Tang's table-driven
+// exponential, ACM TOMS 15, 1989); |t| < 0.0055, so that only its first term needs
+// two floats.
+//
+// A limit is found by a histogram of the weights' logarithms (128 bins to a factor
+// of 2): counts and 14-bit masses by bin tell the bin that the limit is in, exact
+// sums confirm it, and the few elements of that bin are ranked by comparing each
+// with each.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "common.h"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 4096, kPerOctave = 128;
+constexpr int kList = 512;       // elements that are ranked by comparing
+constexpr int kChunk = 256;      // elements whose kept mass is one number
+constexpr int kMaxV = 1 << 20;   // sums stay below 2^64
+constexpr int kMaxCluster = 8;
+constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236e-09f;  // ln 2 in two floats
+constexpr float kCold = 0x1p-60f;  // a temperature below counts as 0, one above the inverse as that
+
+// 2^(j / 64 + 43), rounded
+__constant__ unsigned long long kPowers[64] = {
+    8796093022208ull, 8891876195264ull, 8988702378691ull, 9086582930126ull,
+    9185529330885ull, 9285553187305ull, 9386666232110ull, 9488880325783ull,
+    9592207457961ull, 9696659748838ull, 9802249450589ull, 9908988948806ull,
+    10016890763953ull, 10125967552830ull, 10236232110063ull, 10347697369602ull,
+    10460376406236ull, 10574282437131ull, 10689428823381ull, 10805829071568ull,
+    10923496835354ull, 11042445917079ull, 11162690269381ull, 11284243996830ull,
+    11407121357589ull, 11531336765078ull, 11656904789672ull, 11783840160404ull,
+    11912157766698ull, 12041872660113ull, 12173000056107ull, 12305555335825ull,
+    12439554047902ull, 12575011910285ull, 12711944812080ull, 12850368815412ull,
+    12990300157313ull, 13131755251623ull, 13274750690919ull, 13419303248457ull,
+    13565429880144ull, 13713147726524ull, 13862474114787ull, 14013426560807ull,
+    14166022771192ull, 14320280645363ull, 14476218277651ull, 14633853959423ull,
+    14793206181226ull, 14954293634955ull, 15117135216047ull, 15281750025697ull,
+    15448157373097ull, 15616376777705ull, 15786427971528ull, 15958330901445ull,
+    16132105731538ull, 16307772845465ull, 16485352848846ull, 16664866571680ull,
+    16846335070792ull, 17029779632301ull, 17215221774115ull, 17402683248456ull};
+
+struct SampleParams {
+  const char* logits;
+  int64_t R;
+  int V;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* u;
+  int32_t* tokens;
+  float* probs;
+  int32_t* status;
+  int slice;  // elements of a CTA, a multiple of kChunk
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Order of elements as one whole number: the value's place, then the lower index first.
+__device__ __forceinline__ uint64_t place(float x, int i) {
+  const uint32_t bits = __float_as_uint(x + 0.f);  // -0 is 0
+  const uint32_t key = bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+  return (uint64_t)key << 32 | (uint32_t)~i;
+}
+
+struct Scale {
+  float m, c1, c2;  // log2 e / T in two floats
+
+  // (x - m) log2 e / T; the first float alone falls with x
+  __device__ __forceinline__ float log2w(float x) const { return (x - m) * c1; }
+
+  // w = mantissa 2^(-43 - s) up to 2^-39 of it, the mantissa within [2^43, 2^44); y > -126
+  __device__ __forceinline__ uint64_t mantissa(float x, const unsigned long long* powers, int& s) const {
+    const float dh = x - m, back = dh - x;
+    const float dl = (x - (dh - back)) - (m + back);
+    const float yh = dh * c1;
+    const float yl = fmaf(dh, c1, -yh) + fmaf(dh, c2, dl * c1);
+    const float n = rintf(yh * 64.f);
+    const float rh = fmaf(n, -0x1p-6f, yh);  // exact
+    const float th = rh * kLn2Hi;
+    const float tl = fmaf(rh, kLn2Hi, -th) + fmaf(rh, kLn2Lo, yl * kLn2Hi);
+    const float t = th + tl;
+    const float q = t * t * fmaf(t, fmaf(t, fmaf(t, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
+    const int e = __float2int_rn(th * 0x1p38f) + __float2int_rn((tl + q) * 0x1p38f);  // (e^t - 1) 2^38
+    const int ni = (int)n;
+    const unsigned long long p = powers[ni & 63];
+    s = -(ni >> 6);
+    return p + (uint64_t)(((int64_t)(p >> 12) * e) >> 26);
+  }
+  // rint(w 2^43)
+  __device__ __forceinline__ uint64_t weight(float x, const unsigned long long* powers) const {
+    if (!(log2w(x) > -45.f)) return 0;
+    int s;
+    const uint64_t w = mantissa(x, powers, s);
+    return s == 0 ? w : ((w >> (s - 1)) + 1) >> 1;
+  }
+  // w, to float32
+  __device__ __forceinline__ float probability(float x, const unsigned long long* powers) const {
+    if (!(log2w(x) > -126.f)) return 0.f;
+    int s;
+    const uint64_t w = mantissa(x, powers, s);
+    return (float)w * 0x1p-43f * __uint_as_float((uint32_t)(127 - s) << 23);
+  }
+};
+
+__device__ __forceinline__ int bin_of(float y) { return min(kBins - 1, (int)(y * -(float)kPerOctave)); }
+
+struct Shared {
+  unsigned long long powers[64];
+  unsigned long long warp_sums[kWarps][2];
+  unsigned long long totals[2][2];  // exchanged with the cluster's CTAs, in turns
+  uint32_t count[kBins], mass[kBins];
+  unsigned long long chunk[kMaxV / kMaxCluster / kChunk + 1];  // kept mass
+  unsigned long long list_place[kList], list_weight[kList];
+  unsigned long long all_place[kList], all_weight[kList];
+  uint32_t scan_count[kThreads], listed;
+  unsigned long long scan_mass[kThreads];
+  unsigned long long limit;
+  int bin;
+};
+
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// floor(x u), x < 2^64, u in [0, 1)
+__device__ __forceinline__ unsigned long long times(unsigned long long x, float u) {
+  if (!(u > 0.f)) return 0;
+  int e;
+  const unsigned long long f = (unsigned long long)(frexpf(u, &e) * 0x1p24f);  // u = f 2^(e - 24)
+  const unsigned long long lo = x * f, hi = __umul64hi(x, f);
+  const int s = 24 - e;  // 24 ..
+  if (s >= 64) return s >= 128 ? 0 : hi >> (s - 64);
+  return hi << (64 - s) | lo >> s;
+}
+// ceil(x u)
+__device__ __forceinline__ unsigned long long times_up(unsigned long long x, float u) {
+  const unsigned long long y = times(x, u);
+  // x u is whole only if nothing was cut off: u = f 2^(e - 24) cuts the low bits of x f
+  int e;
+  const unsigned long long f = (unsigned long long)(frexpf(u, &e) * 0x1p24f);
+  const int s = 24 - e;
+  if (s >= 64) return y + 1;
+  return y + ((x * f & ((1ull << s) - 1)) != 0);
+}
+
+template <typename T>
+struct Row {
+  const SampleParams& p;
+  Shared& sh;
+  cg::cluster_group cluster;
+  int rank, turn;
+  const T* row;   // of the logits
+  int v0, v1;     // this CTA's elements
+  bool wide;      // rows of whole vectors
+
+  // Sums (or maxima) of two numbers over the cluster; before0/1: those of the CTAs before this one.
+  template <bool kMax>
+  __device__ void reduce(unsigned long long& a, unsigned long long& b, unsigned long long* before = nullptr) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    a = kMax ? warp_max(a) : warp_sum(a);
+    b = kMax ? warp_max(b) : warp_sum(b);
+    __syncthreads();
+    if (lane == 0) sh.warp_sums[warp][0] = a, sh.warp_sums[warp][1] = b;
+    __syncthreads();
+    if (warp == 0) {
+      a = lane < kWarps ? sh.warp_sums[lane][0] : 0;
+      b = lane < kWarps ? sh.warp_sums[lane][1] : 0;
+      a = kMax ? warp_max(a) : warp_sum(a);
+      b = kMax ? warp_max(b) : warp_sum(b);
+      if (lane == 0) sh.totals[turn][0] = a, sh.totals[turn][1] = b;
+    }
+    cluster.sync();
+    a = b = 0;
+    const int n = (int)cluster.num_blocks();
+    for (int r = 0; r < n; ++r) {
+      const unsigned long long* t = cluster.map_shared_rank(&sh.totals[turn][0], r);
+      if (before && r == rank) *before = a;
+      a = kMax ? max(a, t[0]) : a + t[0];
+      b = kMax ? max(b, t[1]) : b + t[1];
+    }
+    turn ^= 1;
+  }
+
+  // Calls f(x, index) for this CTA's elements, each thread's in ascending order.  A warp's 256 elements of one turn lie
+  // together: thread l has the 8 from 8 l on.
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int i = v0 + threadIdx.x * 8; i < v1; i += kThreads * 8) {
+      float x[8];
+      load(i, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + k < v1) f(x[k], i + k);
+    }
+  }
+  __device__ __forceinline__ void load(int i, float (&x)[8]) const {
+    if (wide && i + 8 <= v1) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(row + i)), b = __ldg(reinterpret_cast<const float4*>(row + i) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+      } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + i));
+        const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[2 * k] = __uint_as_float(v[k] << 16), x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = i + k < v1 ? (float)row[i + k] : -INFINITY;
+    }
+  }
+
+  // Bins of the whole row from those of the cluster's CTAs: every CTA adds up all of them.
+  __device__ void share_bins() {
+    cluster.sync();
+    const int n = (int)cluster.num_blocks();
+    if (n == 1) return;
+    constexpr int kPer = kBins / kThreads;
+    uint32_t c[kPer] = {}, w[kPer] = {};
+    for (int r = 0; r < n; ++r) {
+      const uint32_t* rc = cluster.map_shared_rank(sh.count, r);
+      const uint32_t* rw = cluster.map_shared_rank(sh.mass, r);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) c[k] += rc[threadIdx.x + k * kThreads], w[k] += rw[threadIdx.x + k * kThreads] >> 3;
+    }
+    cluster.sync();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) sh.count[threadIdx.x + k * kThreads] = c[k], sh.mass[threadIdx.x + k * kThreads] = w[k];
+    __syncthreads();
+  }
+
+  // First bin at which the running count (or mass, in the weights' unit) reaches target; -1 without one.
+  template <bool kMass>
+  __device__ int find_bin(unsigned long long target, int last_bin, int unit_bits) {
+    constexpr int kPer = kBins / kThreads;
+    auto of = [&](int b) -> unsigned long long {
+      if (b > last_bin) return 0;
+      if (!kMass) return sh.count[b];
+      return (unsigned long long)sh.mass[b] << unit_bits >> (b / kPerOctave);
+    };
+    unsigned long long mine = 0;
+    for (int k = 0; k < kPer; ++k) mine += of(threadIdx.x * kPer + k);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    unsigned long long run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp_sums[warp][0] = run;
+    if (threadIdx.x == 0) sh.bin = -1;
+    __syncthreads();
+    run -= mine;
+    for (int k = 0; k < warp; ++k) run += sh.warp_sums[k][0];
+    if (run < target && run + mine >= target) {
+      for (int k = 0; k < kPer; ++k) {
+        const unsigned long long y = of(threadIdx.x * kPer + k);
+        if (run < target && run + y >= target) sh.bin = threadIdx.x * kPer + k;
+        run += y;
+      }
+    }
+    __syncthreads();
+    return sh.bin;
+  }
+  // Next bin in a direction with anything in it
+  __device__ int next_bin(int b, int step, int last_bin) const {
+    for (b += step; b >= 0 && b <= last_bin; b += step)
+      if (sh.count[b]) return b;
+    return -1;
+  }
+
+  // Kept elements of bin `bin` with lo <= place <= hi, which are kList at most, in every CTA's list; their number.
+  template <class Kept>
+  __device__ int gather(const Scale& sc, int bin, unsigned long long lo, unsigned long long hi, Kept kept) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.listed = 0;
+    __syncthreads();
+    each([&](float x, int i) {
+      const float y = sc.log2w(x);
+      if (bin_of(y) != bin || !kept(x, y)) return;
+      const unsigned long long at = place(x, i);
+      if (at < lo || at > hi) return;
+      const uint32_t k = atomicAdd(&sh.listed, 1u);
+      if (k < kList) sh.list_place[k] = at, sh.list_weight[k] = sc.weight(x, sh.powers);
+    });
+    cluster.sync();
+    const int n = (int)cluster.num_blocks();
+    int total = 0;
+    for (int r = 0; r < n; ++r) {
+      const int c = min((int)*cluster.map_shared_rank(&sh.listed, r), kList);
+      for (int k = threadIdx.x; k < c && total + k < kList; k += kThreads) {
+        sh.all_place[total + k] = cluster.map_shared_rank(sh.list_place, r)[k];
+        sh.all_weight[total + k] = cluster.map_shared_rank(sh.list_weight, r)[k];
+      }
+      total += c;
+    }
+    cluster.sync();
+    return min(total, kList);
+  }
+};
+
+// Where the kept elements end.  A limit is the place of the last of them.
+template <typename T>
+__device__ void find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, float least, float floor_y,
+                            unsigned long long& limit) {
+  Shared& sh = r.sh;
+  for (int b = threadIdx.x; b < kBins; b += kThreads) sh.count[b] = 0, sh.mass[b] = 0;
+  __syncthreads();
+  const unsigned long long least_w = (unsigned long long)__float2ull_ru(least * 0x1p43f);
+  // elements that min_p leaves: by their exact weight, which is looked at near the border alone
+  auto kept = [&](float x, float y) { return y >= floor_y && (y >= floor_y + 0x1p-8f || sc.weight(x, sh.powers) >= least_w); };
+  r.each([&](float x, int) {
+    const float y = sc.log2w(x);
+    if (!kept(x, y)) return;
+    const int b = bin_of(y);
+    atomicAdd(&sh.count[b], 1u);
+    atomicAdd(&sh.mass[b], (uint32_t)__float2int_rn(exp2_approx(y + (float)(b / kPerOctave)) * 16384.f));
+  });
+  r.share_bins();
+  const int unit_bits = r.cluster.num_blocks() > 1 ? 29 + 3 : 29;  // 2^-14 in the weights' unit
+
+  int last_bin = kBins - 1;
+  if (top_k > 0) {
+    const int bin = r.template find_bin<false>(top_k, last_bin, 0);
+    if (bin >= 0) {  // else there are no more than top_k
+      unsigned long long above = 0, lo = 0, hi = ~0ull, in_range = sh.count[bin];
+      {
+        unsigned long long a = 0, zero = 0;
+        for (int b = threadIdx.x; b < bin; b += kThreads) a += sh.count[b];
+        // the same in every CTA: no need to ask the others
+        a = warp_sum(a);
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) sh.warp_sums[threadIdx.x / 32][0] = a;
+        __syncthreads();
+        for (int k = 0; k < kWarps; ++k) zero += sh.warp_sums[k][0];
+        above = zero;
+        __syncthreads();
+      }
+      while (in_range > kList) {  // many equal or nearly equal logits: halve the range of places
+        const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+        unsigned long long n = 0, none = 0;
+        r.each([&](float x, int i) {
+          const float y = sc.log2w(x);
+          if (bin_of(y) != bin || !kept(x, y)) return;
+          const unsigned long long at = place(x, i);
+          n += at >= mid && at <= hi;
+        });
+        r.template reduce<false>(n, none);
+        if (above + n >= (unsigned)top_k) lo = mid, in_range = n;
+        else hi = mid - 1, above += n, in_range -= n;
+      }
+      const int n = r.gather(sc, bin, lo, hi, kept);
+      for (int k = threadIdx.x; k < n; k += kThreads) {
+        unsigned long long rank = above;
+        for (int j = 0; j < n; ++j) rank += sh.all_place[j] > sh.all_place[k];
+        if (rank == (unsigned)top_k - 1) sh.limit = sh.all_place[k];
+      }
+      __syncthreads();
+      limit = sh.limit;
+      last_bin = bin;
+      __syncthreads();
+    }
+  }
+  if (!(top_p < 1.f)) return;
+
+  // the bin by its mass, confirmed by exact sums
+  unsigned long long about = 0;
+  {
+    unsigned long long a = 0;
+    for (int b = threadIdx.x; b <= last_bin; b += kThreads) a += (unsigned long long)sh.mass[b] << unit_bits >> (b / kPerOctave);
+    a = warp_sum(a);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh.warp_sums[threadIdx.x / 32][0] = a;
+    __syncthreads();
+    for (int k = 0; k < kWarps; ++k) about += sh.warp_sums[k][0];
+    __syncthreads();
+  }
+  int bin = r.template find_bin<true>(max(times_up(about, top_p), 1ull), last_bin, unit_bits);
+  if (bin < 0) bin = r.next_bin(last_bin + 1, -1, last_bin);
+  unsigned long long target = 0, above = 0, inside = 0;
+  for (bool first = true;; first = false) {
+    // mass above the bin, in it, and (the first time) behind it
+    unsigned long long a = 0, in = 0, behind = 0;
+    r.each([&](float x, int i) {
+      const float y = sc.log2w(x);
+      if (!kept(x, y) || place(x, i) < limit) return;
+      const int b = bin_of(y);
+      if (b > bin && !first) return;
+      const unsigned long long w = sc.weight(x, sh.powers);
+      if (b < bin) a += w;
+      else if (b == bin) in += w;
+      else behind += w;
+    });
+    r.template reduce<false>(a, in);
+    above = a, inside = in;
+    if (first) {
+      unsigned long long none = 0;
+      r.template reduce<false>(behind, none);
+      target = top_p > 0.f ? max(times_up(above + inside + behind, top_p), 1ull) : 1ull;
+    }
+    if (above >= target) {
+      const int b = r.next_bin(bin, -1, last_bin);
+      if (b < 0) break;
+      bin = b;
+    } else if (above + inside < target) {
+      const int b = r.next_bin(bin, 1, last_bin);
+      if (b < 0) return;  // all of them
+      bin = b;
+    } else {
+      break;
+    }
+  }
+  // within the bin
+  unsigned long long lo = limit, hi = ~0ull, in_range;
+  {
+    unsigned long long n = 0, none = 0;
+    r.each([&](float x, int i) {
+      const float y = sc.log2w(x);
+      if (bin_of(y) != bin || !kept(x, y)) return;
+      n += place(x, i) >= lo;
+    });
+    r.template reduce<false>(n, none);
+    in_range = n;
+  }
+  while (in_range > kList) {
+    const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+    unsigned long long n = 0, w = 0;
+    r.each([&](float x, int i) {
+      const float y = sc.log2w(x);
+      if (bin_of(y) != bin || !kept(x, y)) return;
+      const unsigned long long at = place(x, i);
+      if (at >= mid && at <= hi) n += 1, w += sc.weight(x, sh.powers);
+    });
+    r.template reduce<false>(n, w);
+    if (above + w >= target) lo = mid, in_range = n;
+    else hi = mid - 1, above += w, in_range -= n;
+  }
+  const int n = r.gather(sc, bin, lo, hi, kept);
+  if (threadIdx.x == 0) sh.limit = limit;
+  __syncthreads();
+  for (int k = threadIdx.x; k < n; k += kThreads) {
+    unsigned long long before = above;
+    for (int j = 0; j < n; ++j)
+      if (sh.all_place[j] > sh.all_place[k]) before += sh.all_weight[j];
+    if (before < target && before + sh.all_weight[k] >= target) sh.limit = sh.all_place[k];
+  }
+  __syncthreads();
+  limit = sh.limit;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_constant__ SampleParams p) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t at = blockIdx.x / C;
+  Row<T> r{p, sh, cluster, rank, 0};
+  r.row = reinterpret_cast<const T*>(p.logits) + at * p.V;
+  r.v0 = min(p.V, rank * p.slice);
+  r.v1 = min(p.V, (rank + 1) * p.slice);
+  r.wide = (uint64_t)p.V * sizeof(T) % 16 == 0;
+  if (threadIdx.x < 64) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
+
+  float temp = p.temperature ? p.temperature[at] : 1.f;
+  int top_k = p.top_k ? p.top_k[at] : 0;
+  float top_p = p.top_p ? p.top_p[at] : 1.f;
+  const float min_p = p.min_p ? p.min_p[at] : 0.f;
+  float u = p.u[at];
+  const bool bad_temp = !(temp >= 0.f && temp < INFINITY);
+  if (!(top_p > 0.f)) top_p = top_p <= 0.f ? 0.f : 1.f;  // NaN: no limit
+  const float least = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
+
+  // the largest logit's place, and whether the row has a distribution
+  unsigned long long best = 0, odd = 0;
+  r.each([&](float x, int i) {
+    if (!(x < INFINITY)) odd = 1;
+    else best = max(best, (unsigned long long)place(x, i));
+  });
+  r.template reduce<true>(best, odd);
+  const int best_i = (int)~(uint32_t)best;
+  const uint32_t key = (uint32_t)(best >> 32);
+  const float m = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+  float* probs = p.probs ? p.probs + at * p.V : nullptr;
+  if (odd || bad_temp || !(m > -INFINITY)) {
+    if (rank == 0 && threadIdx.x == 0) {
+      p.tokens[at] = -1;
+      if (bad_temp && p.status) atomicOr(p.status, TV_DEV_BAD_PARAM);
+    }
+    if (probs)
+      for (int i = r.v0 + threadIdx.x; i < r.v1; i += kThreads) probs[i] = NAN;
+  } else if (temp < kCold || top_k == 1) {  // the likeliest alone
+    if (rank == 0 && threadIdx.x == 0) p.tokens[at] = best_i;
+    if (probs)
+      for (int i = r.v0 + threadIdx.x; i < r.v1; i += kThreads) probs[i] = i == best_i ? 1.f : 0.f;
+  } else {
+    Scale sc;
+    const double c = 1.4426950408889634074 / (double)fminf(temp, 1.f / kCold);
+    sc.m = m;
+    sc.c1 = (float)c;
+    sc.c2 = (float)(c - (double)sc.c1);
+    if (top_k < 0 || top_k >= p.V) top_k = 0;
+    const float floor_y = least > 0.f ? log2f(least) - 0x1p-9f : -FLT_MAX;
+    unsigned long long limit = 0;
+    const unsigned long long least_w = (unsigned long long)__float2ull_ru(least * 0x1p43f);
+    if (top_k > 0 || top_p < 1.f) find_limits(r, sc, top_k, top_p, least, floor_y, limit);
+
+    // kept mass of every 256 elements
+    auto kept_weight = [&](float x, int i) -> unsigned long long {
+      if (!(sc.log2w(x) >= floor_y) || place(x, i) < limit) return 0;
+      const unsigned long long w = sc.weight(x, sh.powers);
+      return w >= least_w ? w : 0;
+    };
+    unsigned long long total = 0, none = 0, before = 0;
+    const int lane = threadIdx.x % 32;
+    for (int i0 = r.v0 + (threadIdx.x - lane) * 8; i0 < r.v1; i0 += kThreads * 8) {
+      const int i = i0 + lane * 8;
+      unsigned long long w = 0;
+      if (i < r.v1) {
+        float x[8];
+        r.load(i, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k < r.v1) w += kept_weight(x[k], i + k);
+      }
+      total += w;
+      w = warp_sum(w);
+      if (lane == 0) sh.chunk[(i0 - r.v0) / kChunk] = w;
+    }
+    r.template reduce<false>(total, none, &before);
+    // the draw: in the CTA that u W falls into, by one warp
+    const unsigned long long goal = u >= 1.f ? total - 1 : times(total, u);
+    if (threadIdx.x < 32 && goal >= before) {
+      const int chunks = (r.v1 - r.v0 + kChunk - 1) / kChunk;
+      unsigned long long run = before;
+      int hit = -1;
+      for (int c0 = 0; c0 < chunks && hit < 0; c0 += 32) {
+        const unsigned long long w = c0 + lane < chunks ? sh.chunk[c0 + lane] : 0;
+        unsigned long long s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, run + s > goal);
+        if (over) {
+          const int k = __ffs(over) - 1;
+          hit = c0 + k;
+          run += __shfl_sync(0xffffffffu, s - w, k);
+        } else {
+          run += __shfl_sync(0xffffffffu, s, 31);
+        }
+      }
+      if (hit >= 0) {
+        const int i = r.v0 + hit * kChunk + lane * 8;
+        float x[8];
+        unsigned long long w[8], mine = 0;
+        r.load(i, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = i + k < r.v1 ? kept_weight(x[k], i + k) : 0, mine += w[k];
+        unsigned long long s = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, run + s > goal);
+        if (over && lane == __ffs(over) - 1) {
+          run += s - mine;
+          int tok = -1;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            run += w[k];
+            if (tok < 0 && run > goal) tok = i + k;
+          }
+          p.tokens[at] = tok;
+        }
+      }
+    }
+    if (probs) {
+      const float inv = (float)(0x1p43 / (double)total);
+      r.each([&](float x, int i) {
+        const float y = sc.log2w(x);
+        const bool in = y >= floor_y && place(x, i) >= limit && (least_w == 0 || sc.weight(x, sh.powers) >= least_w);
+        probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
+      });
+    }
+  }
+  cluster.sync();  // the others may still read this CTA's numbers
+}
+
+template <typename T>
+int launch_sample(SampleParams p, int sm_count, cudaStream_t stream) {
+  (void)sm_count;
+  int C = 1;
+  while (C < kMaxCluster && (int64_t)p.V > (int64_t)C * 16384) C *= 2;
+  p.slice = (int)(tv::ceil_div(p.V, (int64_t)C * kChunk) * kChunk);
+  const int smem = (int)sizeof(Shared);
+  cudaError_t e = cudaFuncSetAttribute(token_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return tv::cuda_fail(e, "cudaFuncSetAttribute(token_sample_kernel)");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.R * C), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, token_sample_kernel<T>, p);
+  if (e != cudaSuccess) return tv::cuda_fail(e, "token_sample_kernel");
+  return TV_OK;
+}
+
+}  // namespace
+
+extern "C" int tv_token_sample(const void* logits, int64_t R, int32_t V, int32_t dtype, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                               int32_t* tokens, float* probs, int32_t* status, void* stream) {
+  tv::clear_error();
+  if (R < 0 || V < 1) return tv::fail(TV_ERR_INVALID_ARG, "tv_token_sample: bad sizes");
+  if (dtype != TV_F32 && dtype != TV_BF16) return tv::fail(TV_ERR_UNSUPPORTED, "tv_token_sample: dtype %d", dtype);
+  if (V > kMaxV) return tv::fail(TV_ERR_UNSUPPORTED, "tv_token_sample: V %d exceeds %d", V, kMaxV);
+  if (R > INT32_MAX / kMaxCluster) return tv::fail(TV_ERR_UNSUPPORTED, "tv_token_sample: more than 2^28 rows");
+  if (R == 0) return TV_OK;
+  if (!logits || !u || !tokens) return tv::fail(TV_ERR_INVALID_ARG, "tv_token_sample: null pointer");
+  if ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(probs)) & 15)
+    return tv::fail(TV_ERR_INVALID_ARG, "tv_token_sample: logits and probs must be 16-byte aligned");
+  tv::DeviceInfo dev;
+  if (int rc = tv::current_device_info(&dev)) return rc;
+  SampleParams p{};
+  p.logits = static_cast<const char*>(logits);
+  p.R = R;
+  p.V = V;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.u = u;
+  p.tokens = tokens;
+  p.probs = probs;
+  p.status = status;
+  cudaStream_t s = (cudaStream_t)stream;
+  return dtype == TV_BF16 ? launch_sample<__nv_bfloat16>(p, dev.sm_count, s) : launch_sample<float>(p, dev.sm_count, s);
+}
