@@ -261,6 +261,16 @@ int check_shape(const char* fn, int32_t Hq, int32_t Hkv, int32_t head_dim, int32
   return TV_OK;
 }
 
+// CTAs of the tensor-core kernel's grid
+int grid_of(int32_t num_ctas, int* ctas) {
+  *ctas = num_ctas;
+  if (num_ctas > 0) return TV_OK;
+  tv::DeviceInfo dev;
+  if (int rc = tv::current_device_info(&dev)) return rc;
+  *ctas = dev.sm_count;
+  return TV_OK;
+}
+
 }  // namespace
 
 extern "C" int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t dtype, int32_t num_ctas,
@@ -269,6 +279,10 @@ extern "C" int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t hea
   if (!bytes) return tv::fail(TV_ERR_INVALID_ARG, "tv_chunk_attn_workspace_size: null pointer");
   if (int rc = check_shape("tv_chunk_attn_workspace_size", Hq, Hkv, head_dim, dtype, num_ctas)) return rc;
   *bytes = kCounterBytes;
+  if (dtype != TV_BF16 || head_dim == 256) return TV_OK;  // never the tensor-core kernel
+  int ctas = 0;
+  if (int rc = grid_of(num_ctas, &ctas)) return rc;
+  *bytes += tv::chunk_tc_workspace(head_dim, ctas);
   return TV_OK;
 }
 
@@ -305,7 +319,6 @@ extern "C" int tv_chunk_attn(const void* q, int64_t q_stride, const void* k_cach
   if ((int64_t)T + B >= INT32_MAX)
     return tv::fail(TV_ERR_UNSUPPORTED, "tv_chunk_attn: tokens and requests exceed 2^31");
   cudaStream_t st = (cudaStream_t)stream;
-  if (!(flags & TV_ATTN_WORKSPACE_ZEROED)) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
   ChunkParams p{};
   p.q = static_cast<const char*>(q);
   p.q_stride = T > 1 ? q_stride * e : 0;
@@ -330,5 +343,19 @@ extern "C" int tv_chunk_attn(const void* q, int64_t q_stride, const void* k_cach
   p.out = static_cast<char*>(out);
   p.lse = lse;
   p.status = status;
+  if ((flags & 3) != TV_ATTN_SIMT) {
+    tv::DeviceInfo dev;
+    if (int rc = tv::current_device_info(&dev)) return rc;
+    const char* why = tv::chunk_tc_unsupported(dev, p, dtype, head_dim);
+    if (!why) {
+      if (int rc = grid_of(num_ctas, &p.ctas)) return rc;
+      p.arrive = static_cast<uint32_t*>(workspace);
+      p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+      p.part_ml = p.part_o + (int64_t)p.ctas * 2 * 256 * head_dim;
+      if (!(flags & TV_ATTN_WORKSPACE_ZEROED)) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
+      return tv::launch_chunk_tc(p, head_dim, st);
+    }
+    if ((flags & 3) == TV_ATTN_TCGEN05) return tv::fail(TV_ERR_UNSUPPORTED, "tv_chunk_attn: no tcgen05 kernel: %s", why);
+  }
   return dtype == TV_BF16 ? dispatch_simt<__nv_bfloat16>(p, head_dim, st) : dispatch_simt<float>(p, head_dim, st);
 }

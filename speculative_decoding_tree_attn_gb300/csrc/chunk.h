@@ -60,7 +60,7 @@ __device__ __forceinline__ bool chunk_of(const ChunkParams& p, int b, ChunkOf& c
 #endif
 
 // The tcgen05 kernel: why it cannot run a shape (nullptr: it can), its workspace, its launch.
-const char* chunk_tc_unsupported(const DeviceInfo& dev, int dtype, int head_dim, int G, int block_size);
+const char* chunk_tc_unsupported(const DeviceInfo& dev, const ChunkParams& p, int dtype, int head_dim);
 size_t chunk_tc_workspace(int head_dim, int ctas);
 int launch_chunk_tc(const ChunkParams& p, int head_dim, cudaStream_t stream);
 

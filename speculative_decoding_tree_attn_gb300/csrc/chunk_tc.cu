@@ -1,0 +1,914 @@
+// Attention of a chunk of new tokens over the paged cache on the
+// 5th-generation tensor cores (tcgen05 + TMEM + TMA); chunk.cu has the
+// definition.
+//
+// * Rows: the G query heads of one KV head and floor(128 / G) tokens fill a
+//   128-row M tile (row = token * G + head, so rows of one token are
+//   neighbours); a unit is two M tiles of one (request, KV head), so a K/V byte
+//   that reaches the SM feeds 256 rows.  Q comes by one TMA box per 64 columns.
+// * Keys: tiles of 128, K and V in a ring of 32 KB slots of their own, by TMA
+//   boxes of (a power of two of) rows within a cache block.  Boxes without a
+//   key that the unit sees, and bad blocks, are sent out of bounds: zeros.
+// * S_m = Q_m K^T (128 x 128, both operands from shared memory) and O_m += P_m V
+//   (P_m from TMEM, bf16, over S_m's columns) are issued by one thread per M
+//   tile: while the softmax of one M tile runs, the products of the other do.
+//   S_0 128 | S_1 128 | O_0 128 | O_1 128 columns fill the TMEM.
+// * Softmax: a thread per row; the running maximum may lag by 2^8, so that O is
+//   rescaled in TMEM only when it grows by more.  Weights are rounded to bf16 for
+//   P V (an operand of kind::f16 holds no more; half a step, 2^-9 of a weight on
+//   average, against the 2^-9 that rounding the output takes), their sum is not.
+// * Work: the units' tiles (with a few virtual ones for a unit's fixed cost) lie
+//   end to end and each CTA of a persistent grid takes an equal run.  The sums
+//   over a request's units have a closed form (floor sums), so a CTA finds its
+//   run from lengths and offsets alone.  A unit cut by a run's end leaves
+//   (max, sum, output) of each piece in the workspace and the CTA whose piece
+//   arrives last joins them in order, so results do not depend on timing.
+//
+// Every mbarrier wait is bounded (2 s); past it the CTA sets TV_DEV_TIMEOUT, lets
+// its products and loads finish, frees its TMEM and returns.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "attn_score.cuh"
+#include "chunk.h"
+#include "tc_ptx.cuh"
+
+namespace tv {
+
+namespace {
+
+constexpr int kBlk = 128;          // keys of a tile
+constexpr int kHalf = kBlk * 128;  // bytes of 128 rows x 64 columns
+constexpr int kThreads = 512;
+constexpr unsigned long long kLimitNs = 2000000000ull;
+constexpr float kLag = 8.f;        // log2 that the reference may stay behind the maximum
+
+template <int D>
+struct Cfg {
+  static constexpr int kTile = D / 64 * kHalf;     // bytes of a K, V or Q tile
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kOffRing = 2 * kTile;       // behind Q_0, Q_1
+  static constexpr int kSmem = kOffRing + kSlots * kTile + 1024;
+};
+static_assert(Cfg<128>::kSmem <= 227 * 1024 - 1024 && Cfg<64>::kSmem <= 227 * 1024 - 1024, "fits beside the barriers");
+
+constexpr uint32_t kColS(int m) { return m * 128; }
+constexpr uint32_t kColO(int m) { return 256 + m * 128; }
+
+struct Bars {
+  uint64_t full[10], empty[10];
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain[2];
+  uint64_t posted, decided;
+  uint32_t tmem;
+  int abort;
+  int last;
+};
+
+struct Maps {
+  CUtensorMap k, v, q;
+};
+
+#ifdef TV_TEST_HOOKS
+// Development builds only: a shorter wait limit, and a ring entry of CTA 0 that is left without its loads.
+__device__ unsigned long long g_chunk_limit_ns = kLimitNs;
+__device__ int g_chunk_withhold = -1;
+__device__ __forceinline__ unsigned long long limit_ns() { return *(volatile unsigned long long*)&g_chunk_limit_ns; }
+__device__ __forceinline__ bool withhold(uint32_t n) { return blockIdx.x == 0 && (int)n == *(volatile int*)&g_chunk_withhold; }
+#else
+__device__ __forceinline__ unsigned long long limit_ns() { return kLimitNs; }
+__device__ __forceinline__ bool withhold(uint32_t) { return false; }
+#endif
+
+// ---------------------------------------------------------------- the plan
+
+// sum over j < n of floor((b + a j) / m), b >= 0: whole parts are summed apart, what is left is counted along the other
+// axis (the steps of Euclid's algorithm on a and m).
+__device__ int64_t floor_sum(int64_t n, int64_t a, int64_t b, int64_t m) {
+  int64_t sum = 0;
+  while (true) {
+    if (a >= m) {
+      sum += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const int64_t top = a * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const int64_t t = a;
+    a = m;
+    m = t;
+  }
+}
+
+// sum over j < n of max(0, floor((b + a j) / 128)), a >= 1
+__device__ int64_t tiles_below(int64_t n, int a, int64_t b) {
+  if (n <= 0) return 0;
+  if (b < 0) {
+    const int64_t skip = (-b + a - 1) / a;
+    if (skip >= n) return 0;
+    n -= skip;
+    b += skip * a;
+  }
+  if ((a & (a - 1)) == 0 && a <= kBlk) {  // steps of a power of two: runs of r equal terms
+    const int r_log = 7 - (31 - __clz(a));
+    auto upto = [&](int64_t x) {  // sum over i < x of floor(i / r)
+      const int64_t q = x >> r_log;
+      return (q * (q - 1) / 2 << r_log) + q * (x - (q << r_log));
+    };
+    const int64_t c = b >> (31 - __clz(a));
+    return upto(c + n) - upto(c);
+  }
+  return floor_sum(n, a, b, kBlk);
+}
+
+// One request's units.
+struct Request {
+  ChunkOf c;
+  int units;   // per KV head
+  int step;    // tokens of a unit
+  int window, sinks;  // sinks: tiles of kept first keys
+
+  __device__ __forceinline__ void set(const ChunkParams& p, int b) {
+    step = 2 * (128 / p.G);
+    chunk_of(p, b, c);
+    units = (c.n + step - 1) / step;
+    window = p.window;
+    sinks = window > 0 ? (int)(((int64_t)p.n_sink + kBlk - 1) / kBlk) : 0;
+  }
+  // Tiles of unit i (one at least): up to its last position, without those between the kept first keys and the window.
+  __device__ __forceinline__ int tiles(int i) const {
+    const int first = c.first + i * step, last = c.first + min((i + 1) * step, c.n) - 1;
+    const int skipped = window > 0 ? max(0, max(0, max(0, first + 1) - window) / kBlk - sinks) : 0;
+    return 1 + max(0, last) / kBlk - skipped;
+  }
+  // Tiles (and virtual ones) of the units before i, i < units
+  __device__ __forceinline__ int64_t before(int i, int cost) const {
+    int64_t n = (int64_t)i * (1 + cost) + tiles_below(i, step, (int64_t)c.first + step - 1);
+    if (window > 0) n -= tiles_below(i, step, (int64_t)c.first + 1 - window - (int64_t)sinks * kBlk);
+    return n;
+  }
+  __device__ __forceinline__ int64_t all(int cost) const {
+    return units ? before(units - 1, cost) + tiles(units - 1) + cost : 0;
+  }
+};
+
+struct Plan {
+  int64_t x0, x1, total;  // this CTA's run of [0, total)
+  int ctas;               // that take part
+  int b, i, kvh;          // the unit that x0 is in
+  int64_t at;             // where it starts
+};
+
+__device__ __forceinline__ int64_t run_start(int64_t c, int64_t total, int64_t ctas) { return c * total / ctas; }
+__device__ __forceinline__ int64_t run_of(int64_t x, int64_t total, int64_t ctas) { return ((x + 1) * ctas - 1) / total; }
+
+// All threads of the CTA.
+__device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan) {
+  __shared__ int64_t sums[kThreads / 32 + 1];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    Request r;
+    r.set(p, b);
+    mine += r.all(cost);
+  }
+  mine *= p.Hkv;
+  int64_t run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += y;
+  }
+  if (lane == 31) sums[warp] = run;
+  if (tid == 0) plan.b = -1;
+  __syncthreads();
+  int64_t total = 0, start = run - mine;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) start += sums[w];
+    total += sums[w];
+  }
+  const int ctas = (int)min((int64_t)p.ctas, max((int64_t)1, total / least));
+  const int c = blockIdx.x;
+  const int64_t x0 = c < ctas ? run_start(c, total, ctas) : total;
+  const int64_t x1 = c < ctas ? run_start(c + 1, total, ctas) : total;
+  if (x0 < x1 && x0 >= start && x0 < start + mine) {  // one thread: its requests hold the run's start
+    int b = b0;
+    Request r;
+    int64_t at = start;
+    for (;; ++b) {
+      r.set(p, b);
+      const int64_t n = r.all(cost) * p.Hkv;
+      if (x0 < at + n) break;
+      at += n;
+    }
+    int lo = 0;  // the last unit that starts at or before x0
+    for (int hi = r.units; hi - lo > 1;) {
+      const int mid = lo + (hi - lo) / 2;
+      if (at + r.before(mid, cost) * p.Hkv <= x0) lo = mid; else hi = mid;
+    }
+    at += r.before(lo, cost) * p.Hkv;
+    const int one = r.tiles(lo) + cost;
+    plan.kvh = (int)((x0 - at) / one);
+    plan.at = at + (int64_t)plan.kvh * one;
+    plan.b = b;
+    plan.i = lo;
+  }
+  if (tid == 0) {
+    plan.x0 = x0;
+    plan.x1 = x1;
+    plan.total = total;
+    plan.ctas = ctas;
+  }
+  __syncthreads();
+}
+
+// A CTA's part of one unit: tiles [a, e) of it.
+struct Piece {
+  int b, kvh, s0;      // packed row of the unit's first token
+  int tokens[2];       // of the M tiles
+  int pos0, last;      // positions of the unit's first and last token
+  int lo;              // first key of the window of the first token
+  int sink;            // keys below it stay visible
+  int lead;            // tiles before the window's
+  int count[2];        // tiles that an M tile's rows see
+  int a, e, tiles;
+  int64_t real;        // where its tiles start in [0, total)
+
+  __device__ __forceinline__ int key(int t) const { return (t < lead ? t : lo / kBlk + t - lead) * kBlk; }
+  // tiles of this part that M tile m computes
+  __device__ __forceinline__ int computed(int m) const { return max(0, min(e, count[m]) - a); }
+  __device__ __forceinline__ bool split() const { return a > 0 || e < tiles; }
+};
+
+struct Walk {
+  const ChunkParams& p;
+  const Plan& plan;
+  int cost, b, i, kvh;
+  int64_t at;
+  Request r;
+
+  __device__ __forceinline__ Walk(const ChunkParams& p_, const Plan& plan_, int cost_)
+      : p(p_), plan(plan_), cost(cost_), b(plan_.b), i(plan_.i), kvh(plan_.kvh), at(plan_.at) {
+    r.set(p, b);
+  }
+  // The next part with tiles in this CTA's run; false at its end.
+  __device__ __forceinline__ bool next(Piece& s) {
+    while (at < plan.x1) {
+      const int tiles = r.tiles(i);
+      const int64_t real = at + cost;
+      const int64_t a = max((int64_t)0, plan.x0 - real), e = min((int64_t)tiles, plan.x1 - real);
+      const int j0 = i * r.step, n = min(r.step, r.c.n - j0), half = r.step / 2;
+      if (a < e) {
+        s.b = b;
+        s.kvh = kvh;
+        s.s0 = r.c.s0 + j0;
+        s.tokens[0] = min(n, half);
+        s.tokens[1] = max(0, n - half);
+        s.pos0 = r.c.first + j0;
+        s.last = s.pos0 + n - 1;
+        s.lo = p.window > 0 ? max(0, max(0, s.pos0 + 1) - p.window) : 0;
+        s.sink = min(p.n_sink, s.lo);
+        s.lead = min((s.sink + kBlk - 1) / kBlk, s.lo / kBlk);
+        const int last0 = s.pos0 + s.tokens[0] - 1;
+        s.count[0] = last0 < 0 ? 1 : s.lead + last0 / kBlk + 1 - s.lo / kBlk;
+        s.count[1] = s.tokens[1] > 0 ? tiles : 0;
+        s.a = (int)a;
+        s.e = (int)e;
+        s.tiles = tiles;
+        s.real = real;
+      }
+      at += tiles + cost;
+      if (++kvh == p.Hkv) {
+        kvh = 0;
+        if (++i == r.units) {
+          i = 0;
+          if (at < plan.x1)
+            do r.set(p, ++b); while (r.units == 0);
+        }
+      }
+      if (a < e) return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------- roles
+
+// K boxes (warps 0, 1) or V boxes (warps 2, 3) of every tile.
+template <int D>
+__device__ __forceinline__ void run_producer(const ChunkParams& p, const Plan& plan, int cost, const Maps& maps, Bars& bars,
+                                             uint32_t ring, int warp, int lane) {
+  using C = Cfg<D>;
+  const bool is_v = warp >= 2;
+  const int bs = p.block_size, br = min(kBlk, bs & -bs);
+  const int sub_n = kBlk / br;
+  const int j = lane * 2 + (warp & 1);  // box: sub-block j / halves, column half j % halves
+  const int sub = j / (D / 64), h = j % (D / 64);
+  const bool has_box = sub < sub_n;
+  const int64_t rows_total = p.num_blocks * p.Hkv * bs;
+  const CUtensorMap* map = is_v ? &maps.v : &maps.k;
+  const uint32_t dst0 = ring + h * kHalf + sub * br * 128;
+  uint32_t g = 0;  // tiles so far: K of tile g is ring entry 2 g, V 2 g + 1
+  bool ok = true;
+  Walk walk(p, plan, cost);
+  Piece s;
+  while (ok && walk.next(s)) {
+    const int32_t* trow = p.table + (int64_t)s.b * p.max_blocks;
+    // where this lane's box of tile t comes from: the first row, or past the end for zeros
+    auto row_of = [&](int t) -> int {
+      const int pos = s.key(t) + sub * br;
+      if (!has_box || !(pos <= s.last && (pos + br > s.lo || pos < s.sink))) return (int)rows_total;
+      const int col = pos / bs;
+      const int64_t blk = __ldg(trow + col);
+      if (blk < 0 || blk >= p.num_blocks) {
+        if (p.status) atomicOr(p.status, TV_DEV_BAD_BLOCK);
+        return (int)rows_total;
+      }
+      return (int)((blk * p.Hkv + s.kvh) * bs + (pos - col * bs));
+    };
+    int row = row_of(s.a);
+    for (int t = s.a; t < s.e; ++t, ++g) {
+      const int now = row;
+      if (t + 1 < s.e) row = row_of(t + 1);
+      const uint32_t n = 2 * g + (is_v ? 1 : 0), slot = n % C::kSlots, use = n / C::kSlots;
+      if (use > 0) ok = mbar_wait_warp(&bars.empty[slot], (use - 1) & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      if (withhold(n)) continue;
+      if ((warp & 1) == 0 && lane == 0) mbar_expect_tx(&bars.full[slot], C::kTile);
+      __syncwarp();
+      if (has_box) tma_2d(dst0 + slot * C::kTile, map, h * 64, now, &bars.full[slot]);
+      __syncwarp();
+    }
+  }
+  // what was asked for lands before the CTA ends
+  if (!ok && lane == 0) {
+    const uint32_t end = 2 * g + (is_v ? 1 : 0);
+    for (uint32_t n = end > C::kSlots ? end - C::kSlots + ((end - C::kSlots) & 1) : (is_v ? 1 : 0); n < end; n += 2)
+      if ((n & 1) == (is_v ? 1u : 0u))
+        mbar_wait(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, nullptr, limit_ns(), false);
+  }
+}
+
+// Q tiles of the units, each as soon as the unit before it has no more products with its own.
+template <int D>
+__device__ __forceinline__ void run_q_loader(const ChunkParams& p, const Plan& plan, int cost, const Maps& maps, Bars& bars,
+                                             uint32_t base) {
+  using C = Cfg<D>;
+  uint32_t units[2] = {0, 0};
+  bool ok = true;
+  Walk walk(p, plan, cost);
+  Piece s;
+  while (ok && walk.next(s)) {
+    for (int m = 0; m < 2 && ok; ++m) {
+      if (s.computed(m) == 0) continue;
+      if (units[m] > 0) ok = mbar_wait(&bars.q_free[m], (units[m] - 1) & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      mbar_expect_tx(&bars.q_full[m], D / 64 * p.G * (128 / p.G) * 128);
+      for (int h = 0; h < D / 64; ++h)
+        tma_3d(base + m * C::kTile + h * kHalf, &maps.q, h * 64, s.kvh * p.G, s.s0 + m * (128 / p.G), &bars.q_full[m]);
+      ++units[m];
+    }
+  }
+  for (int m = 0; m < 2; ++m)  // what was asked for lands before the CTA ends
+    if (units[m]) mbar_wait(&bars.q_full[m], (units[m] - 1) & 1, &bars.abort, nullptr, limit_ns(), false);
+}
+
+// All products of M tile m.
+template <int D>
+__device__ __forceinline__ void run_issuer(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint32_t base,
+                                           uint32_t tmem, int m) {
+  using C = Cfg<D>;
+  constexpr uint32_t id_s = idesc_bf16(128, kBlk, false), id_o = idesc_bf16(128, D, true);
+  constexpr uint32_t hi = desc_hi(1024);
+  const uint32_t ring = base + C::kOffRing;
+  const uint32_t dS = tmem + kColS(m), dO = tmem + kColO(m);
+  const uint32_t q_lo = desc_lo(base + m * C::kTile, 0);
+  uint32_t g = 0, units = 0, tiles = 0;  // ring's tiles, this M tile's units and tiles
+  bool ok = true;
+  Walk walk(p, plan, cost);
+  Piece s;
+  auto landed = [&](uint32_t n) {
+    return mbar_wait(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
+  };
+  auto issue_pv = [&](uint32_t gv, bool add) {  // O_m += P_m V of ring tile gv
+    const uint32_t n = 2 * gv + 1;
+    if (!mbar_wait(&bars.p_full[m], (tiles - 1) & 1, &bars.abort, p.status, limit_ns()) || !landed(n)) return false;
+    fence_after();
+    const uint32_t lo = desc_lo(ring + n % C::kSlots * C::kTile, kHalf);  // MN-major V: the next 64 columns
+    if (add) mma_ts<true>(dO, dS, lo, hi, id_o);
+    else mma_ts<false>(dO, dS, lo, hi, id_o);
+#pragma unroll
+    for (int k = 1; k < kBlk / 16; ++k) mma_ts<true>(dO, dS + k * 8, lo + k * (2048 >> 4), hi, id_o);
+    mma_commit(&bars.empty[n % C::kSlots]);
+    return true;
+  };
+  while (ok && walk.next(s)) {
+    const int n_mine = s.computed(m);
+    if (n_mine > 0) {
+      ok = mbar_wait(&bars.q_full[m], units & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      ++units;
+    }
+    for (int k = 0; k < s.e - s.a && ok; ++k, ++g) {
+      if (k == n_mine && k > 0) {
+        ok = issue_pv(g - 1, k > 1);
+        if (!ok) break;
+        mma_commit(&bars.o_done[m]);
+      }
+      const uint32_t n = 2 * g;
+      if (k >= n_mine) {  // not this M tile's: its share of the slots is free once they have landed
+        ok = landed(n) && landed(n + 1);
+        if (!ok) break;
+        mbar_arrive(&bars.empty[n % C::kSlots]);
+        mbar_arrive(&bars.empty[(n + 1) % C::kSlots]);
+        continue;
+      }
+      if (k > 0) {
+        ok = issue_pv(g - 1, k > 1);
+        if (!ok) break;
+      }
+      ok = landed(n);
+      if (!ok) break;
+      fence_after();
+      const uint32_t k_lo = desc_lo(ring + n % C::kSlots * C::kTile, 0);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * (kHalf >> 4) + (kk % 4) * 2;
+        mma_bf16(dS, (uint64_t)hi << 32 | (q_lo + off), (uint64_t)hi << 32 | (k_lo + off), id_s, kk > 0);
+      }
+      mma_commit(&bars.s_full[m]);
+      mma_commit(&bars.empty[n % C::kSlots]);
+      ++tiles;
+      if (k == n_mine - 1) mma_commit(&bars.q_free[m]);
+    }
+    if (ok && n_mine > 0 && n_mine == s.e - s.a) {
+      ok = issue_pv(g - 1, n_mine > 1);
+      if (ok) mma_commit(&bars.o_done[m]);
+    }
+  }
+  if (!ok) {  // no product still runs when the CTA frees its TMEM
+    mma_commit(&bars.drain[m]);
+    mbar_wait(&bars.drain[m], 0, &bars.abort, nullptr, limit_ns(), false);
+  }
+}
+
+__device__ __forceinline__ float max128(const float (&v)[128]) {
+  float a[44];
+#pragma unroll
+  for (int i = 0; i < 42; ++i) a[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+  a[42] = v[126], a[43] = v[127];
+  float b[16];
+#pragma unroll
+  for (int i = 0; i < 14; ++i) b[i] = max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
+  b[14] = a[42], b[15] = a[43];
+  float c[6];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) c[i] = max3(b[3 * i], b[3 * i + 1], b[3 * i + 2]);
+  c[5] = b[15];
+  return max3(max3(c[0], c[1], c[2]), c[3], fmaxf(c[4], c[5]));
+}
+
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t count_arrival(uint32_t* counter) {
+  uint32_t before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(counter), "r"(1u) : "memory");
+  return before;
+}
+
+// Joins a split unit's pieces, in order, by the 8 softmax warps, a row at a time each: lane l has D / 32 of its outputs.
+template <int D>
+__device__ void join(const ChunkParams& p, const Plan& plan, const Piece& s, int warp, int lane) {
+  constexpr int kE = D / 32;
+  const int c0 = (int)run_of(s.real, plan.total, plan.ctas), c1 = (int)run_of(s.real + s.tiles - 1, plan.total, plan.ctas);
+  const int n = c1 - c0 + 1, per = 128 / p.G;
+  for (int x = warp; x < (s.tokens[0] + s.tokens[1]) * p.G; x += 8) {
+    const int m = x >= per * p.G, row = m * 128 + x - m * per * p.G;
+    float top = kNoScore, sum = 0.f, o[kE] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      float pm = kNoScore, pl = 0.f;
+      if (i < n) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + ((int64_t)(c0 + i) * 2 + (i == 0)) * 256 + row);
+        pm = ml.x, pl = ml.y;
+      }
+      float t = pm;
+#pragma unroll
+      for (int w = 16; w; w /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
+      const float now = fmaxf(top, t), scale = exp2_approx(top - now);
+      top = now;
+      const float w = pl == 0.f ? 0.f : exp2_approx(pm - now);
+      sum *= scale;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] *= scale;
+      const int here = min(32, n - i0);
+#pragma unroll 4
+      for (int k = 0; k < here; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k), lk = __shfl_sync(0xffffffffu, pl, k);
+        const float* src = p.part_o + (((int64_t)(c0 + i0 + k) * 2 + (i0 + k == 0)) * 256 + row) * D + lane * kE;
+        float v[kE];
+        if constexpr (kE == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+          v[0] = y.x, v[1] = y.y;
+        }
+        sum = fmaf(wk, lk, sum);
+        if (wk != 0.f) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) o[e] = fmaf(wk, v[e], o[e]);
+        }
+      }
+    }
+    const float f = inverse(sum);
+    const int64_t at = ((int64_t)s.s0 + x / p.G) * p.Hq + s.kvh * p.G + x % p.G;
+    uint32_t out[kE / 2];
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) out[e] = pack_bf16(o[2 * e] * f, o[2 * e + 1] * f);
+    char* dst = p.out + (at * D + lane * kE) * 2;
+    if constexpr (kE == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = out[0];
+    if (p.lse && lane == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
+  }
+}
+
+// Softmax and results of M tile m's rows, one a thread.  kAny: a cap, a bias or a scale that is not positive.
+template <int D, bool kAny>
+__device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint8_t* ring,
+                                            uint32_t tmem, int m, int warp, int lane) {
+  using C = Cfg<D>;
+  const int rl = (warp % 4) * 32 + lane;  // row of the M tile = TMEM lane
+  const uint32_t lane_at = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+  const uint32_t tS = lane_at + kColS(m), tO = lane_at + kColO(m);
+  const float mul = p.scale * kLog2e;
+  const Scorer score(p);
+  uint32_t g = 0, tiles = 0, units = 0, posts = 0;
+  bool ok = true;
+  Walk walk(p, plan, cost);
+  Piece s;
+  while (ok && walk.next(s)) {
+    const int n_mine = s.computed(m);
+    const int tok = rl / p.G, head = s.kvh * p.G + rl % p.G;
+    const bool valid = tok < s.tokens[m];
+    const int first = s.pos0 + m * (128 / p.G);      // position of the M tile's first token
+    const int last = first + s.tokens[m] - 1;
+    const int pos = valid ? first + tok : -1;
+    const float slope = kAny && p.slopes && valid ? slope_of(p.slopes, head) : 0.f;
+    float top = kNoScore, sum = 0.f;
+    for (int k = 0; k < n_mine; ++k, ++tiles) {
+      const int t0 = s.key(s.a + k);
+      ok = mbar_wait_warp(&bars.s_full[m], tiles & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      fence_after();
+      float sv[kBlk];
+      {
+        uint32_t r0[32], r1[32], r2[32], r3[32];
+        tmem_ld32(tS, r0);
+        tmem_ld32(tS + 32, r1);
+        tmem_ld32(tS + 64, r2);
+        tmem_ld32(tS + 96, r3);
+        tmem_ld_wait(r0);
+        tmem_loaded(r1);
+        tmem_loaded(r2);
+        tmem_loaded(r3);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          sv[c] = __uint_as_float(r0[c]);
+          sv[32 + c] = __uint_as_float(r1[c]);
+          sv[64 + c] = __uint_as_float(r2[c]);
+          sv[96 + c] = __uint_as_float(r3[c]);
+        }
+      }
+      if constexpr (kAny) {
+#pragma unroll
+        for (int c = 0; c < kBlk; c += 16) {
+          float x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = sv[c + e];
+          score(x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sv[c + e] = p.slopes ? fmaf(slope, (float)(t0 + c + e - pos), x[e]) : x[e];
+        }
+      }
+      // rows that do not see all of the tile; keys that no row of the unit sees also leave V
+      if (t0 + kBlk - 1 > first || (p.window > 0 && last - t0 >= p.window)) {
+        const int most = min(pos - t0, kBlk);  // keys up to it
+        const int least = p.window > 0 && pos >= t0 ? max(-1, min(pos - t0 - p.window + 1, kBlk)) : -1;  // from it on
+        const int kept = max(-1, min(p.n_sink - t0, kBlk));  // or below it
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c)
+          if (!(c <= most && (c >= least || c < kept))) sv[c] = -INFINITY;
+        const int t = t0 + rl;
+        if (t0 + kBlk - 1 > s.last || t0 < s.lo) {
+          const uint32_t n = 2 * (g + k) + 1;
+          ok = mbar_wait_warp(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
+          if (!ok) break;
+          if (t > s.last || (t < s.lo && t >= s.sink)) {
+            uint4* row = reinterpret_cast<uint4*>(ring + n % C::kSlots * C::kTile + rl * 128);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) row[h * (kHalf / 16) + x] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+      }
+      const float mx = kAny ? max128(sv) : max128(sv) * mul;
+      const float now = fmaxf(top, mx);
+      const bool grow = now > top + kLag;
+      if (k > 0 && __any_sync(0xffffffffu, grow)) {  // S of this tile was committed behind P V of the one before
+        const float alpha = grow ? exp2_approx(top - now) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tO + c, r);
+          tmem_ld_wait(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+          tmem_st32(tO + c, r);
+        }
+      }
+      if (grow) {
+        sum *= exp2_approx(top - now);
+        top = now;
+      }
+      const float f = kAny ? 1.f : mul;
+      const uint64_t sc2 = pack_f32x2(f, f), neg2 = pack_f32x2(-top, -top);
+      uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float e0, e1;
+          exp2_pair(sv[half * 64 + 2 * c], sv[half * 64 + 2 * c + 1], sc2, neg2, e0, e1);
+          if (c & 1) acc1 = add_f32x2(acc1, pack_f32x2(e0, e1)); else acc0 = add_f32x2(acc0, pack_f32x2(e0, e1));
+          pk[c] = pack_bf16(e0, e1);
+        }
+        tmem_st32(tS + half * 32, pk);
+      }
+      sum += sum_f32x2(add_f32x2(acc0, acc1));
+      tmem_st_wait();
+      fence_before();
+      mbar_arrive(&bars.p_full[m]);
+    }
+    if (!ok) break;
+    g += s.e - s.a;
+    if (n_mine > 0) {
+      ok = mbar_wait_warp(&bars.o_done[m], units & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      fence_after();
+      ++units;
+    }
+    if (!s.split()) {
+      if (n_mine > 0) {
+        const int64_t at = ((int64_t)s.s0 + m * (128 / p.G) + tok) * p.Hq + head;
+        const float f = inverse(sum);
+        char* dst = p.out + at * D * 2;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tO + c, r);
+          tmem_ld_wait(r);
+          if (valid) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack_bf16(__uint_as_float(r[16 * x + 2 * e]) * f, __uint_as_float(r[16 * x + 2 * e + 1]) * f);
+              store32(dst + (c + 16 * x) * 2, w);
+            }
+          }
+        }
+        if (valid && p.lse) p.lse[at] = (top + log2f(sum)) * kLn2;
+        fence_before();
+      }
+      continue;
+    }
+    // a piece: its rows to the workspace; the unit's last arrival joins them
+    {
+      const int64_t slot = (int64_t)blockIdx.x * 2 + (s.a == 0);
+      const int64_t row = slot * 256 + m * 128 + rl;
+      if (valid) {
+        reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(top, sum);
+        if (n_mine == 0) {
+          const uint32_t zero[8] = {};
+#pragma unroll 1
+          for (int c = 0; c < D; c += 8) store32(p.part_o + row * D + c, zero);
+        }
+      }
+      if (n_mine > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tO + c, r);
+          tmem_ld_wait(r);
+          if (valid) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = r[8 * x + e];
+              store32(p.part_o + row * D + c + 8 * x, w);
+            }
+          }
+        }
+        fence_before();
+      }
+      __threadfence();
+      mbar_arrive(&bars.posted);
+      ok = mbar_wait_warp(&bars.posted, posts & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      if (warp == 8 && lane == 0) {
+        const int c0 = (int)run_of(s.real, plan.total, plan.ctas);
+        const uint32_t n = (uint32_t)(run_of(s.real + s.tiles - 1, plan.total, plan.ctas) - c0 + 1);
+        const bool all = count_arrival(p.arrive + c0) == n - 1;
+        if (all) p.arrive[c0] = 0;
+        bars.last = all;
+        mbar_arrive(&bars.decided);
+      }
+      ok = mbar_wait_warp(&bars.decided, posts & 1, &bars.abort, p.status, limit_ns());
+      if (!ok) break;
+      ++posts;
+      if (*(volatile int*)&bars.last) {
+        __threadfence();
+        join<D>(p, plan, s, warp - 8, lane);
+      }
+    }
+  }
+}
+
+template <int D, bool kAny>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, int cost, int least) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Bars bars;
+  __shared__ Plan plan;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* ring = raw + (base - smem_u32(raw)) + C::kOffRing;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (p.cu && p.status && blockIdx.x == 0) {
+    ChunkOf c;
+    for (int b = threadIdx.x; b < p.B; b += kThreads)
+      if (!chunk_of(p, b, c)) atomicOr(p.status, TV_DEV_BAD_OFFSETS);
+  }
+  make_plan(p, cost, least, plan);
+  if (plan.x0 >= plan.x1) return;  // all threads, before anything is set up
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 2);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&bars.q_full[m], 1);
+      mbar_init(&bars.q_free[m], 1);
+      mbar_init(&bars.s_full[m], 1);
+      mbar_init(&bars.p_full[m], 128);
+      mbar_init(&bars.o_done[m], 1);
+      mbar_init(&bars.drain[m], 1);
+    }
+    mbar_init(&bars.posted, 256);
+    mbar_init(&bars.decided, 1);
+    bars.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 6) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars.tmem;
+  // registers: 256 threads x 64 + 256 x 192 = 512 x 128, what the block was launched with
+  if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 4) {
+      run_producer<D>(p, plan, cost, maps, bars, base + C::kOffRing, warp, lane);
+    } else if (warp < 6) {
+      if (lane == 0) run_issuer<D>(p, plan, cost, bars, base, tmem, warp - 4);
+    } else if (warp == 6) {
+      if (lane == 0) run_q_loader<D>(p, plan, cost, maps, bars, base);
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    run_softmax<D, kAny>(p, plan, cost, bars, ring, tmem, (warp - 8) / 4, warp, lane);
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 6) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int get_encoder(EncodeTiled* fn) {
+  static std::once_flag once;
+  static EncodeTiled cached = nullptr;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    if (err == cudaSuccess && q == cudaDriverEntryPointSuccess) cached = reinterpret_cast<EncodeTiled>(f);
+  });
+  if (!cached) return fail(TV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorName(err));
+  *fn = cached;
+  return TV_OK;
+}
+
+int encode(EncodeTiled fn, CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+           const cuuint32_t* box, const char* what) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TV_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
+  return TV_OK;
+}
+
+template <int D, bool kAny>
+int launch(const ChunkParams& p, const Maps& maps, cudaStream_t stream) {
+  constexpr int smem = Cfg<D>::kSmem;
+  const cudaError_t e =
+      cudaFuncSetAttribute(chunk_tc_kernel<D, kAny>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(chunk_tc_kernel)");
+  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, 2, 4);
+  TV_LAUNCH_CHECK("chunk_tc_kernel");
+  return TV_OK;
+}
+
+}  // namespace
+
+const char* chunk_tc_unsupported(const DeviceInfo& dev, const ChunkParams& p, int dtype, int head_dim) {
+  if (dev.cc_major != 10) return "device is not sm_10x";
+  if (dtype != TV_BF16) return "dtype is not bf16";
+  if (head_dim != 64 && head_dim != 128) return "head_dim is not 64 or 128";
+  if (p.G > 128) return "more than 128 query heads per KV head";
+  if (p.block_size % 8) return "block_size is not a multiple of 8";
+  if (p.num_blocks >= INT32_MAX / ((int64_t)p.Hkv * p.block_size)) return "the cache has 2^31 rows";
+  if (p.T > 1 && (p.q_stride < (int64_t)p.Hq * head_dim * 2 || p.q_stride >= (int64_t)1 << 40))
+    return "queries of neighbouring tokens overlap, or lie 2^40 bytes apart";
+  if (dev.max_smem_optin < (size_t)Cfg<128>::kSmem + sizeof(Bars) + sizeof(Plan) + 256) return "not enough shared memory";
+  return nullptr;
+}
+
+size_t chunk_tc_workspace(int head_dim, int ctas) { return (size_t)ctas * 2 * 256 * (head_dim + 2) * 4; }
+
+int launch_chunk_tc(const ChunkParams& p, int D, cudaStream_t stream) {
+  EncodeTiled fn;
+  if (int rc = get_encoder(&fn)) return rc;
+  Maps maps;
+  const int br = std::min(kBlk, p.block_size & -p.block_size);
+  const cuuint64_t row = (cuuint64_t)D * 2;
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)p.num_blocks * p.Hkv * p.block_size}, strides[1] = {row};
+    const cuuint32_t box[2] = {64, (cuuint32_t)br};
+    if (int rc = encode(fn, &maps.k, p.k_cache, 2, dims, strides, box, "k_cache")) return rc;
+    if (int rc = encode(fn, &maps.v, p.v_cache, 2, dims, strides, box, "v_cache")) return rc;
+  }
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    const cuuint64_t strides[2] = {row, p.T > 1 ? (cuuint64_t)p.q_stride : row * p.Hq};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
+    if (int rc = encode(fn, &maps.q, p.q, 3, dims, strides, box, "q")) return rc;
+  }
+  // the plain form masks before it scales: its factor has to keep -inf what it is
+  const bool any = p.softcap > 0.f || p.slopes || !(p.scale * kLog2e >= FLT_MIN);
+  if (D == 64) return any ? launch<64, true>(p, maps, stream) : launch<64, false>(p, maps, stream);
+  return any ? launch<128, true>(p, maps, stream) : launch<128, false>(p, maps, stream);
+}
+
+}  // namespace tv
+
+#ifdef TV_TEST_HOOKS
+// Development builds only: the wait limit, and the ring entry of CTA 0 that gets no loads (-1: none).
+extern "C" int tv_test_set_chunk_hooks(unsigned long long limit_ns, int withhold_entry) {
+  if (cudaMemcpyToSymbol(tv::g_chunk_limit_ns, &limit_ns, sizeof(limit_ns)) != cudaSuccess) return -6;
+  if (cudaMemcpyToSymbol(tv::g_chunk_withhold, &withhold_entry, sizeof(withhold_entry)) != cudaSuccess) return -6;
+  return cudaDeviceSynchronize() == cudaSuccess ? 0 : -6;
+}
+#endif
