@@ -9,10 +9,11 @@
 // * Keys: tiles of 128, K and V in a ring of 32 KB slots of their own, by TMA
 //   boxes of (a power of two of) rows within a cache block.  Boxes without a
 //   key that the unit sees, and bad blocks, are sent out of bounds: zeros.
-// * S_m = Q_m K^T (128 x 128, both operands from shared memory) and O_m += P_m V
-//   (P_m from TMEM, bf16, over S_m's columns) are issued by one thread per M
-//   tile: while the softmax of one M tile runs, the products of the other do.
-//   S_0 128 | S_1 128 | O_0 128 | O_1 128 columns fill the TMEM.
+// * S_m = Q_m K^T (128 x 64, both operands from shared memory) and O_m += P_m V
+//   (P_m from TMEM, bf16, over S_m's columns) in steps of 64 keys, issued by one
+//   thread per M tile.  Each M tile has two S buffers, so the products of the
+//   next step and of the other M tile run while a step's softmax does.
+//   S_0 2 x 64 | S_1 2 x 64 | O_0 128 | O_1 128 columns fill the TMEM.
 // * Softmax: a thread per row; the running maximum may lag by 2^8, so that O is
 //   rescaled in TMEM only when it grows by more.  Weights are rounded to bf16 for
 //   P V (an operand of kind::f16 holds no more; half a step, 2^-9 of a weight on
@@ -59,7 +60,7 @@ constexpr uint32_t kColO(int m) { return 256 + m * 128; }
 
 struct Bars {
   uint64_t full[10], empty[10];
-  uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], drain[2];
+  uint64_t q_full[2], q_free[2], s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
   uint64_t posted, decided;
   uint32_t tmem;
   int abort;
@@ -245,6 +246,18 @@ struct Piece {
   __device__ __forceinline__ int key(int t) const { return (t < lead ? t : lo / kBlk + t - lead) * kBlk; }
   // tiles of this part that M tile m computes
   __device__ __forceinline__ int computed(int m) const { return max(0, min(e, count[m]) - a); }
+  __device__ __forceinline__ int last_of(int m) const { return m ? last : pos0 + tokens[0] - 1; }
+  // Its steps, 64 keys each: step x is half x % 2 of tile a + x / 2; halves that none of its rows sees are left out at
+  // the window's start and at the end.
+  __device__ __forceinline__ void steps(const ChunkParams& p, int m, int& from, int& to) const {
+    const int n = computed(m);
+    from = 0;
+    to = 2 * n;
+    if (n == 0) return;
+    if (a + n == count[m] && last_of(m) < key(a + n - 1) + 64) --to;
+    const int from_pos = pos0 + m * (128 / p.G);  // of the M tile's first token
+    if (a == 0 && p.window > 0 && p.n_sink <= key(0) && from_pos - key(0) - 63 >= p.window) from = 1;
+  }
   __device__ __forceinline__ bool split() const { return a > 0 || e < tiles; }
 };
 
@@ -381,78 +394,78 @@ __device__ __forceinline__ void run_q_loader(const ChunkParams& p, const Plan& p
     if (units[m]) mbar_wait(&bars.q_full[m], (units[m] - 1) & 1, &bars.abort, nullptr, limit_ns(), false);
 }
 
-// All products of M tile m.
+// All products of M tile m: S of step j + 2 follows P V of step j, whose columns it takes, in the pipe's order.
 template <int D>
 __device__ __forceinline__ void run_issuer(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint32_t base,
                                            uint32_t tmem, int m) {
   using C = Cfg<D>;
-  constexpr uint32_t id_s = idesc_bf16(128, kBlk, false), id_o = idesc_bf16(128, D, true);
+  constexpr uint32_t id_s = idesc_bf16(128, 64, false), id_o = idesc_bf16(128, D, true);
   constexpr uint32_t hi = desc_hi(1024);
   const uint32_t ring = base + C::kOffRing;
-  const uint32_t dS = tmem + kColS(m), dO = tmem + kColO(m);
+  const uint32_t dO = tmem + kColO(m);
   const uint32_t q_lo = desc_lo(base + m * C::kTile, 0);
-  uint32_t g = 0, units = 0, tiles = 0;  // ring's tiles, this M tile's units and tiles
+  uint32_t g = 0, units = 0;   // ring's tiles, this M tile's units
+  uint32_t n_s = 0, n_pv = 0;  // its steps so far
   bool ok = true;
   Walk walk(p, plan, cost);
   Piece s;
   auto landed = [&](uint32_t n) {
     return mbar_wait(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
   };
-  auto issue_pv = [&](uint32_t gv, bool add) {  // O_m += P_m V of ring tile gv
-    const uint32_t n = 2 * gv + 1;
-    if (!mbar_wait(&bars.p_full[m], (tiles - 1) & 1, &bars.abort, p.status, limit_ns()) || !landed(n)) return false;
-    fence_after();
-    const uint32_t lo = desc_lo(ring + n % C::kSlots * C::kTile, kHalf);  // MN-major V: the next 64 columns
-    if (add) mma_ts<true>(dO, dS, lo, hi, id_o);
-    else mma_ts<false>(dO, dS, lo, hi, id_o);
-#pragma unroll
-    for (int k = 1; k < kBlk / 16; ++k) mma_ts<true>(dO, dS + k * 8, lo + k * (2048 >> 4), hi, id_o);
-    mma_commit(&bars.empty[n % C::kSlots]);
-    return true;
-  };
   while (ok && walk.next(s)) {
+    int from, to;
+    s.steps(p, m, from, to);
     const int n_mine = s.computed(m);
-    if (n_mine > 0) {
-      ok = mbar_wait(&bars.q_full[m], units & 1, &bars.abort, p.status, limit_ns());
-      if (!ok) break;
-      ++units;
-    }
-    for (int k = 0; k < s.e - s.a && ok; ++k, ++g) {
-      if (k == n_mine && k > 0) {
-        ok = issue_pv(g - 1, k > 1);
-        if (!ok) break;
-        mma_commit(&bars.o_done[m]);
-      }
-      const uint32_t n = 2 * g;
-      if (k >= n_mine) {  // not this M tile's: its share of the slots is free once they have landed
-        ok = landed(n) && landed(n + 1);
-        if (!ok) break;
-        mbar_arrive(&bars.empty[n % C::kSlots]);
-        mbar_arrive(&bars.empty[(n + 1) % C::kSlots]);
-        continue;
-      }
-      if (k > 0) {
-        ok = issue_pv(g - 1, k > 1);
-        if (!ok) break;
-      }
-      ok = landed(n);
-      if (!ok) break;
+    auto issue_s = [&](int x) {
+      const uint32_t n = 2 * (g + (x >> 1));
+      if ((x == from || (x & 1) == 0) && !landed(n)) return false;
       fence_after();
-      const uint32_t k_lo = desc_lo(ring + n % C::kSlots * C::kTile, 0);
+      const uint32_t k_lo = desc_lo(ring + n % C::kSlots * C::kTile + (x & 1) * 8192, 0);
+      const uint32_t dS = tmem + kColS(m) + (n_s & 1) * 64;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * (kHalf >> 4) + (kk % 4) * 2;
         mma_bf16(dS, (uint64_t)hi << 32 | (q_lo + off), (uint64_t)hi << 32 | (k_lo + off), id_s, kk > 0);
       }
-      mma_commit(&bars.s_full[m]);
-      mma_commit(&bars.empty[n % C::kSlots]);
-      ++tiles;
-      if (k == n_mine - 1) mma_commit(&bars.q_free[m]);
+      mma_commit(&bars.s_full[m][n_s & 1]);
+      if ((x & 1) || x == to - 1) mma_commit(&bars.empty[n % C::kSlots]);
+      if (x == to - 1) mma_commit(&bars.q_free[m]);
+      ++n_s;
+      return true;
+    };
+    auto issue_pv = [&](int x) {
+      const uint32_t n = 2 * (g + (x >> 1)) + 1;
+      if (!mbar_wait(&bars.p_full[m][n_pv & 1], (n_pv >> 1) & 1, &bars.abort, p.status, limit_ns()) || !landed(n)) return false;
+      fence_after();
+      const uint32_t aP = tmem + kColS(m) + (n_pv & 1) * 64;
+      const uint32_t lo = desc_lo(ring + n % C::kSlots * C::kTile + (x & 1) * 8192, kHalf);  // MN-major V: the next 64 columns
+      if (x > from) mma_ts<true>(dO, aP, lo, hi, id_o);
+      else mma_ts<false>(dO, aP, lo, hi, id_o);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) mma_ts<true>(dO, aP + k * 8, lo + k * (2048 >> 4), hi, id_o);
+      mma_commit(&bars.pv_done[m][n_pv & 1]);
+      if ((x & 1) || x == to - 1) mma_commit(&bars.empty[n % C::kSlots]);
+      ++n_pv;
+      return true;
+    };
+    if (n_mine > 0) {
+      ok = mbar_wait(&bars.q_full[m], units & 1, &bars.abort, p.status, limit_ns());
+      ++units;
+      for (int x = from; ok && x < min(from + 2, to); ++x) ok = issue_s(x);
+      for (int x = from; ok && x < to; ++x) {
+        ok = issue_pv(x);
+        if (ok && x + 2 < to) ok = issue_s(x + 2);
+      }
     }
-    if (ok && n_mine > 0 && n_mine == s.e - s.a) {
-      ok = issue_pv(g - 1, n_mine > 1);
-      if (ok) mma_commit(&bars.o_done[m]);
+    // tiles that are not this M tile's: its share of the slots is free once they have landed
+    for (int k = n_mine; ok && k < s.e - s.a; ++k) {
+      const uint32_t n = 2 * (g + k);
+      ok = landed(n) && landed(n + 1);
+      if (!ok) break;
+      mbar_arrive(&bars.empty[n % C::kSlots]);
+      mbar_arrive(&bars.empty[(n + 1) % C::kSlots]);
     }
+    g += s.e - s.a;
   }
   if (!ok) {  // no product still runs when the CTA frees its TMEM
     mma_commit(&bars.drain[m]);
@@ -460,20 +473,16 @@ __device__ __forceinline__ void run_issuer(const ChunkParams& p, const Plan& pla
   }
 }
 
-__device__ __forceinline__ float max128(const float (&v)[128]) {
-  float a[44];
+__device__ __forceinline__ float max64(const float (&v)[64]) {
+  float a[22];
 #pragma unroll
-  for (int i = 0; i < 42; ++i) a[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-  a[42] = v[126], a[43] = v[127];
-  float b[16];
+  for (int i = 0; i < 21; ++i) a[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+  a[21] = v[63];
+  float b[8];
 #pragma unroll
-  for (int i = 0; i < 14; ++i) b[i] = max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
-  b[14] = a[42], b[15] = a[43];
-  float c[6];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) c[i] = max3(b[3 * i], b[3 * i + 1], b[3 * i + 2]);
-  c[5] = b[15];
-  return max3(max3(c[0], c[1], c[2]), c[3], fmaxf(c[4], c[5]));
+  for (int i = 0; i < 7; ++i) b[i] = max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
+  b[7] = a[21];
+  return max3(max3(b[0], b[1], b[2]), max3(b[3], b[4], b[5]), fmaxf(b[6], b[7]));
 }
 
 __device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
@@ -555,12 +564,14 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
   const uint32_t tS = lane_at + kColS(m), tO = lane_at + kColO(m);
   const float mul = p.scale * kLog2e;
   const Scorer score(p);
-  uint32_t g = 0, tiles = 0, units = 0, posts = 0;
+  uint32_t g = 0, done = 0, posts = 0;  // ring's tiles, this M tile's steps
   bool ok = true;
   Walk walk(p, plan, cost);
   Piece s;
   while (ok && walk.next(s)) {
     const int n_mine = s.computed(m);
+    int from, to;
+    s.steps(p, m, from, to);
     const int tok = rl / p.G, head = s.kvh * p.G + rl % p.G;
     const bool valid = tok < s.tokens[m];
     const int first = s.pos0 + m * (128 / p.G);      // position of the M tile's first token
@@ -568,68 +579,67 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
     const int pos = valid ? first + tok : -1;
     const float slope = kAny && p.slopes && valid ? slope_of(p.slopes, head) : 0.f;
     float top = kNoScore, sum = 0.f;
-    for (int k = 0; k < n_mine; ++k, ++tiles) {
-      const int t0 = s.key(s.a + k);
-      ok = mbar_wait_warp(&bars.s_full[m], tiles & 1, &bars.abort, p.status, limit_ns());
+    for (int x = from; x < to; ++x, ++done) {
+      const int tile0 = s.key(s.a + (x >> 1)), t0 = tile0 + (x & 1) * 64;
+      const uint32_t tB = tS + (done & 1) * 64;
+      ok = mbar_wait_warp(&bars.s_full[m][done & 1], (done >> 1) & 1, &bars.abort, p.status, limit_ns());
       if (!ok) break;
       fence_after();
-      float sv[kBlk];
+      float sv[64];
       {
-        uint32_t r0[32], r1[32], r2[32], r3[32];
-        tmem_ld32(tS, r0);
-        tmem_ld32(tS + 32, r1);
-        tmem_ld32(tS + 64, r2);
-        tmem_ld32(tS + 96, r3);
+        uint32_t r0[32], r1[32];
+        tmem_ld32(tB, r0);
+        tmem_ld32(tB + 32, r1);
         tmem_ld_wait(r0);
         tmem_loaded(r1);
-        tmem_loaded(r2);
-        tmem_loaded(r3);
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           sv[c] = __uint_as_float(r0[c]);
           sv[32 + c] = __uint_as_float(r1[c]);
-          sv[64 + c] = __uint_as_float(r2[c]);
-          sv[96 + c] = __uint_as_float(r3[c]);
         }
       }
       if constexpr (kAny) {
 #pragma unroll
-        for (int c = 0; c < kBlk; c += 16) {
-          float x[16];
+        for (int c = 0; c < 64; c += 16) {
+          float y[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = sv[c + e];
-          score(x);
+          for (int e = 0; e < 16; ++e) y[e] = sv[c + e];
+          score(y);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sv[c + e] = p.slopes ? fmaf(slope, (float)(t0 + c + e - pos), x[e]) : x[e];
+          for (int e = 0; e < 16; ++e) sv[c + e] = p.slopes ? fmaf(slope, (float)(t0 + c + e - pos), y[e]) : y[e];
         }
       }
-      // rows that do not see all of the tile; keys that no row of the unit sees also leave V
-      if (t0 + kBlk - 1 > first || (p.window > 0 && last - t0 >= p.window)) {
-        const int most = min(pos - t0, kBlk);  // keys up to it
-        const int least = p.window > 0 && pos >= t0 ? max(-1, min(pos - t0 - p.window + 1, kBlk)) : -1;  // from it on
-        const int kept = max(-1, min(p.n_sink - t0, kBlk));  // or below it
+      // rows that do not see all of the step's keys
+      if (t0 + 63 > first || (p.window > 0 && last - t0 >= p.window)) {
+        const int most = min(pos - t0, 64);  // keys up to it
+        const int least = p.window > 0 && pos >= t0 ? max(-1, min(pos - t0 - p.window + 1, 64)) : -1;  // from it on
+        const int kept = max(-1, min(p.n_sink - t0, 64));  // or below it
 #pragma unroll
-        for (int c = 0; c < kBlk; ++c)
+        for (int c = 0; c < 64; ++c)
           if (!(c <= most && (c >= least || c < kept))) sv[c] = -INFINITY;
-        const int t = t0 + rl;
-        if (t0 + kBlk - 1 > s.last || t0 < s.lo) {
-          const uint32_t n = 2 * (g + k) + 1;
-          ok = mbar_wait_warp(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
-          if (!ok) break;
-          if (t > s.last || (t < s.lo && t >= s.sink)) {
-            uint4* row = reinterpret_cast<uint4*>(ring + n % C::kSlots * C::kTile + rl * 128);
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-              for (int x = 0; x < 8; ++x) row[h * (kHalf / 16) + x] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-        }
       }
-      const float mx = kAny ? max128(sv) : max128(sv) * mul;
+      // keys that no row of the unit sees leave V
+      if ((x == from || (x & 1) == 0) && (tile0 + kBlk - 1 > s.last || tile0 < s.lo)) {
+        const int t = tile0 + rl;
+        const uint32_t n = 2 * (g + (x >> 1)) + 1;
+        ok = mbar_wait_warp(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
+        if (!ok) break;
+        if (t > s.last || (t < s.lo && t >= s.sink)) {
+          uint4* row = reinterpret_cast<uint4*>(ring + n % C::kSlots * C::kTile + rl * 128);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) row[h * (kHalf / 16) + y] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+      }
+      const float mx = kAny ? max64(sv) : max64(sv) * mul;
       const float now = fmaxf(top, mx);
       const bool grow = now > top + kLag;
-      if (k > 0 && __any_sync(0xffffffffu, grow)) {  // S of this tile was committed behind P V of the one before
+      if (x > from && __any_sync(0xffffffffu, grow)) {
+        ok = mbar_wait_warp(&bars.pv_done[m][(done - 1) & 1], ((done - 1) >> 1) & 1, &bars.abort, p.status, limit_ns());
+        if (!ok) break;
+        fence_after();
         const float alpha = grow ? exp2_approx(top - now) : 1.f;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -648,30 +658,26 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
       const float f = kAny ? 1.f : mul;
       const uint64_t sc2 = pack_f32x2(f, f), neg2 = pack_f32x2(-top, -top);
       uint64_t acc0 = 0, acc1 = 0;
+      uint32_t pk[32];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float e0, e1;
-          exp2_pair(sv[half * 64 + 2 * c], sv[half * 64 + 2 * c + 1], sc2, neg2, e0, e1);
-          if (c & 1) acc1 = add_f32x2(acc1, pack_f32x2(e0, e1)); else acc0 = add_f32x2(acc0, pack_f32x2(e0, e1));
-          pk[c] = pack_bf16(e0, e1);
-        }
-        tmem_st32(tS + half * 32, pk);
+      for (int c = 0; c < 32; ++c) {
+        float e0, e1;
+        exp2_pair(sv[2 * c], sv[2 * c + 1], sc2, neg2, e0, e1);
+        if (c & 1) acc1 = add_f32x2(acc1, pack_f32x2(e0, e1)); else acc0 = add_f32x2(acc0, pack_f32x2(e0, e1));
+        pk[c] = pack_bf16(e0, e1);
       }
+      tmem_st32(tB, pk);
       sum += sum_f32x2(add_f32x2(acc0, acc1));
       tmem_st_wait();
       fence_before();
-      mbar_arrive(&bars.p_full[m]);
+      mbar_arrive(&bars.p_full[m][done & 1]);
     }
     if (!ok) break;
     g += s.e - s.a;
     if (n_mine > 0) {
-      ok = mbar_wait_warp(&bars.o_done[m], units & 1, &bars.abort, p.status, limit_ns());
+      ok = mbar_wait_warp(&bars.pv_done[m][(done - 1) & 1], ((done - 1) >> 1) & 1, &bars.abort, p.status, limit_ns());
       if (!ok) break;
       fence_after();
-      ++units;
     }
     if (!s.split()) {
       if (n_mine > 0) {
@@ -777,9 +783,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int m = 0; m < 2; ++m) {
       mbar_init(&bars.q_full[m], 1);
       mbar_init(&bars.q_free[m], 1);
-      mbar_init(&bars.s_full[m], 1);
-      mbar_init(&bars.p_full[m], 128);
-      mbar_init(&bars.o_done[m], 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&bars.s_full[m][x], 1);
+        mbar_init(&bars.p_full[m][x], 128);
+        mbar_init(&bars.pv_done[m][x], 1);
+      }
       mbar_init(&bars.drain[m], 1);
     }
     mbar_init(&bars.posted, 256);
@@ -796,9 +804,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = bars.tmem;
-  // registers: 256 threads x 64 + 256 x 192 = 512 x 128, what the block was launched with
+  // registers: 256 threads x 96 + 256 x 160 = 512 x 128, what the block was launched with
   if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp < 4) {
       run_producer<D>(p, plan, cost, maps, bars, base + C::kOffRing, warp, lane);
     } else if (warp < 6) {
@@ -808,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     run_softmax<D, kAny>(p, plan, cost, bars, ring, tmem, (warp - 8) / 4, warp, lane);
   }
   fence_before();
