@@ -6,16 +6,17 @@
 //   128-row M tile (row = token * G + head, so rows of one token are
 //   neighbours); a unit is two M tiles of one (request, KV head), so a K/V byte
 //   that reaches the SM feeds 256 rows.  Q comes by one TMA box per 64 columns.
-// * Keys: tiles of 128, K and V in a ring of 32 KB slots of their own, by TMA
-//   boxes of (a power of two of) rows within a cache block.  Boxes without a
+// * Keys: tiles of 64, K and V in rings of their own, by TMA boxes of (a power
+//   of two of) rows within a cache block.  Boxes without a
 //   key that the unit sees, and bad blocks, are sent out of bounds: zeros.
 // * S_m = Q_m K^T (128 x 64, both operands from shared memory) and O_m += P_m V
-//   (P_m from TMEM, bf16, over S_m's columns) in steps of 64 keys, issued by one
-//   thread per M tile.  Each M tile has two S buffers, so the products of the
-//   next step and of the other M tile run while a step's softmax does.
+//   (P_m from TMEM, bf16, over S_m's columns), issued by a thread each.  Each M
+//   tile has two S buffers, so the products of the next tile and of the other M
+//   tile run while a tile's softmax does.
 //   S_0 2 x 64 | S_1 2 x 64 | O_0 128 | O_1 128 columns fill the TMEM.
-// * Softmax: a thread per row; the running maximum may lag by 2^8, so that O is
-//   rescaled in TMEM only when it grows by more.  Weights are rounded to bf16 for
+// * Softmax: a thread per row, against a reference that is the first tile's
+//   maximum and moves, with O rescaled in TMEM, only when weights pass 2^20; so
+//   later tiles need no maximum at all (it took a third of a tile's time).  Weights are rounded to bf16 for
 //   P V (an operand of kind::f16 holds no more; half a step, 2^-9 of a weight on
 //   average, against the 2^-9 that rounding the output takes), their sum is not.
 // * Work: the units' tiles (with a few virtual ones for a unit's fixed cost) lie
@@ -40,18 +41,21 @@ namespace tv {
 
 namespace {
 
-constexpr int kBlk = 128;          // keys of a tile
-constexpr int kHalf = kBlk * 128;  // bytes of 128 rows x 64 columns
+constexpr int kBlk = 64;           // keys of a tile
+constexpr int kQHalf = 128 * 128;  // bytes of 64 columns of a Q tile
+constexpr int kHalf = kBlk * 128;  // ... of a K or V tile
 constexpr int kThreads = 512;
 constexpr unsigned long long kLimitNs = 2000000000ull;
-constexpr float kLag = 8.f;        // log2 that the reference may stay behind the maximum
+constexpr float kMost = 0x1p20f;   // sum of a row's weights in a tile before its reference moves
 
 template <int D>
 struct Cfg {
-  static constexpr int kTile = D / 64 * kHalf;     // bytes of a K, V or Q tile
-  static constexpr int kSlots = D == 128 ? 5 : 10;
-  static constexpr int kOffRing = 2 * kTile;       // behind Q_0, Q_1
-  static constexpr int kSmem = kOffRing + kSlots * kTile + 1024;
+  static constexpr int kQTile = D / 64 * kQHalf;
+  static constexpr int kTile = D / 64 * kHalf;     // bytes of a K or V tile
+  static constexpr int kSlots = D == 128 ? 5 : 8;  // of K, and of V
+  static constexpr int kOffK = 2 * kQTile;         // behind Q_0, Q_1
+  static constexpr int kOffV = kOffK + kSlots * kTile;
+  static constexpr int kSmem = kOffV + kSlots * kTile + 1024;
 };
 static_assert(Cfg<128>::kSmem <= 227 * 1024 - 1024 && Cfg<64>::kSmem <= 227 * 1024 - 1024, "fits beside the barriers");
 
@@ -59,8 +63,8 @@ constexpr uint32_t kColS(int m) { return m * 128; }
 constexpr uint32_t kColO(int m) { return 256 + m * 128; }
 
 struct Bars {
-  uint64_t full[10], empty[10];
-  uint64_t q_full[2], q_free[2], s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
+  uint64_t full[2][8], empty[2][8];  // of K, of V
+  uint64_t q_full[2], q_free[2], s_full[2][2], p_full[2][2], pv_done[2][2], v_seen[2], drain[4];
   uint64_t posted, decided;
   uint32_t tmem;
   int abort;
@@ -107,7 +111,7 @@ __device__ int64_t floor_sum(int64_t n, int64_t a, int64_t b, int64_t m) {
   }
 }
 
-// sum over j < n of max(0, floor((b + a j) / 128)), a >= 1
+// sum over j < n of max(0, floor((b + a j) / 64)), a >= 1
 __device__ int64_t tiles_below(int64_t n, int a, int64_t b) {
   if (n <= 0) return 0;
   if (b < 0) {
@@ -117,7 +121,7 @@ __device__ int64_t tiles_below(int64_t n, int a, int64_t b) {
     b += skip * a;
   }
   if ((a & (a - 1)) == 0 && a <= kBlk) {  // steps of a power of two: runs of r equal terms
-    const int r_log = 7 - (31 - __clz(a));
+    const int r_log = 6 - (31 - __clz(a));
     auto upto = [&](int64_t x) {  // sum over i < x of floor(i / r)
       const int64_t q = x >> r_log;
       return (q * (q - 1) / 2 << r_log) + q * (x - (q << r_log));
@@ -246,18 +250,8 @@ struct Piece {
   __device__ __forceinline__ int key(int t) const { return (t < lead ? t : lo / kBlk + t - lead) * kBlk; }
   // tiles of this part that M tile m computes
   __device__ __forceinline__ int computed(int m) const { return max(0, min(e, count[m]) - a); }
-  __device__ __forceinline__ int last_of(int m) const { return m ? last : pos0 + tokens[0] - 1; }
-  // Its steps, 64 keys each: step x is half x % 2 of tile a + x / 2; halves that none of its rows sees are left out at
-  // the window's start and at the end.
-  __device__ __forceinline__ void steps(const ChunkParams& p, int m, int& from, int& to) const {
-    const int n = computed(m);
-    from = 0;
-    to = 2 * n;
-    if (n == 0) return;
-    if (a + n == count[m] && last_of(m) < key(a + n - 1) + 64) --to;
-    const int from_pos = pos0 + m * (128 / p.G);  // of the M tile's first token
-    if (a == 0 && p.window > 0 && p.n_sink <= key(0) && from_pos - key(0) - 63 >= p.window) from = 1;
-  }
+  // V of a tile at t0 holds keys that no row of the unit sees
+  __device__ __forceinline__ bool ragged(int t0) const { return t0 + kBlk - 1 > last || t0 < lo; }
   __device__ __forceinline__ bool split() const { return a > 0 || e < tiles; }
 };
 
@@ -318,18 +312,18 @@ struct Walk {
 // K boxes (warps 0, 1) or V boxes (warps 2, 3) of every tile.
 template <int D>
 __device__ __forceinline__ void run_producer(const ChunkParams& p, const Plan& plan, int cost, const Maps& maps, Bars& bars,
-                                             uint32_t ring, int warp, int lane) {
+                                             uint32_t base, int warp, int lane) {
   using C = Cfg<D>;
-  const bool is_v = warp >= 2;
+  const int v = warp / 2;
   const int bs = p.block_size, br = min(kBlk, bs & -bs);
   const int sub_n = kBlk / br;
   const int j = lane * 2 + (warp & 1);  // box: sub-block j / halves, column half j % halves
   const int sub = j / (D / 64), h = j % (D / 64);
   const bool has_box = sub < sub_n;
   const int64_t rows_total = p.num_blocks * p.Hkv * bs;
-  const CUtensorMap* map = is_v ? &maps.v : &maps.k;
-  const uint32_t dst0 = ring + h * kHalf + sub * br * 128;
-  uint32_t g = 0;  // tiles so far: K of tile g is ring entry 2 g, V 2 g + 1
+  const CUtensorMap* map = v ? &maps.v : &maps.k;
+  const uint32_t dst0 = base + (v ? C::kOffV : C::kOffK) + h * kHalf + sub * br * 128;
+  uint32_t g = 0;  // tiles so far
   bool ok = true;
   Walk walk(p, plan, cost);
   Piece s;
@@ -351,126 +345,126 @@ __device__ __forceinline__ void run_producer(const ChunkParams& p, const Plan& p
     for (int t = s.a; t < s.e; ++t, ++g) {
       const int now = row;
       if (t + 1 < s.e) row = row_of(t + 1);
-      const uint32_t n = 2 * g + (is_v ? 1 : 0), slot = n % C::kSlots, use = n / C::kSlots;
-      if (use > 0) ok = mbar_wait_warp(&bars.empty[slot], (use - 1) & 1, &bars.abort, p.status, limit_ns());
+      const uint32_t slot = g % C::kSlots, use = g / C::kSlots;
+      if (use > 0) ok = mbar_wait_warp(&bars.empty[v][slot], (use - 1) & 1, &bars.abort, p.status, limit_ns());
       if (!ok) break;
-      if (withhold(n)) continue;
-      if ((warp & 1) == 0 && lane == 0) mbar_expect_tx(&bars.full[slot], C::kTile);
+      if (withhold(2 * g + v)) continue;
+      if ((warp & 1) == 0 && lane == 0) mbar_expect_tx(&bars.full[v][slot], C::kTile);
       __syncwarp();
-      if (has_box) tma_2d(dst0 + slot * C::kTile, map, h * 64, now, &bars.full[slot]);
+      if (has_box) tma_2d(dst0 + slot * C::kTile, map, h * 64, now, &bars.full[v][slot]);
       __syncwarp();
     }
   }
   // what was asked for lands before the CTA ends
-  if (!ok && lane == 0) {
-    const uint32_t end = 2 * g + (is_v ? 1 : 0);
-    for (uint32_t n = end > C::kSlots ? end - C::kSlots + ((end - C::kSlots) & 1) : (is_v ? 1 : 0); n < end; n += 2)
-      if ((n & 1) == (is_v ? 1u : 0u))
-        mbar_wait(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, nullptr, limit_ns(), false);
-  }
+  if (!ok && lane == 0)
+    for (uint32_t i = g > C::kSlots ? g - C::kSlots : 0; i < g; ++i)
+      mbar_wait(&bars.full[v][i % C::kSlots], (i / C::kSlots) & 1, &bars.abort, nullptr, limit_ns(), false);
 }
 
-// Q tiles of the units, each as soon as the unit before it has no more products with its own.
+// The end of an issuing thread: nothing that it asked for still runs, or arrives, when the CTA frees its TMEM and ends.
+__device__ __forceinline__ void drain(Bars& bars, int i) {
+  mma_commit(&bars.drain[i]);
+  mbar_wait(&bars.drain[i], 0, &bars.abort, nullptr, limit_ns(), false);
+}
+
+// A slot is released by both M tiles, by a commit behind the products that read it or, where none do, by an arrival once
+// it has landed: so every waiting thread sees every phase of its barriers, and parities tell them apart.
+
+// Loads M tile m's Q of each unit, once the unit before it has no more products with its own, and issues S = Q K^T of
+// its tiles.  Tile j takes the columns of tile j - 2, whose P V has to be done.
 template <int D>
-__device__ __forceinline__ void run_q_loader(const ChunkParams& p, const Plan& plan, int cost, const Maps& maps, Bars& bars,
-                                             uint32_t base) {
+__device__ __forceinline__ void issue_scores(const ChunkParams& p, const Plan& plan, int cost, const Maps& maps, Bars& bars,
+                                             uint32_t base, uint32_t tmem, int m) {
   using C = Cfg<D>;
-  uint32_t units[2] = {0, 0};
+  constexpr uint32_t id = idesc_bf16(128, kBlk, false);
+  constexpr uint32_t hi = desc_hi(1024);
+  const uint32_t sQ = base + m * C::kQTile;
+  const uint32_t q_lo = desc_lo(sQ, 0);
+  uint32_t g = 0, units = 0, n_s = 0;  // ring's tiles, this M tile's units and tiles
   bool ok = true;
   Walk walk(p, plan, cost);
   Piece s;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &bars.abort, p.status, limit_ns()); };
   while (ok && walk.next(s)) {
-    for (int m = 0; m < 2 && ok; ++m) {
-      if (s.computed(m) == 0) continue;
-      if (units[m] > 0) ok = mbar_wait(&bars.q_free[m], (units[m] - 1) & 1, &bars.abort, p.status, limit_ns());
+    const int n_mine = s.computed(m);
+    if (n_mine > 0) {
+      if (units > 0) ok = wait(&bars.q_free[m], (units - 1) & 1);
       if (!ok) break;
       mbar_expect_tx(&bars.q_full[m], D / 64 * p.G * (128 / p.G) * 128);
+#pragma unroll
       for (int h = 0; h < D / 64; ++h)
-        tma_3d(base + m * C::kTile + h * kHalf, &maps.q, h * 64, s.kvh * p.G, s.s0 + m * (128 / p.G), &bars.q_full[m]);
-      ++units[m];
+        tma_3d(sQ + h * kQHalf, &maps.q, h * 64, s.kvh * p.G, s.s0 + m * (128 / p.G), &bars.q_full[m]);
+      ++units;
+      ok = wait(&bars.q_full[m], (units - 1) & 1);
     }
-  }
-  for (int m = 0; m < 2; ++m)  // what was asked for lands before the CTA ends
-    if (units[m]) mbar_wait(&bars.q_full[m], (units[m] - 1) & 1, &bars.abort, nullptr, limit_ns(), false);
-}
-
-// All products of M tile m: S of step j + 2 follows P V of step j, whose columns it takes, in the pipe's order.
-template <int D>
-__device__ __forceinline__ void run_issuer(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint32_t base,
-                                           uint32_t tmem, int m) {
-  using C = Cfg<D>;
-  constexpr uint32_t id_s = idesc_bf16(128, 64, false), id_o = idesc_bf16(128, D, true);
-  constexpr uint32_t hi = desc_hi(1024);
-  const uint32_t ring = base + C::kOffRing;
-  const uint32_t dO = tmem + kColO(m);
-  const uint32_t q_lo = desc_lo(base + m * C::kTile, 0);
-  uint32_t g = 0, units = 0;   // ring's tiles, this M tile's units
-  uint32_t n_s = 0, n_pv = 0;  // its steps so far
-  bool ok = true;
-  Walk walk(p, plan, cost);
-  Piece s;
-  auto landed = [&](uint32_t n) {
-    return mbar_wait(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
-  };
-  while (ok && walk.next(s)) {
-    int from, to;
-    s.steps(p, m, from, to);
-    const int n_mine = s.computed(m);
-    auto issue_s = [&](int x) {
-      const uint32_t n = 2 * (g + (x >> 1));
-      if ((x == from || (x & 1) == 0) && !landed(n)) return false;
+    for (int k = 0; ok && k < s.e - s.a; ++k, ++g) {
+      const uint32_t slot = g % C::kSlots;
+      ok = wait(&bars.full[0][slot], (g / C::kSlots) & 1);
+      if (!ok) break;
+      if (k >= n_mine) {
+        mbar_arrive(&bars.empty[0][slot]);
+        continue;
+      }
+      if (n_s >= 2) ok = wait(&bars.pv_done[m][n_s & 1], ((n_s - 2) >> 1) & 1);
+      if (!ok) break;
       fence_after();
-      const uint32_t k_lo = desc_lo(ring + n % C::kSlots * C::kTile + (x & 1) * 8192, 0);
+      const uint32_t k_lo = desc_lo(base + C::kOffK + slot * C::kTile, 0);
       const uint32_t dS = tmem + kColS(m) + (n_s & 1) * 64;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk / 4) * (kHalf >> 4) + (kk % 4) * 2;
-        mma_bf16(dS, (uint64_t)hi << 32 | (q_lo + off), (uint64_t)hi << 32 | (k_lo + off), id_s, kk > 0);
+        const uint32_t in = (kk % 4) * 2;  // 16 columns further in a 64-column half
+        mma_bf16(dS, (uint64_t)hi << 32 | (q_lo + (kk / 4) * (kQHalf >> 4) + in),
+                 (uint64_t)hi << 32 | (k_lo + (kk / 4) * (kHalf >> 4) + in), id, kk > 0);
       }
       mma_commit(&bars.s_full[m][n_s & 1]);
-      if ((x & 1) || x == to - 1) mma_commit(&bars.empty[n % C::kSlots]);
-      if (x == to - 1) mma_commit(&bars.q_free[m]);
+      mma_commit(&bars.empty[0][slot]);
+      if (k == n_mine - 1) mma_commit(&bars.q_free[m]);
       ++n_s;
-      return true;
-    };
-    auto issue_pv = [&](int x) {
-      const uint32_t n = 2 * (g + (x >> 1)) + 1;
-      if (!mbar_wait(&bars.p_full[m][n_pv & 1], (n_pv >> 1) & 1, &bars.abort, p.status, limit_ns()) || !landed(n)) return false;
+    }
+  }
+  if (units) mbar_wait(&bars.q_full[m], (units - 1) & 1, &bars.abort, nullptr, limit_ns(), false);  // no load is left
+  drain(bars, m);
+}
+
+// Issues O_m += P_m V of its tiles.
+template <int D>
+__device__ __forceinline__ void issue_outputs(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint32_t base,
+                                              uint32_t tmem, int m) {
+  using C = Cfg<D>;
+  constexpr uint32_t id = idesc_bf16(128, D, true);
+  constexpr uint32_t hi = desc_hi(1024);
+  const uint32_t dO = tmem + kColO(m);
+  uint32_t g = 0, n_pv = 0;  // ring's tiles, this M tile's tiles
+  bool ok = true;
+  Walk walk(p, plan, cost);
+  Piece s;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &bars.abort, p.status, limit_ns()); };
+  while (ok && walk.next(s)) {
+    const int n_mine = s.computed(m);
+    for (int k = 0; ok && k < s.e - s.a; ++k, ++g) {
+      const uint32_t slot = g % C::kSlots;
+      ok = wait(&bars.full[1][slot], (g / C::kSlots) & 1);
+      if (!ok) break;
+      if (k >= n_mine) {
+        mbar_arrive(&bars.empty[1][slot]);
+        continue;
+      }
+      if (s.ragged(s.key(s.a + k))) mbar_arrive(&bars.v_seen[m]);  // the softmax threads clear those keys
+      ok = wait(&bars.p_full[m][n_pv & 1], (n_pv >> 1) & 1);
+      if (!ok) break;
       fence_after();
       const uint32_t aP = tmem + kColS(m) + (n_pv & 1) * 64;
-      const uint32_t lo = desc_lo(ring + n % C::kSlots * C::kTile + (x & 1) * 8192, kHalf);  // MN-major V: the next 64 columns
-      if (x > from) mma_ts<true>(dO, aP, lo, hi, id_o);
-      else mma_ts<false>(dO, aP, lo, hi, id_o);
+      const uint32_t lo = desc_lo(base + C::kOffV + slot * C::kTile, kHalf);  // MN-major V: the next 64 columns
+      if (k > 0) mma_ts<true>(dO, aP, lo, hi, id);
+      else mma_ts<false>(dO, aP, lo, hi, id);
 #pragma unroll
-      for (int k = 1; k < 4; ++k) mma_ts<true>(dO, aP + k * 8, lo + k * (2048 >> 4), hi, id_o);
+      for (int kk = 1; kk < kBlk / 16; ++kk) mma_ts<true>(dO, aP + kk * 8, lo + kk * (2048 >> 4), hi, id);
       mma_commit(&bars.pv_done[m][n_pv & 1]);
-      if ((x & 1) || x == to - 1) mma_commit(&bars.empty[n % C::kSlots]);
+      mma_commit(&bars.empty[1][slot]);
       ++n_pv;
-      return true;
-    };
-    if (n_mine > 0) {
-      ok = mbar_wait(&bars.q_full[m], units & 1, &bars.abort, p.status, limit_ns());
-      ++units;
-      for (int x = from; ok && x < min(from + 2, to); ++x) ok = issue_s(x);
-      for (int x = from; ok && x < to; ++x) {
-        ok = issue_pv(x);
-        if (ok && x + 2 < to) ok = issue_s(x + 2);
-      }
     }
-    // tiles that are not this M tile's: its share of the slots is free once they have landed
-    for (int k = n_mine; ok && k < s.e - s.a; ++k) {
-      const uint32_t n = 2 * (g + k);
-      ok = landed(n) && landed(n + 1);
-      if (!ok) break;
-      mbar_arrive(&bars.empty[n % C::kSlots]);
-      mbar_arrive(&bars.empty[(n + 1) % C::kSlots]);
-    }
-    g += s.e - s.a;
   }
-  if (!ok) {  // no product still runs when the CTA frees its TMEM
-    mma_commit(&bars.drain[m]);
-    mbar_wait(&bars.drain[m], 0, &bars.abort, nullptr, limit_ns(), false);
-  }
+  drain(bars, 2 + m);
 }
 
 __device__ __forceinline__ float max64(const float (&v)[64]) {
@@ -489,6 +483,10 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+__device__ __forceinline__ void store16(void* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  *reinterpret_cast<uint4*>(dst) = make_uint4(a, b, c, d);
 }
 
 __device__ __forceinline__ uint32_t count_arrival(uint32_t* counter) {
@@ -556,22 +554,21 @@ __device__ void join(const ChunkParams& p, const Plan& plan, const Piece& s, int
 
 // Softmax and results of M tile m's rows, one a thread.  kAny: a cap, a bias or a scale that is not positive.
 template <int D, bool kAny>
-__device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint8_t* ring,
+__device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint8_t* sV,
                                             uint32_t tmem, int m, int warp, int lane) {
   using C = Cfg<D>;
   const int rl = (warp % 4) * 32 + lane;  // row of the M tile = TMEM lane
   const uint32_t lane_at = tmem + ((uint32_t)(warp % 4 * 32) << 16);
   const uint32_t tS = lane_at + kColS(m), tO = lane_at + kColO(m);
   const float mul = p.scale * kLog2e;
+  const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // else 16-byte stores
   const Scorer score(p);
-  uint32_t g = 0, done = 0, posts = 0;  // ring's tiles, this M tile's steps
+  uint32_t g = 0, done = 0, posts = 0, cleared = 0;  // ring's tiles, this M tile's tiles
   bool ok = true;
   Walk walk(p, plan, cost);
   Piece s;
   while (ok && walk.next(s)) {
     const int n_mine = s.computed(m);
-    int from, to;
-    s.steps(p, m, from, to);
     const int tok = rl / p.G, head = s.kvh * p.G + rl % p.G;
     const bool valid = tok < s.tokens[m];
     const int first = s.pos0 + m * (128 / p.G);      // position of the M tile's first token
@@ -579,8 +576,8 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
     const int pos = valid ? first + tok : -1;
     const float slope = kAny && p.slopes && valid ? slope_of(p.slopes, head) : 0.f;
     float top = kNoScore, sum = 0.f;
-    for (int x = from; x < to; ++x, ++done) {
-      const int tile0 = s.key(s.a + (x >> 1)), t0 = tile0 + (x & 1) * 64;
+    for (int k = 0; k < n_mine; ++k, ++done) {
+      const int t0 = s.key(s.a + k);
       const uint32_t tB = tS + (done & 1) * 64;
       ok = mbar_wait_warp(&bars.s_full[m][done & 1], (done >> 1) & 1, &bars.abort, p.status, limit_ns());
       if (!ok) break;
@@ -609,7 +606,7 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
           for (int e = 0; e < 16; ++e) sv[c + e] = p.slopes ? fmaf(slope, (float)(t0 + c + e - pos), y[e]) : y[e];
         }
       }
-      // rows that do not see all of the step's keys
+      // rows that do not see all of the tile's keys
       if (t0 + 63 > first || (p.window > 0 && last - t0 >= p.window)) {
         const int most = min(pos - t0, 64);  // keys up to it
         const int least = p.window > 0 && pos >= t0 ? max(-1, min(pos - t0 - p.window + 1, 64)) : -1;  // from it on
@@ -619,55 +616,66 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
           if (!(c <= most && (c >= least || c < kept))) sv[c] = -INFINITY;
       }
       // keys that no row of the unit sees leave V
-      if ((x == from || (x & 1) == 0) && (tile0 + kBlk - 1 > s.last || tile0 < s.lo)) {
-        const int t = tile0 + rl;
-        const uint32_t n = 2 * (g + (x >> 1)) + 1;
-        ok = mbar_wait_warp(&bars.full[n % C::kSlots], (n / C::kSlots) & 1, &bars.abort, p.status, limit_ns());
+      if (s.ragged(t0)) {
+        const uint32_t slot = (g + k) % C::kSlots;
+        ok = mbar_wait_warp(&bars.v_seen[m], cleared & 1, &bars.abort, p.status, limit_ns());
         if (!ok) break;
-        if (t > s.last || (t < s.lo && t >= s.sink)) {
-          uint4* row = reinterpret_cast<uint4*>(ring + n % C::kSlots * C::kTile + rl * 128);
+        ++cleared;
+        const int t = t0 + rl % kBlk, h = rl / kBlk;
+        if (h < D / 64 && (t > s.last || (t < s.lo && t >= s.sink))) {
+          uint4* row = reinterpret_cast<uint4*>(sV + slot * C::kTile + h * kHalf + rl % kBlk * 128);
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int y = 0; y < 8; ++y) row[h * (kHalf / 16) + y] = make_uint4(0, 0, 0, 0);
+          for (int y = 0; y < 8; ++y) row[y] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
+        __syncwarp();
       }
-      const float mx = kAny ? max64(sv) : max64(sv) * mul;
-      const float now = fmaxf(top, mx);
-      const bool grow = now > top + kLag;
-      if (x > from && __any_sync(0xffffffffu, grow)) {
-        ok = mbar_wait_warp(&bars.pv_done[m][(done - 1) & 1], ((done - 1) >> 1) & 1, &bars.abort, p.status, limit_ns());
-        if (!ok) break;
-        fence_after();
-        const float alpha = grow ? exp2_approx(top - now) : 1.f;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(tO + c, r);
-          tmem_ld_wait(r);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-          tmem_st32(tO + c, r);
-        }
-      }
-      if (grow) {
-        sum *= exp2_approx(top - now);
-        top = now;
-      }
+      // Weights against the reference as it is.  It may lie below the maximum as long as their sum stays below 2^20:
+      // floats do not mind.  Past that, and in a unit's first tile, it becomes the maximum and the weights are taken again.
       const float f = kAny ? 1.f : mul;
-      const uint64_t sc2 = pack_f32x2(f, f), neg2 = pack_f32x2(-top, -top);
-      uint64_t acc0 = 0, acc1 = 0;
+      const uint64_t sc2 = pack_f32x2(f, f);
       uint32_t pk[32];
+      float tile_sum;
+      auto weigh = [&]() {
+        const uint64_t neg2 = pack_f32x2(-top, -top);
+        uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        float e0, e1;
-        exp2_pair(sv[2 * c], sv[2 * c + 1], sc2, neg2, e0, e1);
-        if (c & 1) acc1 = add_f32x2(acc1, pack_f32x2(e0, e1)); else acc0 = add_f32x2(acc0, pack_f32x2(e0, e1));
-        pk[c] = pack_bf16(e0, e1);
+        for (int c = 0; c < 32; ++c) {
+          float e0, e1;
+          exp2_pair(sv[2 * c], sv[2 * c + 1], sc2, neg2, e0, e1);
+          if (c & 1) acc1 = add_f32x2(acc1, pack_f32x2(e0, e1)); else acc0 = add_f32x2(acc0, pack_f32x2(e0, e1));
+          pk[c] = pack_bf16(e0, e1);
+        }
+        tile_sum = sum_f32x2(add_f32x2(acc0, acc1));
+      };
+      bool grow = k == 0;
+      if (k > 0) {
+        weigh();
+        grow = valid && !(tile_sum <= kMost);
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        const float now = grow ? fmaxf(top, max64(sv) * f) : top;
+        const float alpha = exp2_approx(top - now);  // 0 without a score before
+        if (k > 0) {
+          ok = mbar_wait_warp(&bars.pv_done[m][(done - 1) & 1], ((done - 1) >> 1) & 1, &bars.abort, p.status, limit_ns());
+          if (!ok) break;
+          fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tO + c, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+            tmem_st32(tO + c, r);
+          }
+        }
+        sum *= alpha;
+        top = now;
+        weigh();
       }
       tmem_st32(tB, pk);
-      sum += sum_f32x2(add_f32x2(acc0, acc1));
+      sum += tile_sum;
       tmem_st_wait();
       fence_before();
       mbar_arrive(&bars.p_full[m][done & 1]);
@@ -696,9 +704,15 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 w[e] = pack_bf16(__uint_as_float(r[16 * x + 2 * e]) * f, __uint_as_float(r[16 * x + 2 * e + 1]) * f);
-              store32(dst + (c + 16 * x) * 2, w);
+              if (wide) {
+                store32(dst + (c + 16 * x) * 2, w);
+              } else {
+                store16(dst + (c + 16 * x) * 2, w[0], w[1], w[2], w[3]);
+                store16(dst + (c + 16 * x) * 2 + 16, w[4], w[5], w[6], w[7]);
+              }
             }
           }
+          __syncwarp();
         }
         if (valid && p.lse) p.lse[at] = (top + log2f(sum)) * kLn2;
         fence_before();
@@ -717,6 +731,7 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
           for (int c = 0; c < D; c += 8) store32(p.part_o + row * D + c, zero);
         }
       }
+      __syncwarp();
       if (n_mine > 0) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -732,6 +747,7 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
               store32(p.part_o + row * D + c + 8 * x, w);
             }
           }
+          __syncwarp();
         }
         fence_before();
       }
@@ -766,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ Plan plan;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  uint8_t* ring = raw + (base - smem_u32(raw)) + C::kOffRing;
+  uint8_t* sV = raw + (base - smem_u32(raw)) + C::kOffV;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (p.cu && p.status && blockIdx.x == 0) {
     ChunkOf c;
@@ -777,8 +793,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (plan.x0 >= plan.x1) return;  // all threads, before anything is set up
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 2);
+      for (int v = 0; v < 2; ++v) {
+        mbar_init(&bars.full[v][i], 1);
+        mbar_init(&bars.empty[v][i], 2);
+      }
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&bars.q_full[m], 1);
@@ -788,7 +806,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars.p_full[m][x], 128);
         mbar_init(&bars.pv_done[m][x], 1);
       }
+      mbar_init(&bars.v_seen[m], 1);
       mbar_init(&bars.drain[m], 1);
+      mbar_init(&bars.drain[2 + m], 1);
     }
     mbar_init(&bars.posted, 256);
     mbar_init(&bars.decided, 1);
@@ -804,20 +824,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = bars.tmem;
-  // registers: 256 threads x 96 + 256 x 160 = 512 x 128, what the block was launched with
+  // registers: 256 threads x 72 + 256 x 184 = 512 x 128, what the block was launched with
   if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < 4) {
-      run_producer<D>(p, plan, cost, maps, bars, base + C::kOffRing, warp, lane);
+      run_producer<D>(p, plan, cost, maps, bars, base, warp, lane);
     } else if (warp < 6) {
-      if (lane == 0) run_issuer<D>(p, plan, cost, bars, base, tmem, warp - 4);
-    } else if (warp == 6) {
-      if (lane == 0) run_q_loader<D>(p, plan, cost, maps, bars, base);
+      if (lane == 0) issue_scores<D>(p, plan, cost, maps, bars, base, tmem, warp - 4);
+    } else {
+      if (lane == 0) issue_outputs<D>(p, plan, cost, bars, base, tmem, warp - 6);
     }
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    run_softmax<D, kAny>(p, plan, cost, bars, ring, tmem, (warp - 8) / 4, warp, lane);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    run_softmax<D, kAny>(p, plan, cost, bars, sV, tmem, (warp - 8) / 4, warp, lane);
   }
   fence_before();
   __syncthreads();
@@ -864,7 +884,7 @@ int launch(const ChunkParams& p, const Maps& maps, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(chunk_tc_kernel<D, kAny>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(chunk_tc_kernel)");
-  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, 2, 4);
+  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, 4, 8);
   TV_LAUNCH_CHECK("chunk_tc_kernel");
   return TV_OK;
 }

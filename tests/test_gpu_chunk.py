@@ -300,6 +300,39 @@ def test_any_grid(ctas):
     _check(c, out, lse, True)
 
 
+@pytest.mark.parametrize("D,G,bs", [(128, 4, 16), (64, 4, 64), (128, 16, 8)])
+def test_long_runs_of_a_cta(D, G, bs):
+    """Few CTAs: hundreds of tiles each, half of an M tile pair idle for whole requests, and then not."""
+    rng = np.random.default_rng(D + G)
+    c = _case(rng.integers(500, 4000, size=24), rng.choice([1, 3, 30, 40, 70, 200], size=24), 2 * G, 2, D, "bf16", bs, seed=9)
+    for ctas in (1, 3):
+        out, lse, status = _run(c, num_ctas=ctas)
+        assert status == 0
+        _check(c, out, lse, True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_output_on_a_16_byte_boundary(D):
+    c = _case([30, 200], [40, 70], 8, 2, D, "bf16", 16)
+    want, _, _ = _run(c)
+    room = torch.zeros(c["q"].numel() + 8, device="cuda", dtype=torch.bfloat16)
+    out = room[8:].view(c["q"].shape)
+    capi.tv_chunk_attn(c["q"], c["kc"], c["vc"], c["table"], c["lens"], cu_new=c["cu"], out=out)
+    assert out.data_ptr() % 32 == 16 and torch.equal(out, want) and not room[:8].any()
+
+
+def test_scores_that_rise_along_the_keys():
+    """Every tile's scores lie far above the last one's: the reference of the weights has to follow."""
+    c = _case([0], [300], 4, 1, 128, "bf16", 16, poison=False)
+    c["q"] = torch.ones_like(c["q"])
+    ramp = torch.arange(300, device="cuda", dtype=torch.float32) * 0.25
+    t = torch.arange(300, device="cuda")
+    c["kc"][c["table"][0].long()[t // 16], :, t % 16] = ramp[:, None, None].expand(300, 1, 128).bfloat16()
+    out, lse, status = _run(c)
+    assert status == 0
+    _check(c, out, lse, True)
+
+
 def test_same_bits_again_and_counters_left_zero():
     c = _case([4000, 10, 900], [60, 300, 3], 8, 2, 128, "bf16", 16, seed=5)
     ws = capi.alloc_workspace(capi.tv_chunk_attn_workspace_size(8, 2, 128, torch.bfloat16))
