@@ -12,7 +12,8 @@
 // * S_m = Q_m K^T (128 x 64, both operands from shared memory) and O_m += P_m V
 //   (P_m from TMEM, bf16, over S_m's columns), issued by a thread each.  Each M
 //   tile has two S buffers, so the products of the next tile and of the other M
-//   tile run while a tile's softmax does.
+//   tile run while a tile's softmax does.  (One S buffer, freed once it is in
+//   registers, and two for P: 6.0 against 5.7 ms.)
 //   S_0 2 x 64 | S_1 2 x 64 | O_0 128 | O_1 128 columns fill the TMEM.
 // * Softmax: a thread per row, against a reference that is the first tile's
 //   maximum and moves, with O rescaled in TMEM, only when weights pass 2^20; so
@@ -32,6 +33,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_score.cuh"
 #include "chunk.h"
@@ -52,14 +54,15 @@ template <int D>
 struct Cfg {
   static constexpr int kQTile = D / 64 * kQHalf;
   static constexpr int kTile = D / 64 * kHalf;     // bytes of a K or V tile
-  static constexpr int kSlots = D == 128 ? 5 : 8;  // of K, and of V
+  static constexpr int kSlots = D == 128 ? 4 : 8;  // of K, and of V
   static constexpr int kOffK = 2 * kQTile;         // behind Q_0, Q_1
   static constexpr int kOffV = kOffK + kSlots * kTile;
-  static constexpr int kSmem = kOffV + kSlots * kTile + 1024;
+  static constexpr int kOffOut = kOffV + kSlots * kTile;  // 4 KB a softmax warp: 32 rows of 64 output columns
+  static constexpr int kSmem = kOffOut + 8 * 4096 + 1024;
 };
 static_assert(Cfg<128>::kSmem <= 227 * 1024 - 1024 && Cfg<64>::kSmem <= 227 * 1024 - 1024, "fits beside the barriers");
 
-constexpr uint32_t kColS(int m) { return m * 128; }
+__host__ __device__ constexpr uint32_t kColS(int m, uint32_t tile) { return m * 128 + (tile & 1) * 64; }
 constexpr uint32_t kColO(int m) { return 256 + m * 128; }
 
 struct Bars {
@@ -73,6 +76,8 @@ struct Bars {
 
 struct Maps {
   CUtensorMap k, v, q;
+  CUtensorMap out;  // boxes of a warp's 32 rows x 64 columns
+  int out_tokens;   // of such a box, 0: the group does not fit one and rows are stored directly
 };
 
 #ifdef TV_TEST_HOOKS
@@ -170,8 +175,12 @@ struct Plan {
   int64_t at;             // where it starts
 };
 
-__device__ __forceinline__ int64_t run_start(int64_t c, int64_t total, int64_t ctas) { return c * total / ctas; }
-__device__ __forceinline__ int64_t run_of(int64_t x, int64_t total, int64_t ctas) { return ((x + 1) * ctas - 1) / total; }
+// a / b, a >= 0, b > 0, without a division of 64 bits where 32 do
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t run_start(int64_t c, int64_t total, int64_t ctas) { return divide(c * total, ctas); }
+__device__ __forceinline__ int64_t run_of(int64_t x, int64_t total, int64_t ctas) { return divide((x + 1) * ctas - 1, total); }
 
 // All threads of the CTA.
 __device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan) {
@@ -200,7 +209,7 @@ __device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan)
     if (w < warp) start += sums[w];
     total += sums[w];
   }
-  const int ctas = (int)min((int64_t)p.ctas, max((int64_t)1, total / least));
+  const int ctas = (int)min((int64_t)p.ctas, max((int64_t)1, divide(total, least)));
   const int c = blockIdx.x;
   const int64_t x0 = c < ctas ? run_start(c, total, ctas) : total;
   const int64_t x1 = c < ctas ? run_start(c + 1, total, ctas) : total;
@@ -221,7 +230,7 @@ __device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan)
     }
     at += r.before(lo, cost) * p.Hkv;
     const int one = r.tiles(lo) + cost;
-    plan.kvh = (int)((x0 - at) / one);
+    plan.kvh = (int)divide(x0 - at, one);
     plan.at = at + (int64_t)plan.kvh * one;
     plan.b = b;
     plan.i = lo;
@@ -261,21 +270,19 @@ struct Walk {
   int cost, b, i, kvh;
   int64_t at;
   Request r;
+  bool fresh = true;  // a new unit's tokens
 
   __device__ __forceinline__ Walk(const ChunkParams& p_, const Plan& plan_, int cost_)
       : p(p_), plan(plan_), cost(cost_), b(plan_.b), i(plan_.i), kvh(plan_.kvh), at(plan_.at) {
     r.set(p, b);
   }
-  // The next part with tiles in this CTA's run; false at its end.
+  // The next part with tiles in this CTA's run; false at its end.  s is the last one, from which the next KV head's differs
+  // little (code that runs once a unit is fetched anew each time: the whole of this took 2000 cycles a unit).
   __device__ __forceinline__ bool next(Piece& s) {
     while (at < plan.x1) {
-      const int tiles = r.tiles(i);
-      const int64_t real = at + cost;
-      const int64_t a = max((int64_t)0, plan.x0 - real), e = min((int64_t)tiles, plan.x1 - real);
-      const int j0 = i * r.step, n = min(r.step, r.c.n - j0), half = r.step / 2;
-      if (a < e) {
+      if (fresh) {
+        const int j0 = i * r.step, n = min(r.step, r.c.n - j0), half = r.step / 2;
         s.b = b;
-        s.kvh = kvh;
         s.s0 = r.c.s0 + j0;
         s.tokens[0] = min(n, half);
         s.tokens[1] = max(0, n - half);
@@ -284,17 +291,21 @@ struct Walk {
         s.lo = p.window > 0 ? max(0, max(0, s.pos0 + 1) - p.window) : 0;
         s.sink = min(p.n_sink, s.lo);
         s.lead = min((s.sink + kBlk - 1) / kBlk, s.lo / kBlk);
+        s.tiles = r.tiles(i);
         const int last0 = s.pos0 + s.tokens[0] - 1;
         s.count[0] = last0 < 0 ? 1 : s.lead + last0 / kBlk + 1 - s.lo / kBlk;
-        s.count[1] = s.tokens[1] > 0 ? tiles : 0;
-        s.a = (int)a;
-        s.e = (int)e;
-        s.tiles = tiles;
-        s.real = real;
+        s.count[1] = s.tokens[1] > 0 ? s.tiles : 0;
+        fresh = false;
       }
-      at += tiles + cost;
+      s.kvh = kvh;
+      s.real = at + cost;
+      const int64_t a = max((int64_t)0, plan.x0 - s.real), e = min((int64_t)s.tiles, plan.x1 - s.real);
+      s.a = (int)a;
+      s.e = (int)e;
+      at += s.tiles + cost;
       if (++kvh == p.Hkv) {
         kvh = 0;
+        fresh = true;
         if (++i == r.units) {
           i = 0;
           if (at < plan.x1)
@@ -409,7 +420,7 @@ __device__ __forceinline__ void issue_scores(const ChunkParams& p, const Plan& p
       if (!ok) break;
       fence_after();
       const uint32_t k_lo = desc_lo(base + C::kOffK + slot * C::kTile, 0);
-      const uint32_t dS = tmem + kColS(m) + (n_s & 1) * 64;
+      const uint32_t dS = tmem + kColS(m, n_s);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t in = (kk % 4) * 2;  // 16 columns further in a 64-column half
@@ -418,6 +429,11 @@ __device__ __forceinline__ void issue_scores(const ChunkParams& p, const Plan& p
       }
       mma_commit(&bars.s_full[m][n_s & 1]);
       mma_commit(&bars.empty[0][slot]);
+      if (k == 0 && s.kvh + 1 < p.Hkv) {  // the next unit's Q, most likely, on its way to L2
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tma_prefetch_3d(&maps.q, h * 64, (s.kvh + 1) * p.G, s.s0 + m * (128 / p.G));
+      }
       if (k == n_mine - 1) mma_commit(&bars.q_free[m]);
       ++n_s;
     }
@@ -453,7 +469,7 @@ __device__ __forceinline__ void issue_outputs(const ChunkParams& p, const Plan& 
       ok = wait(&bars.p_full[m][n_pv & 1], (n_pv >> 1) & 1);
       if (!ok) break;
       fence_after();
-      const uint32_t aP = tmem + kColS(m) + (n_pv & 1) * 64;
+      const uint32_t aP = tmem + kColS(m, n_pv);
       const uint32_t lo = desc_lo(base + C::kOffV + slot * C::kTile, kHalf);  // MN-major V: the next 64 columns
       if (k > 0) mma_ts<true>(dO, aP, lo, hi, id);
       else mma_ts<false>(dO, aP, lo, hi, id);
@@ -495,74 +511,85 @@ __device__ __forceinline__ uint32_t count_arrival(uint32_t* counter) {
   return before;
 }
 
-// Joins a split unit's pieces, in order, by the 8 softmax warps, a row at a time each: lane l has D / 32 of its outputs.
+// Joins a split unit's pieces, in order, by the 8 softmax warps: 8 neighbouring rows at a time, the lanes sharing their
+// outputs, the next piece on its way meanwhile.  (A row at a time, every trip to memory waited for: 45 us for 256 rows.)
 template <int D>
-__device__ void join(const ChunkParams& p, const Plan& plan, const Piece& s, int warp, int lane) {
-  constexpr int kE = D / 32;
+__device__ __noinline__ void join(const ChunkParams& p, const Plan& plan, const Piece& s, int warp, int lane) {
+  constexpr int kE = D / 32, kRows = 8;
+  using Part = typename std::conditional<kE == 4, float4, float2>::type;
   const int c0 = (int)run_of(s.real, plan.total, plan.ctas), c1 = (int)run_of(s.real + s.tiles - 1, plan.total, plan.ctas);
   const int n = c1 - c0 + 1, per = 128 / p.G;
-  for (int x = warp; x < (s.tokens[0] + s.tokens[1]) * p.G; x += 8) {
-    const int m = x >= per * p.G, row = m * 128 + x - m * per * p.G;
-    float top = kNoScore, sum = 0.f, o[kE] = {};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      float pm = kNoScore, pl = 0.f;
-      if (i < n) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + ((int64_t)(c0 + i) * 2 + (i == 0)) * 256 + row);
-        pm = ml.x, pl = ml.y;
-      }
-      float t = pm;
+  const int blocks0 = (s.tokens[0] * p.G + kRows - 1) / kRows, blocks = blocks0 + (s.tokens[1] * p.G + kRows - 1) / kRows;
+  // piece 0 lies in its CTA's second slot, the others in the first
+  const int64_t first = ((int64_t)c0 * 2 + 1) * 256, then = ((int64_t)c0 * 2 + 2) * 256;
+#pragma unroll 1
+  for (int blk = warp; blk < blocks; blk += 8) {
+    const int m = blk >= blocks0, row = (blk - (m ? blocks0 : 0)) * kRows;  // of the M tile
+    const int in_unit = m * 128 + row;
+    auto load = [&](int i, float2& ml, Part (&v)[kRows]) {
+      const int64_t at = (i == 0 ? first : then + (int64_t)(i - 1) * 512) + in_unit;
+      ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + lane % kRows);
+      const Part* src = reinterpret_cast<const Part*>(p.part_o + at * D) + lane;
 #pragma unroll
-      for (int w = 16; w; w /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
-      const float now = fmaxf(top, t), scale = exp2_approx(top - now);
+      for (int r = 0; r < kRows; ++r) v[r] = __ldcg(src + r * 32);
+    };
+    float top = kNoScore, sum = 0.f, o[kRows][kE] = {};
+    float2 ml;
+    Part v[kRows];
+    load(0, ml, v);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      float2 ml_next = ml;
+      Part v_next[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) v_next[r] = v[r];
+      if (i + 1 < n) load(i + 1, ml_next, v_next);
+      const float now = fmaxf(top, ml.x), keep = exp2_approx(top - now);
+      const float w = ml.y == 0.f ? 0.f : exp2_approx(ml.x - now);
+      sum = fmaf(sum, keep, w * ml.y);
       top = now;
-      const float w = pl == 0.f ? 0.f : exp2_approx(pm - now);
-      sum *= scale;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] *= scale;
-      const int here = min(32, n - i0);
-#pragma unroll 4
-      for (int k = 0; k < here; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k), lk = __shfl_sync(0xffffffffu, pl, k);
-        const float* src = p.part_o + (((int64_t)(c0 + i0 + k) * 2 + (i0 + k == 0)) * 256 + row) * D + lane * kE;
-        float v[kE];
-        if constexpr (kE == 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-          v[0] = y.x, v[1] = y.y;
-        }
-        sum = fmaf(wk, lk, sum);
-        if (wk != 0.f) {
+      for (int r = 0; r < kRows; ++r) {
+        const float kr = __shfl_sync(0xffffffffu, keep, r), wr = __shfl_sync(0xffffffffu, w, r);
+        const float* x = reinterpret_cast<const float*>(&v[r]);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) o[e] = fmaf(wk, v[e], o[e]);
-        }
+        for (int e = 0; e < kE; ++e) o[r][e] = fmaf(o[r][e], kr, wr == 0.f ? 0.f : wr * x[e]);  // else x may be anything
+        v[r] = v_next[r];
       }
+      ml = ml_next;
     }
     const float f = inverse(sum);
-    const int64_t at = ((int64_t)s.s0 + x / p.G) * p.Hq + s.kvh * p.G + x % p.G;
-    uint32_t out[kE / 2];
+    const int rows = s.tokens[m] * p.G - row;  // that are the unit's
+    auto out_row = [&](int r) {
+      return ((int64_t)s.s0 + m * per + (row + r) / p.G) * p.Hq + s.kvh * p.G + (row + r) % p.G;
+    };
+    if (lane < min(rows, kRows) && p.lse) p.lse[out_row(lane)] = (top + log2f(sum)) * kLn2;
 #pragma unroll
-    for (int e = 0; e < kE / 2; ++e) out[e] = pack_bf16(o[2 * e] * f, o[2 * e + 1] * f);
-    char* dst = p.out + (at * D + lane * kE) * 2;
-    if constexpr (kE == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-    else *reinterpret_cast<uint32_t*>(dst) = out[0];
-    if (p.lse && lane == 0) p.lse[at] = (top + log2f(sum)) * kLn2;
+    for (int r = 0; r < kRows; ++r) {
+      const float fr = __shfl_sync(0xffffffffu, f, r);
+      if (r >= rows) continue;
+      char* dst = p.out + (out_row(r) * D + lane * kE) * 2;
+      if constexpr (kE == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[r][0] * fr, o[r][1] * fr), pack_bf16(o[r][2] * fr, o[r][3] * fr));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[r][0] * fr, o[r][1] * fr);
+    }
   }
 }
 
 // Softmax and results of M tile m's rows, one a thread.  kAny: a cap, a bias or a scale that is not positive.
 template <int D, bool kAny>
-__device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& plan, int cost, Bars& bars, uint8_t* sV,
-                                            uint32_t tmem, int m, int warp, int lane) {
+__device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& plan, int cost, const Maps& maps, Bars& bars,
+                                            uint8_t* sV, uint32_t stage, uint32_t tmem, int m, int warp, int lane) {
   using C = Cfg<D>;
   const int rl = (warp % 4) * 32 + lane;  // row of the M tile = TMEM lane
   const uint32_t lane_at = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-  const uint32_t tS = lane_at + kColS(m), tO = lane_at + kColO(m);
+  const uint32_t tO = lane_at + kColO(m);
   const float mul = p.scale * kLog2e;
   const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // else 16-byte stores
   const Scorer score(p);
+  // factor of the cap's exponential where the cap is small enough for that form, else 0
+  const float cap_in = kAny && score.cap2 > 0.f && score.cap2 <= 128.f ? fminf(fmaxf(score.cap_mul, -0x1p100f), 0x1p100f) * (2.f * kLog2e) : 0.f;
   uint32_t g = 0, done = 0, posts = 0, cleared = 0;  // ring's tiles, this M tile's tiles
   bool ok = true;
   Walk walk(p, plan, cost);
@@ -576,17 +603,33 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
     const int pos = valid ? first + tok : -1;
     const float slope = kAny && p.slopes && valid ? slope_of(p.slopes, head) : 0.f;
     float top = kNoScore, sum = 0.f;
+    // The M tiles' softmaxes share the issue slots, their products the tensor pipe: out of step with each other they
+    // share better (a long prompt piece 5.30 -> 5.21 ms; 32 prompts of 512 tokens, with few tiles a unit, 170 -> 174 us).
+    if (m == 1 && n_mine >= 16) {
+      const long long from = clock64();
+      while (clock64() - from < 600) {
+      }
+    }
     for (int k = 0; k < n_mine; ++k, ++done) {
       const int t0 = s.key(s.a + k);
-      const uint32_t tB = tS + (done & 1) * 64;
+      const uint32_t tS = lane_at + kColS(m, done);
       ok = mbar_wait_warp(&bars.s_full[m][done & 1], (done >> 1) & 1, &bars.abort, p.status, limit_ns());
       if (!ok) break;
       fence_after();
+      // rows that do not see all of the tile's keys
+      const bool cut = t0 + kBlk - 1 > first || (p.window > 0 && last - t0 >= p.window);
+      uint64_t seen = ~0ull;
+      if (cut) {
+        auto below = [](int n) -> uint64_t { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; };
+        seen = below(min(pos - t0, 63) + 1);
+        if (p.window > 0 && pos - t0 >= p.window)  // not below the window, but for the kept first keys
+          seen &= ~below(min(pos - t0 - p.window, 63) + 1) | below(min(p.n_sink - t0, 64));
+      }
       float sv[64];
       {
         uint32_t r0[32], r1[32];
-        tmem_ld32(tB, r0);
-        tmem_ld32(tB + 32, r1);
+        tmem_ld32(tS, r0);
+        tmem_ld32(tS + 32, r1);
         tmem_ld_wait(r0);
         tmem_loaded(r1);
 #pragma unroll
@@ -596,24 +639,33 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
         }
       }
       if constexpr (kAny) {
+        if (cap_in > 0.f || cap_in < 0.f) {
+          // tanh y = 1 - 2 / (1 + e^2y): off by 2^-22 of the cap at most, which is 3e-5 here
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) {
-          float y[16];
+          for (int c = 0; c < 64; ++c) sv[c] = fmaf(rcp_approx(1.f + exp2_approx(sv[c] * cap_in)), -2.f * score.cap2, score.cap2);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = sv[c + e];
-          score(y);
+          for (int c = 0; c < 64; c += 16) {
+            float y[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sv[c + e] = p.slopes ? fmaf(slope, (float)(t0 + c + e - pos), y[e]) : y[e];
+            for (int e = 0; e < 16; ++e) y[e] = sv[c + e];
+            score(y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sv[c + e] = y[e];
+          }
+        }
+        if (p.slopes) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sv[c] = fmaf(slope, (float)(t0 + c - pos), sv[c]);
         }
       }
-      // rows that do not see all of the tile's keys
-      if (t0 + 63 > first || (p.window > 0 && last - t0 >= p.window)) {
-        const int most = min(pos - t0, 64);  // keys up to it
-        const int least = p.window > 0 && pos >= t0 ? max(-1, min(pos - t0 - p.window + 1, 64)) : -1;  // from it on
-        const int kept = max(-1, min(p.n_sink - t0, 64));  // or below it
+      if (cut) {
+        const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (!(c <= most && (c >= least || c < kept))) sv[c] = -INFINITY;
+        for (int c = 0; c < 32; ++c) {
+          if (!(lo & 1u << c)) sv[c] = -INFINITY;
+          if (!(hi & 1u << c)) sv[32 + c] = -INFINITY;
+        }
       }
       // keys that no row of the unit sees leave V
       if (s.ragged(t0)) {
@@ -648,33 +700,29 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
         }
         tile_sum = sum_f32x2(add_f32x2(acc0, acc1));
       };
-      bool grow = k == 0;
-      if (k > 0) {
-        weigh();
-        grow = valid && !(tile_sum <= kMost);
-      }
+      if (k == 0) top = fmaxf(top, max64(sv) * f);
+      weigh();
+      const bool grow = valid && k > 0 && tile_sum > kMost;
       if (__any_sync(0xffffffffu, grow)) {
         const float now = grow ? fmaxf(top, max64(sv) * f) : top;
         const float alpha = exp2_approx(top - now);  // 0 without a score before
-        if (k > 0) {
-          ok = mbar_wait_warp(&bars.pv_done[m][(done - 1) & 1], ((done - 1) >> 1) & 1, &bars.abort, p.status, limit_ns());
-          if (!ok) break;
-          fence_after();
+        ok = mbar_wait_warp(&bars.pv_done[m][(done - 1) & 1], ((done - 1) >> 1) & 1, &bars.abort, p.status, limit_ns());
+        if (!ok) break;
+        fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(tO + c, r);
-            tmem_ld_wait(r);
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tO + c, r);
+          tmem_ld_wait(r);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-            tmem_st32(tO + c, r);
-          }
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+          tmem_st32(tO + c, r);
         }
         sum *= alpha;
         top = now;
         weigh();
       }
-      tmem_st32(tB, pk);
+      tmem_st32(tS, pk);
       sum += tile_sum;
       tmem_st_wait();
       fence_before();
@@ -692,7 +740,41 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
         const int64_t at = ((int64_t)s.s0 + m * (128 / p.G) + tok) * p.Hq + head;
         const float f = inverse(sum);
         char* dst = p.out + at * D * 2;
+        if (maps.out_tokens && __all_sync(0xffffffffu, valid)) {
+          // whole warps: 64 columns at a time through shared memory, stored by TMA (rows of their own, stored directly,
+          // touch 32 lines an instruction: 3600 cycles a unit, 1500 this way)
+          const uint32_t mine = stage + (warp - 8) * 4096;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tO + c, r);
+            tmem_ld_wait(r);
+            if (c % 64 == 0) {
+              if (lane == 0) tma_store_read_wait();  // the last box has left
+              __syncwarp();
+            }
 #pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(__uint_as_float(r[8 * x + 2 * e]) * f, __uint_as_float(r[8 * x + 2 * e + 1]) * f);
+              sts16(mine + lane * 128 + (((c % 64 / 8 + x) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            if (c % 64 == 32) {
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) {
+                const int row = (warp % 4) * 32;  // of the M tile
+                tma_store_3d(&maps.out, mine, c - 32, s.kvh * p.G + row % p.G, s.s0 + m * (128 / p.G) + row / p.G);
+              }
+            }
+          }
+          if (p.lse) p.lse[at] = (top + log2f(sum)) * kLn2;
+          fence_before();
+          continue;
+        }
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t r[32];
           tmem_ld32(tO + c, r);
@@ -772,6 +854,8 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
       }
     }
   }
+  if (lane == 0) tma_store_wait();  // outputs are written when the CTA ends
+  __syncwarp();
 }
 
 template <int D, bool kAny>
@@ -837,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    run_softmax<D, kAny>(p, plan, cost, bars, sV, tmem, (warp - 8) / 4, warp, lane);
+    run_softmax<D, kAny>(p, plan, cost, maps, bars, sV, base + C::kOffOut, tmem, (warp - 8) / 4, warp, lane);
   }
   fence_before();
   __syncthreads();
@@ -876,6 +960,19 @@ int encode(EncodeTiled fn, CUtensorMap* map, const void* ptr, int rank, const cu
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(TV_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
   return TV_OK;
+}
+
+// Boxes of a softmax warp's 32 rows, where rows of one token fill them: 32 / G tokens, or 32 heads of one.
+int encode_out(EncodeTiled fn, Maps* maps, const ChunkParams& p, int D) {
+  maps->out_tokens = p.G <= 32 && 32 % p.G == 0 ? 32 / p.G : p.G % 32 == 0 ? 1 : 0;
+  if (!maps->out_tokens) {
+    maps->out = maps->q;
+    return TV_OK;
+  }
+  const cuuint64_t row = (cuuint64_t)D * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.T}, strides[2] = {row, row * p.Hq};
+  const cuuint32_t box[3] = {64, (cuuint32_t)std::min(p.G, 32), (cuuint32_t)maps->out_tokens};
+  return encode(fn, &maps->out, p.out, 3, dims, strides, box, "out");
 }
 
 template <int D, bool kAny>
@@ -924,6 +1021,7 @@ int launch_chunk_tc(const ChunkParams& p, int D, cudaStream_t stream) {
     const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
     if (int rc = encode(fn, &maps.q, p.q, 3, dims, strides, box, "q")) return rc;
   }
+  if (int rc = encode_out(fn, &maps, p, D)) return rc;
   // the plain form masks before it scales: its factor has to keep -inf what it is
   const bool any = p.softcap > 0.f || p.slopes || !(p.scale * kLog2e >= FLT_MIN);
   if (D == 64) return any ? launch<64, true>(p, maps, stream) : launch<64, false>(p, maps, stream);
