@@ -171,6 +171,7 @@ struct Request {
 struct Plan {
   int64_t x0, x1, total;  // this CTA's run of [0, total)
   int ctas;               // that take part
+  int whole;              // a unit of this length or less is not cut: it goes to the CTA whose run it starts in
   int b, i, kvh;          // the unit that x0 is in
   int64_t at;             // where it starts
 };
@@ -240,6 +241,9 @@ __device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan)
     plan.x1 = x1;
     plan.total = total;
     plan.ctas = ctas;
+    // A cut costs about 15 tiles (the pieces written and read back, the wait for the last), an uneven run up to one unit:
+    // 32 prompts of 1-1023 tokens 202 -> 180 us.
+    plan.whole = (int)min((int64_t)24, divide(total, ctas) / 4);
   }
   __syncthreads();
 }
@@ -299,7 +303,11 @@ struct Walk {
       }
       s.kvh = kvh;
       s.real = at + cost;
-      const int64_t a = max((int64_t)0, plan.x0 - s.real), e = min((int64_t)s.tiles, plan.x1 - s.real);
+      int64_t a = max((int64_t)0, plan.x0 - s.real), e = min((int64_t)s.tiles, plan.x1 - s.real);
+      if (s.tiles + cost <= plan.whole) {
+        a = 0;
+        e = at >= plan.x0 ? s.tiles : 0;  // at < x1 here
+      }
       s.a = (int)a;
       s.e = (int)e;
       at += s.tiles + cost;
