@@ -43,21 +43,11 @@ __device__ __forceinline__ void unpack(const Raw<kVec<T>>& r, float (&v)[8]) {
   Vec8<T>::load(reinterpret_cast<const T*>(&r), v);
 }
 
-template <int N>
-__device__ __forceinline__ Raw<N> pick(bool first, const Raw<N>& a, const Raw<N>& b) {
-  Raw<N> r;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    r.v[i] = make_uint4(first ? a.v[i].x : b.v[i].x, first ? a.v[i].y : b.v[i].y, first ? a.v[i].z : b.v[i].z,
-                        first ? a.v[i].w : b.v[i].w);
-  return r;
-}
-
-// One head's row: a lane's two runs of 8, normalised with the weights w1, w2 and rotated.
+// One head's row: a lane's two runs of 8, normalised with the weights at w (null: not), runs lo and hi of them, and rotated.
 template <typename T, int D>
-__device__ __forceinline__ void finish_row(const NormParams& p, bool norm, bool turn, const Raw<kVec<T>>& x1,
-                                           const Raw<kVec<T>>& x2, const Raw<kVec<T>>& w1, const Raw<kVec<T>>& w2,
-                                           const float (&co)[8], const float (&si)[8], float (&a)[8], float (&d)[8]) {
+__device__ __forceinline__ void finish_row(const NormParams& p, const char* w_at, int64_t lo, int64_t hi, bool turn,
+                                           const Raw<kVec<T>>& x1, const Raw<kVec<T>>& x2, const float (&co)[8],
+                                           const float (&si)[8], float (&a)[8], float (&d)[8]) {
   unpack<T>(x1, a);
   unpack<T>(x2, d);
   float sum = 0.f;
@@ -65,13 +55,13 @@ __device__ __forceinline__ void finish_row(const NormParams& p, bool norm, bool 
   for (int e = 0; e < 8; ++e) sum += a[e] * a[e] + d[e] * d[e];
 #pragma unroll
   for (int o = 1; o < D / 16; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (norm) {
+  if (w_at) {  // read for each head (they stay in L1): kept in registers they left a third less room for the rows
     const float f = 1.f / sqrtf(sum * (1.f / D) + p.eps);
     float w[8];
-    unpack<T>(w1, w);
+    unpack<T>(*reinterpret_cast<const Raw<kVec<T>>*>(w_at + lo), w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) a[e] = a[e] * f * w[e];
-    unpack<T>(w2, w);
+    unpack<T>(*reinterpret_cast<const Raw<kVec<T>>*>(w_at + hi), w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] = d[e] * f * w[e];
   }
@@ -90,7 +80,7 @@ __device__ __forceinline__ void finish_row(const NormParams& p, bool norm, bool 
 
 // One warp per (token, slice of its heads), as in kv_append.cu; the warps behind the tokens' count the new lengths.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const __grid_constant__ NormParams np) {
+__global__ void __launch_bounds__(kThreads, 5) kv_append_norm_kernel(const __grid_constant__ NormParams np) {
   const AppendParams& p = np.a;
   constexpr int kChunks = D / 16;
   constexpr int kHeads = 32 / kChunks;          // heads a warp covers at once
@@ -128,15 +118,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const __grid_c
   }
   const int64_t lo = e1 * sizeof(T), hi = e2 * sizeof(T);
   using Run = Raw<kVec<T>>;
-  Run qw1{}, qw2{}, kw1{}, kw2{};
-  if (np.q_weight) {
-    qw1 = *reinterpret_cast<const Run*>(np.q_weight + lo);
-    qw2 = *reinterpret_cast<const Run*>(np.q_weight + hi);
-  }
-  if (np.k_weight) {
-    kw1 = *reinterpret_cast<const Run*>(np.k_weight + lo);
-    kw2 = *reinterpret_cast<const Run*>(np.k_weight + hi);
-  }
   const int Hq = p.q ? p.Hq : 0;
   const int H = Hq + 2 * p.Hkv;
   const int rounds = (H + kHeads - 1) / kHeads;
@@ -165,8 +146,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const __grid_c
       const int h = h0 + u * kHeads;
       const bool is_q = h < Hq, is_v = h >= Hq + p.Hkv;
       float y1[8], y2[8];
-      finish_row<T, D>(np, is_q ? np.q_weight != nullptr : np.k_weight && !is_v, turn, x1[u], x2[u], pick(is_q, qw1, kw1),
-                       pick(is_q, qw2, kw2), co, si, y1, y2);
+      finish_row<T, D>(np, is_q ? np.q_weight : is_v ? nullptr : np.k_weight, lo, hi, turn, x1[u], x2[u], co, si, y1, y2);
       if (h >= h_end || (!is_q && !placed)) continue;
       char* dst;
       if (is_q) {
