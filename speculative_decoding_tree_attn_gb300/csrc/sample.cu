@@ -18,10 +18,15 @@
 // exponential, ACM TOMS 15, 1989); |t| < 0.0055, so that only its first term needs
 // two floats.
 //
-// A limit is found by a histogram of the weights' logarithms (128 bins to a factor
-// of 2): counts and 14-bit masses by bin tell the bin that the limit is in, exact
-// sums confirm it, and the few elements of that bin are ranked by comparing each
-// with each.
+// A top_k limit: the threads' own largest logits give a bar that top_k elements reach
+// and few more; those are sorted in one CTA.  Else a limit is found by a
+// histogram of the weights' logarithms (128 bins to a factor of 2), whose
+// approximate masses tell the bin that it is in; one pass of exact sums confirms
+// it and collects that bin's elements, which are sorted.
+//
+// A row is read again for each pass, from L2: bound by the instructions of the
+// exact pass (45 an element of float32, 15 of bf16) where there is no top_k, by
+// the passes' exchanges where there are few rows.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -37,8 +42,7 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 4096, kPerOctave = 128;
-constexpr int kList = 512;       // elements that are ranked by comparing
-constexpr int kSorted = 1024;    // that are sorted
+constexpr int kList = 1024;      // elements that are sorted
 constexpr int kChunk = 256;      // elements whose kept mass is one number
 constexpr int kMaxV = 1 << 20;   // sums stay below 2^64
 constexpr int kMaxCluster = 8;
@@ -141,15 +145,8 @@ struct Shared {
   unsigned long long totals[2][2];  // exchanged with the cluster's CTAs, in turns
   uint32_t count[kBins], mass[kBins];
   unsigned long long chunk[kMaxV / kMaxCluster / kChunk + 1];  // kept mass
-  union {
-    struct {
-      unsigned long long list_place[kList], list_weight[kList];
-      unsigned long long all_place[kList], all_weight[kList];
-    };
-    struct {
-      unsigned long long place[kSorted], weight[kSorted];
-    } sorted;
-  };
+  unsigned long long list_place[kList], list_weight[kList];  // of this CTA
+  unsigned long long all_place[kList], all_weight[kList];    // of the cluster
   uint32_t listed, gathered;
   unsigned long long limit, total;
   unsigned long long table[2][kTableSize];  // weights of bf16 logits, by sign and magnitude
@@ -338,11 +335,42 @@ struct Row {
     __syncthreads();
     return sh.bin;
   }
+  // Mass of the bins above one, by their approximate masses; the same in every CTA.
+  __device__ unsigned long long mass_above(int bin, int unit_bits) {
+    unsigned long long a = 0;
+    for (int b = threadIdx.x; b < bin; b += kThreads) a += (unsigned long long)sh.mass[b] << unit_bits >> (b / kPerOctave);
+    a = warp_sum(a);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh.warp_sums[threadIdx.x / 32][0] = a;
+    __syncthreads();
+    a = 0;
+    for (int k = 0; k < kWarps; ++k) a += sh.warp_sums[k][0];
+    __syncthreads();
+    return a;
+  }
   // Next bin in a direction with anything in it
   __device__ int next_bin(int b, int step, int last_bin) const {
     for (b += step; b >= 0 && b <= last_bin; b += step)
       if (sh.count[b]) return b;
     return -1;
+  }
+
+  // Least and largest place of a bin's kept elements from `from` on.
+  template <class Kept>
+  __device__ void range_of(const Scale& sc, int bin, unsigned long long from, unsigned long long& lo, unsigned long long& hi,
+                           Kept kept) {
+    unsigned long long least = 0, most = 0;  // least: inverted
+    each([&](float x, int i) {
+      const float y = sc.log2w(x);
+      if (bin_of(y) != bin || !kept(x, y)) return;
+      const unsigned long long at = place(x, i);
+      if (at < from) return;
+      least = max(least, ~at);
+      most = max(most, at);
+    });
+    reduce<true>(least, most);
+    lo = ~least;
+    hi = most;
   }
 
   // Kept elements of bin `bin` with lo <= place <= hi, which are kList at most, in every CTA's list; their number.
@@ -381,21 +409,27 @@ struct Row {
 
 // Sorts n places in descending order, their weights along; n2 >= n is a power of two.
 __device__ void sort_places(Shared& sh, int n, int n2) {
-  for (int i = n + threadIdx.x; i < n2; i += kThreads) sh.sorted.place[i] = 0, sh.sorted.weight[i] = 0;
+  for (int i = n + threadIdx.x; i < n2; i += kThreads) sh.all_place[i] = 0, sh.all_weight[i] = 0;
   for (int k = 2; k <= n2; k *= 2)
     for (int j = k / 2; j > 0; j /= 2) {
       __syncthreads();
       for (int x = threadIdx.x; x < n2 / 2; x += kThreads) {
         const int lo = 2 * x - (x & (j - 1)), hi = lo + j;
-        const unsigned long long a = sh.sorted.place[lo], b = sh.sorted.place[hi];
+        const unsigned long long a = sh.all_place[lo], b = sh.all_place[hi];
         if ((a < b) == ((lo & k) == 0)) {
-          sh.sorted.place[lo] = b, sh.sorted.place[hi] = a;
-          const unsigned long long w = sh.sorted.weight[lo];
-          sh.sorted.weight[lo] = sh.sorted.weight[hi], sh.sorted.weight[hi] = w;
+          sh.all_place[lo] = b, sh.all_place[hi] = a;
+          const unsigned long long w = sh.all_weight[lo];
+          sh.all_weight[lo] = sh.all_weight[hi], sh.all_weight[hi] = w;
         }
       }
     }
   __syncthreads();
+}
+
+__device__ void sort_list(Shared& sh, int n) {
+  int n2 = 2;
+  while (n2 < n) n2 *= 2;
+  sort_places(sh, n, n2);
 }
 
 // First i < n at which the running sum of the sorted weights exceeds goal, in sh.bin (n - 1 without one), and the running
@@ -403,7 +437,7 @@ __device__ void sort_places(Shared& sh, int n, int n2) {
 __device__ unsigned long long scan_weights(Shared& sh, int n, unsigned long long goal, bool find) {
   const int per = (n + kThreads - 1) / kThreads, i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
   unsigned long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += sh.sorted.weight[i];
+  for (int i = i0; i < i1; ++i) mine += sh.all_weight[i];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   unsigned long long run = mine;
 #pragma unroll
@@ -424,7 +458,7 @@ __device__ unsigned long long scan_weights(Shared& sh, int n, unsigned long long
   if (find) {
     if (run <= goal && run + mine > goal) {
       for (int i = i0; i < i1; ++i) {
-        run += sh.sorted.weight[i];
+        run += sh.all_weight[i];
         if (run > goal) {
           sh.bin = i;
           sh.total = run;
@@ -439,7 +473,7 @@ __device__ unsigned long long scan_weights(Shared& sh, int n, unsigned long long
   return total;
 }
 
-// A row whose limits leave at most kSorted candidates: those with a bin up to `bar` and of at least min_p.  They are sorted
+// A row whose limits leave at most kList candidates: those with a bin up to `bar` and of at least min_p.  They are sorted
 // in the cluster's first CTA, which cuts and draws.  False where there are more.
 template <typename T>
 __device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, float top_p, float least, float floor_y,
@@ -450,24 +484,23 @@ __device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, fl
   if (threadIdx.x == 0) sh.gathered = 0;
   r.cluster.sync();
   uint32_t* count = r.cluster.map_shared_rank(&sh.gathered, 0);
-  unsigned long long* places = r.cluster.map_shared_rank(sh.sorted.place, 0);
-  unsigned long long* weights = r.cluster.map_shared_rank(sh.sorted.weight, 0);
+  unsigned long long* places = r.cluster.map_shared_rank(sh.all_place, 0);
+  unsigned long long* weights = r.cluster.map_shared_rank(sh.all_weight, 0);
   r.each([&](float x, int i) {
     const float y = sc.log2w(x);
     if (!(y >= floor_y) || bin_of(y) > bar) return;
     const unsigned long long w = sc.weight(x, sh.powers);
     if (w < least_w) return;
     const uint32_t k = atomicAdd(count, 1u);
-    if (k < kSorted) places[k] = place(x, i), weights[k] = w;
+    if (k < kList) places[k] = place(x, i), weights[k] = w;
   });
   r.cluster.sync();
   const uint32_t n_all = *count;
   r.cluster.sync();
-  if (n_all > kSorted) return false;
+  if (n_all > kList) return false;
   if (r.rank == 0) {
-    int n = (int)n_all, n2 = 2;
-    while (n2 < n) n2 *= 2;
-    sort_places(sh, n, n2);
+    int n = (int)n_all;
+    sort_list(sh, n);
     if (top_k > 0) n = min(n, top_k);
     unsigned long long total = scan_weights(sh, n, 0, false);
     if (top_p < 1.f) {
@@ -477,33 +510,20 @@ __device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, fl
       total = sh.total;
       __syncthreads();
     }
-    if (threadIdx.x == 0) sh.limit = sh.sorted.place[n - 1];
+    if (threadIdx.x == 0) sh.limit = sh.all_place[n - 1];
     const unsigned long long goal = u >= 1.f ? total - 1 : times(total, u);
     __syncthreads();
     // in the order of their index: the place's lower half, inverted, falls with it
-    for (int i = threadIdx.x; i < n; i += kThreads) sh.sorted.place[i] &= 0xffffffffu;
-    n2 = 2;
-    while (n2 < n) n2 *= 2;
+    for (int i = threadIdx.x; i < n; i += kThreads) sh.all_place[i] &= 0xffffffffu;
     __syncthreads();
-    sort_places(sh, n, n2);
+    sort_list(sh, n);
     scan_weights(sh, n, goal, true);
     if (threadIdx.x == 0) {
-      *token = (int32_t) ~(uint32_t)sh.sorted.place[sh.bin];
+      *token = (int32_t) ~(uint32_t)sh.all_place[sh.bin];
       sh.total = total;
     }
   }
   return true;
-}
-
-// The listed element at which the mass from `above` on reaches target is the limit.
-__device__ void rank_by_mass(Shared& sh, int n, unsigned long long above, unsigned long long target) {
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    unsigned long long before = above;
-    for (int j = 0; j < n; ++j)
-      if (sh.all_place[j] > sh.all_place[k]) before += sh.all_weight[j];
-    if (before < target && before + sh.all_weight[k] >= target) sh.limit = sh.all_place[k];
-  }
-  __syncthreads();
 }
 
 // Where the kept elements end: the place of the last of them.  True where the chunks' kept masses, and this thread's in
@@ -544,6 +564,7 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
         above = zero;
         __syncthreads();
       }
+      if (in_range > kList) r.range_of(sc, bin, 0, lo, hi, kept);
       while (in_range > kList) {  // many equal or nearly equal logits: halve the range of places
         const unsigned long long mid = lo + (hi - lo) / 2 + 1;
         unsigned long long n = 0, none = 0;
@@ -558,13 +579,8 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
         else hi = mid - 1, above += n, in_range -= n;
       }
       const int n = r.gather(sc, bin, lo, hi, kept);
-      for (int k = threadIdx.x; k < n; k += kThreads) {
-        unsigned long long rank = above;
-        for (int j = 0; j < n; ++j) rank += sh.all_place[j] > sh.all_place[k];
-        if (rank == (unsigned)top_k - 1) sh.limit = sh.all_place[k];
-      }
-      __syncthreads();
-      limit = sh.limit;
+      sort_list(sh, n);
+      limit = sh.all_place[top_k - 1 - above];
       last_bin = bin;
       __syncthreads();
     }
@@ -572,17 +588,7 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
   if (!(top_p < 1.f)) return false;
 
   // the bin by its mass, confirmed by exact sums
-  unsigned long long about = 0;
-  {
-    unsigned long long a = 0;
-    for (int b = threadIdx.x; b <= last_bin; b += kThreads) a += (unsigned long long)sh.mass[b] << unit_bits >> (b / kPerOctave);
-    a = warp_sum(a);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.warp_sums[threadIdx.x / 32][0] = a;
-    __syncthreads();
-    for (int k = 0; k < kWarps; ++k) about += sh.warp_sums[k][0];
-    __syncthreads();
-  }
+  const unsigned long long about = r.mass_above(last_bin + 1, unit_bits);
   int bin = r.template find_bin<true>(max(times_up(about, top_p), 1ull), last_bin, unit_bits);
   if (bin < 0) bin = r.next_bin(last_bin + 1, -1, last_bin);
   unsigned long long target = 0, above = 0, inside = 0, in_bin = 0;
@@ -604,8 +610,7 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
           const float y = sc.log2w(x[k]);
           const int b = bin_of(y);
           if (i + k >= r.v1 || (b > bin && !first) || !kept(x[k], y)) continue;
-          const unsigned long long at = place(x[k], i + k);
-          if (at < limit) continue;
+          if (limit && place(x[k], i + k) < limit) continue;
           const unsigned long long w = r.weight(sc, x[k]);
           if (b < bin) {
             mass += w;
@@ -615,7 +620,7 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
             in += w;
             ++n;
             const uint32_t j = atomicAdd(&sh.listed, 1u);
-            if (j < kList) sh.list_place[j] = at, sh.list_weight[j] = w;
+            if (j < kList) sh.list_place[j] = place(x[k], i + k), sh.list_weight[j] = w;
           }
         }
       }
@@ -628,24 +633,23 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
     r.template reduce<false>(behind, n);
     above = a, inside = in, in_bin = n;
     if (first) target = top_p > 0.f ? max(times_up(above + inside + behind, top_p), 1ull) : 1ull;
-    if (above >= target) {
-      const int b = r.next_bin(bin, -1, last_bin);
-      if (b < 0) break;
-      bin = b;
-    } else if (above + inside < target) {
-      const int b = r.next_bin(bin, 1, last_bin);
-      if (b < 0) return false;  // all of them
-      bin = b;
-    } else {
-      break;
+    const bool low = above + inside < target;
+    if (above < target && !low) break;
+    // the first time, by how far the bins' masses were off here; then from bin to bin
+    int b = -1;
+    if (first) {
+      const unsigned long long off = r.mass_above(bin, unit_bits) - above;  // of either sign
+      b = r.template find_bin<true>(max(target + off, 1ull), last_bin, unit_bits);
     }
+    if (b < 0 || (low ? b <= bin : b >= bin)) b = r.next_bin(bin, low ? 1 : -1, last_bin);
+    if (b < 0) return false;  // all of them
+    bin = b;
   }
   if (in_bin <= kList) {
     const int n = r.merge_lists();
-    if (threadIdx.x == 0) sh.limit = limit;
-    __syncthreads();
-    rank_by_mass(sh, n, above, target);
-    limit = sh.limit;
+    sort_list(sh, n);
+    scan_weights(sh, n, target - above - 1, true);
+    limit = sh.all_place[sh.bin];
     for (int k = threadIdx.x; k < min((int)sh.listed, kList); k += kThreads)
       if (sh.list_place[k] >= limit) {
         kept_here += sh.list_weight[k];
@@ -656,6 +660,7 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
   }
   // many equal or nearly equal logits: halve the range of places
   unsigned long long lo = limit, hi = ~0ull, in_range = in_bin;
+  r.range_of(sc, bin, limit, lo, hi, kept);
   while (in_range > kList) {
     const unsigned long long mid = lo + (hi - lo) / 2 + 1;
     unsigned long long n = 0, w = 0;
@@ -670,15 +675,15 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
     else hi = mid - 1, above += w, in_range -= n;
   }
   const int n = r.gather(sc, bin, lo, hi, kept);
-  if (threadIdx.x == 0) sh.limit = limit;
+  sort_list(sh, n);
+  scan_weights(sh, n, target - above - 1, true);
+  limit = sh.all_place[sh.bin];
   __syncthreads();
-  rank_by_mass(sh, n, above, target);
-  limit = sh.limit;
   return false;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) unsigned char raw[];
   Shared& sh = *reinterpret_cast<Shared*>(raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -700,23 +705,19 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
   if (!(top_p > 0.f)) top_p = top_p <= 0.f ? 0.f : 1.f;  // NaN: no limit
   const float least = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
 
-  // the largest logit's place, and whether the row has a distribution
-  unsigned long long best = 0, odd = 0;
+  // the largest logit, and whether the row has a distribution
+  float mine = -INFINITY;  // this thread's largest
+  unsigned long long best, odd;
   {
-    float top = -INFINITY;
-    int top_i = 0x7fffffff;
     bool bad = false;
-    r.each([&](float x, int i) {
+    r.each([&](float x, int) {
       bad |= !(x < INFINITY);
-      if (x > top) top = x, top_i = i;  // a thread meets its elements in order: the first of equal ones stays
+      mine = fmaxf(mine, x);
     });
-    odd = bad;
-    if (top_i != 0x7fffffff) best = place(top, top_i);
+    best = place(mine, 0) >> 32, odd = bad;
   }
-  const unsigned long long mine = best;  // this thread's largest
   r.template reduce<true>(best, odd);
-  const int best_i = (int)~(uint32_t)best;
-  const uint32_t key = (uint32_t)(best >> 32);
+  const uint32_t key = (uint32_t)best;
   const float m = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
   float* probs = p.probs ? p.probs + at * p.V : nullptr;
   if (odd || bad_temp || !(m > -INFINITY)) {
@@ -727,6 +728,12 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     if (probs)
       for (int i = r.v0 + threadIdx.x; i < r.v1; i += kThreads) probs[i] = NAN;
   } else if (temp < kCold || top_k == 1) {  // the likeliest alone
+    unsigned long long first = 0, none = 0;
+    r.each([&](float x, int i) {
+      if (x == m) first = max(first, (unsigned long long)(uint32_t)~i);
+    });
+    r.template reduce<true>(first, none);
+    const int best_i = (int)~(uint32_t)first;
     if (rank == 0 && threadIdx.x == 0) p.tokens[at] = best_i;
     if (probs)
       for (int i = r.v0 + threadIdx.x; i < r.v1; i += kThreads) probs[i] = i == best_i ? 1.f : 0.f;
@@ -745,9 +752,7 @@ __global__ void __launch_bounds__(kThreads) token_sample_kernel(const __grid_con
     if (top_k > 0 && top_k <= 128 * C) {
       for (int b = threadIdx.x; b < kBins; b += kThreads) sh.count[b] = 0;
       __syncthreads();
-      const uint32_t mk = (uint32_t)(mine >> 32);
-      const float mx = __uint_as_float(mk & 0x80000000u ? mk & 0x7fffffffu : ~mk);
-      if (mine && mx > -INFINITY) atomicAdd(&sh.count[bin_of(sc.log2w(mx))], 1u);
+      if (mine > -INFINITY) atomicAdd(&sh.count[bin_of(sc.log2w(mine))], 1u);
       r.template share_bins<false>();
       const int b = r.template find_bin<false>(top_k, kBins - 1, 0);
       if (b >= 0) bar = b;
