@@ -33,6 +33,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstring>
 
 #include "common.h"
 
@@ -242,33 +243,60 @@ struct Row {
     return sc.weight(x, sh.powers);
   }
 
-  // Calls f(x, index) for this CTA's elements, each thread's in ascending order.  A warp's 256 elements of one turn lie
-  // together: thread l has the 8 from 8 l on.
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int i = v0 + threadIdx.x * 8; i < v1; i += kThreads * 8) {
-      float x[8];
-      load(i, x);
+  // Eight elements from i on as they lie in memory; -inf behind the slice's end.
+  struct Raw {
+    uint4 v[sizeof(T) / 2];
+  };
+  __device__ __forceinline__ Raw load(int i) const {
+    Raw r;
+    if (wide && i + 8 <= v1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i + k < v1) f(x[k], i + k);
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.v[k] = __ldg(reinterpret_cast<const uint4*>(row + i) + k);
+      return r;
+    }
+    T x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = i + k < v1 ? row[i + k] : (T)-INFINITY;
+    memcpy(&r, x, sizeof(r));
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[8]) {
+    if constexpr (sizeof(T) == 4) {
+      memcpy(x, &r, sizeof(r));
+    } else {
+      const uint32_t v[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[2 * k] = __uint_as_float(v[k] << 16), x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
     }
   }
-  __device__ __forceinline__ void load(int i, float (&x)[8]) const {
-    if (wide && i + 8 <= v1) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(row + i)), b = __ldg(reinterpret_cast<const float4*>(row + i) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-      } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + i));
-        const uint32_t v[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[2 * k] = __uint_as_float(v[k] << 16), x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = i + k < v1 ? (float)row[i + k] : -INFINITY;
+  // Calls g(x[8], index of x[0], turn) for this CTA's elements, each thread's in ascending order and every lane of a warp
+  // in every turn.  A warp's 256 elements of one turn lie together, the next turns' are on their way.
+  template <class G>
+  __device__ __forceinline__ void turns(G g) const {
+    const int lane = threadIdx.x % 32;
+    constexpr int kStep = kThreads * 8;
+    int i0 = v0 + (threadIdx.x - lane) * 8;
+    if (i0 >= v1) return;
+    constexpr bool kTwo = sizeof(T) == 2;  // 64 bytes of a thread on their way
+    Raw now = load(i0 + lane * 8), next;
+    if constexpr (kTwo) next = load(i0 + kStep + lane * 8);
+#pragma unroll 1
+    for (; i0 < v1; i0 += kStep) {
+      const Raw after = load(i0 + (kTwo ? 2 : 1) * kStep + lane * 8);
+      float x[8];
+      unpack(now, x);
+      g(x, i0 + lane * 8, (i0 - v0) / kChunk);
+      now = kTwo ? next : after;
+      next = after;
     }
+  }
+  // Calls f(x, index) for them one by one (and for some -inf behind the slice's end).
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    turns([&](const float (&x)[8], int i, int) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f(x[k], i + k);
+    });
   }
 
   // Bins of the whole row from those of the cluster's CTAs: each adds up its share of them and hands it to the others.
@@ -599,35 +627,30 @@ __device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, 
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
     unsigned long long a = 0, in = 0, behind = 0, n = 0;
-    for (int i0 = r.v0 + (threadIdx.x - lane) * 8; i0 < r.v1; i0 += kThreads * 8) {
-      const int i = i0 + lane * 8;
+    r.turns([&](const float (&x)[8], int i, int chunk) {
       unsigned long long mass = 0;
-      if (i < r.v1) {
-        float x[8];
-        r.load(i, x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float y = sc.log2w(x[k]);
-          const int b = bin_of(y);
-          if (i + k >= r.v1 || (b > bin && !first) || !kept(x[k], y)) continue;
-          if (limit && place(x[k], i + k) < limit) continue;
-          const unsigned long long w = r.weight(sc, x[k]);
-          if (b < bin) {
-            mass += w;
-          } else if (b > bin) {
-            behind += w;
-          } else {
-            in += w;
-            ++n;
-            const uint32_t j = atomicAdd(&sh.listed, 1u);
-            if (j < kList) sh.list_place[j] = place(x[k], i + k), sh.list_weight[j] = w;
-          }
+      for (int k = 0; k < 8; ++k) {
+        const float y = sc.log2w(x[k]);
+        const int b = bin_of(y);
+        if ((b > bin && !first) || !kept(x[k], y)) continue;
+        if (limit && place(x[k], i + k) < limit) continue;
+        const unsigned long long w = r.weight(sc, x[k]);
+        if (b < bin) {
+          mass += w;
+        } else if (b > bin) {
+          behind += w;
+        } else {
+          in += w;
+          ++n;
+          const uint32_t j = atomicAdd(&sh.listed, 1u);
+          if (j < kList) sh.list_place[j] = place(x[k], i + k), sh.list_weight[j] = w;
         }
       }
       a += mass;
       mass = warp_sum(mass);
-      if (lane == 0) sh.chunk[(i0 - r.v0) / kChunk] = mass;
-    }
+      if (lane == 0) sh.chunk[chunk] = mass;
+    });
     kept_here = a;
     r.template reduce<false>(a, in);
     r.template reduce<false>(behind, n);
@@ -765,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
         r.each([&](float x, int i) {
           const float y = sc.log2w(x);
           const bool in = y >= floor_y && place(x, i) >= limit && (least_w == 0 || sc.weight(x, sh.powers) >= least_w);
-          probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
+          if (i < r.v1) probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
         });
       }
       cluster.sync();
@@ -784,20 +807,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
     };
     const int lane = threadIdx.x % 32;
     if (!known) total = 0;
-    for (int i0 = known ? r.v1 : r.v0 + (threadIdx.x - lane) * 8; i0 < r.v1; i0 += kThreads * 8) {
-      const int i = i0 + lane * 8;
-      unsigned long long w = 0;
-      if (i < r.v1) {
-        float x[8];
-        r.load(i, x);
+    if (!known)
+      r.turns([&](const float (&x)[8], int i, int chunk) {
+        unsigned long long w = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (i + k < r.v1) w += kept_weight(x[k], i + k);
-      }
-      total += w;
-      w = warp_sum(w);
-      if (lane == 0) sh.chunk[(i0 - r.v0) / kChunk] = w;
-    }
+        for (int k = 0; k < 8; ++k) w += kept_weight(x[k], i + k);
+        total += w;
+        w = warp_sum(w);
+        if (lane == 0) sh.chunk[chunk] = w;
+      });
     r.template reduce<false>(total, none, &before);
     // the draw: in the CTA that u W falls into, by one warp
     const unsigned long long goal = u >= 1.f ? total - 1 : times(total, u);
@@ -826,9 +844,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
         const int i = r.v0 + hit * kChunk + lane * 8;
         float x[8];
         unsigned long long w[8], mine = 0;
-        r.load(i, x);
+        r.unpack(r.load(i), x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = i + k < r.v1 ? kept_weight(x[k], i + k) : 0, mine += w[k];
+        for (int k = 0; k < 8; ++k) w[k] = kept_weight(x[k], i + k), mine += w[k];
         unsigned long long s = mine;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -853,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
       r.each([&](float x, int i) {
         const float y = sc.log2w(x);
         const bool in = y >= floor_y && place(x, i) >= limit && (least_w == 0 || sc.weight(x, sh.powers) >= least_w);
-        probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
+        if (i < r.v1) probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
       });
     }
   }
