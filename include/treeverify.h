@@ -717,7 +717,7 @@ int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int3
  *            requests, or lead past, holds either's result or what it held.  Rows of
  *            no request are left as they are, in out and lse.
  * scale, softcap, window, n_sink, slopes: as in tv_decode_attn.
- * out        device [T, Hq, head_dim] (dtype) out, contiguous.
+ * out        device [T, Hq, head_dim] (dtype) out, contiguous; overlaps no input.
  * lse        device float32 [T, Hq] out (nullable): natural-log normaliser.
  * workspace  device buffer of at least tv_chunk_attn_workspace_size bytes, 256-byte
  *            aligned; its counters (the first 16 KiB) as in tv_decode_attn: cleared

@@ -225,7 +225,7 @@ struct Row {
   }
 
   // bf16 has few values: the weights of nearly all that logits take fit a table, and a weight costs a lookup instead of
-  // some 45 instructions (64 rows of 128,000 without limits 45 -> 30 us).
+  // some 45 instructions (64 rows of 128,000 without limits 45 -> 36 us).
   __device__ void fill_table(const Scale& sc) {
     if constexpr (sizeof(T) == 2) {
       for (uint32_t i = threadIdx.x; i < 2 * kTableSize; i += kThreads) {

@@ -147,15 +147,19 @@ SHAPES = [
 ]
 
 
-def _runs_on(c, kernel):
-    if kernel == "auto":
-        return True
-    try:
-        capi.tv_chunk_attn(c["q"], c["kc"], c["vc"], c["table"], c["lens"], cu_new=c["cu"], flags=KERNELS[kernel])
-    except capi.TVError as e:
-        assert e.code == -4
-        return False
-    return True
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,bs,stride", [(4, 1, 256, "bf16", 16, 1), (4, 1, 128, "f32", 16, 1), (4, 1, 64, "bf16", 12, 1),
+                                                     (130, 1, 64, "bf16", 16, 1), (4, 1, 128, "bf16", 16, 0)])
+def test_shapes_without_a_tcgen05_kernel(Hq, Hkv, D, dtype, bs, stride):
+    """Refused by name, and computed by the other kernel (the last: one query row for every token)."""
+    c = _case([20], [30], Hq, Hkv, D, dtype, bs)
+    if not stride:
+        c["q"] = c["q"][:1].expand(30, Hq, D)
+    with pytest.raises(capi.TVError) as e:
+        _run(c, capi.TV_ATTN_TCGEN05)
+    assert e.value.code == -4 and "tcgen05" in str(e.value)
+    out, lse, status = _run(c)
+    assert status == 0
+    _check(dict(c, q=c["q"].contiguous()), out, lse, False)
 
 
 @pytest.mark.parametrize("kernel", ["simt", "auto"])

@@ -53,6 +53,16 @@ def test_every_limit_alone_and_together(V, dtype):
         _check(x, u, **kw)
 
 
+def test_the_longest_rows_and_many_short_ones():
+    x = _logits(2, 1 << 20, "f32", 21)
+    _check(x, [0.3, 0.999], top_p=[0.9, 0.5])
+    _check(x, [0.3, 0.999], top_k=[100000, 40], top_p=[0.7, 1.0])
+    x = _logits(3000, 700, "bf16", 22)
+    u = np.linspace(0.0, 0.999, 3000)
+    _check(x, u, top_k=[9] * 3000, top_p=[0.8] * 3000)
+    _check(x, u, min_p=[0.05] * 3000)
+
+
 def test_limits_that_are_off_and_at_their_ends():
     x = _logits(12, 1000, "f32", 5)
     u = np.linspace(0.0, 0.99, 12)
