@@ -184,7 +184,7 @@ __device__ __forceinline__ int64_t run_start(int64_t c, int64_t total, int64_t c
 __device__ __forceinline__ int64_t run_of(int64_t x, int64_t total, int64_t ctas) { return divide((x + 1) * ctas - 1, total); }
 
 // All threads of the CTA.
-__device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan) {
+__device__ void make_plan(const ChunkParams& p, int cost, int least, float join_cost, Plan& plan) {
   __shared__ int64_t sums[kThreads / 32 + 1];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -210,6 +210,9 @@ __device__ void make_plan(const ChunkParams& p, int cost, int least, Plan& plan)
     if (w < warp) start += sums[w];
     total += sums[w];
   }
+  // n pieces of a unit of U tiles take U / n tiles, and n pieces' join in one CTA: least for runs of sqrt(U join_cost)
+  // (64 tokens over 8000: 74 us over all CTAs, 61 this way)
+  least = max(least, (int)sqrtf((float)total * join_cost));
   const int ctas = (int)min((int64_t)p.ctas, max((int64_t)1, divide(total, least)));
   const int c = blockIdx.x;
   const int64_t x0 = c < ctas ? run_start(c, total, ctas) : total;
@@ -530,28 +533,29 @@ __device__ __noinline__ void join(const ChunkParams& p, const Plan& plan, const 
   const int blocks0 = (s.tokens[0] * p.G + kRows - 1) / kRows, blocks = blocks0 + (s.tokens[1] * p.G + kRows - 1) / kRows;
   // piece 0 lies in its CTA's second slot, the others in the first
   const int64_t first = ((int64_t)c0 * 2 + 1) * 256, then = ((int64_t)c0 * 2 + 2) * 256;
+  auto load = [&](int blk, int i, float2& ml, Part (&v)[kRows]) {
+    const int at_row = blk < blocks0 ? blk * kRows : 128 + (blk - blocks0) * kRows;
+    const int64_t at = (i == 0 ? first : then + (int64_t)(i - 1) * 512) + at_row;
+    ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + lane % kRows);
+    const Part* src = reinterpret_cast<const Part*>(p.part_o + at * D) + lane;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) v[r] = __ldcg(src + r * 32);
+  };
+  float2 ml;
+  Part v[kRows];
+  if (warp < blocks) load(warp, 0, ml, v);
 #pragma unroll 1
   for (int blk = warp; blk < blocks; blk += 8) {
     const int m = blk >= blocks0, row = (blk - (m ? blocks0 : 0)) * kRows;  // of the M tile
-    const int in_unit = m * 128 + row;
-    auto load = [&](int i, float2& ml, Part (&v)[kRows]) {
-      const int64_t at = (i == 0 ? first : then + (int64_t)(i - 1) * 512) + in_unit;
-      ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + lane % kRows);
-      const Part* src = reinterpret_cast<const Part*>(p.part_o + at * D) + lane;
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) v[r] = __ldcg(src + r * 32);
-    };
     float top = kNoScore, sum = 0.f, o[kRows][kE] = {};
-    float2 ml;
-    Part v[kRows];
-    load(0, ml, v);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       float2 ml_next = ml;
       Part v_next[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) v_next[r] = v[r];
-      if (i + 1 < n) load(i + 1, ml_next, v_next);
+      if (i + 1 < n) load(blk, i + 1, ml_next, v_next);
+      else if (blk + 8 < blocks) load(blk + 8, 0, ml_next, v_next);
       const float now = fmaxf(top, ml.x), keep = exp2_approx(top - now);
       const float w = ml.y == 0.f ? 0.f : exp2_approx(ml.x - now);
       sum = fmaf(sum, keep, w * ml.y);
@@ -868,7 +872,8 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
 
 template <int D, bool kAny>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, int cost, int least) {
+    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, int cost, int least,
+                    float join_cost) {
   using C = Cfg<D>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
@@ -881,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = threadIdx.x; b < p.B; b += kThreads)
       if (!chunk_of(p, b, c)) atomicOr(p.status, TV_DEV_BAD_OFFSETS);
   }
-  make_plan(p, cost, least, plan);
+  make_plan(p, cost, least, join_cost, plan);
   if (plan.x0 >= plan.x1) return;  // all threads, before anything is set up
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -989,7 +994,12 @@ int launch(const ChunkParams& p, const Maps& maps, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(chunk_tc_kernel<D, kAny>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(chunk_tc_kernel)");
-  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, 4, 8);
+  // join of one piece in tiles, over the number of units (about): 1500 cycles of 1900 for 64 rows
+  const int step = 2 * (128 / p.G);
+  const int64_t units = (int64_t)p.Hkv * std::max<int64_t>(ceil_div(p.T, step), std::min(p.T, p.B));
+  const int64_t rows = std::min<int64_t>(step, ceil_div(p.T, p.B)) * p.G;
+  const float join_cost = 0.8f * (float)ceil_div(rows, 64) / (float)units;
+  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, 4, 8, join_cost);
   TV_LAUNCH_CHECK("chunk_tc_kernel");
   return TV_OK;
 }
