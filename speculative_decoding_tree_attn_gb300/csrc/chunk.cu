@@ -11,8 +11,9 @@
 // walks their keys in tiles of 32 with the running maximum and sum of a
 // softmax; a thread holds 8 rows x 2 scores and 8 rows x D / 16 outputs in
 // registers, so 10 16-byte reads of shared memory feed 64 products.  Everything
-// is float32; bound by the FP32 pipe.  Keys that no row of the tile sees are
-// not read.
+// is float32.  Keys that no row of the tile sees are not read.  Bound by the
+// latency of its own steps (load, scores, weights, outputs) at 8-16 warps an SM:
+// 17-26 TFLOP/s of the FP32 pipe's 80.
 #include <algorithm>
 #include <climits>
 
@@ -36,6 +37,9 @@ struct Simt {
   static constexpr int kRows = D == 256 ? 32 : 64;
   static constexpr int kMine = kRows / 8;   // rows of a thread
   static constexpr int kCols = D / 64;      // runs of 4 outputs of a thread
+  // few registers for more CTAs an SM (6 x 33-500 tokens, 16 heads of 64, float32: 345 -> 280 us; 8 x 500, 32/8 heads of 128:
+  // 725 -> 635 us), but for the longest rows, which gain nothing
+  static constexpr int kUnroll = D == 256 ? 2 : 1;
   static constexpr int kPitch = D + 4;      // of a row of Q and K: keys in turn lie in neighbouring banks
   static constexpr int kPitchP = kKeys + 4;
   static constexpr int kBytes = 4 * (kRows * kPitch + kKeys * kPitch + kKeys * D + kRows * kPitchP);
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
     }
     __syncthreads();
     float s[S::kMine * 2] = {};
-#pragma unroll 2
+#pragma unroll S::kUnroll
     for (int d = 0; d < D; d += 4) {
       const float4 k0 = *reinterpret_cast<const float4*>(sk + tx * S::kPitch + d);
       const float4 k1 = *reinterpret_cast<const float4*>(sk + (tx + 16) * S::kPitch + d);
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
       sp[(ty + 8 * r) * S::kPitchP + tx + 16] = e1;
     }
     __syncwarp();  // a row's weights are its own half warp's
-#pragma unroll 2
+#pragma unroll S::kUnroll
     for (int key = 0; key < kKeys; key += 4) {
       float4 w[S::kMine];
 #pragma unroll
