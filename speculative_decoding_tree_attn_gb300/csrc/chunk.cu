@@ -283,7 +283,7 @@ extern "C" int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t hea
   if (!bytes) return tv::fail(TV_ERR_INVALID_ARG, "tv_chunk_attn_workspace_size: null pointer");
   if (int rc = check_shape("tv_chunk_attn_workspace_size", Hq, Hkv, head_dim, dtype, num_ctas)) return rc;
   *bytes = kCounterBytes;
-  if (dtype != TV_BF16 || head_dim == 256) return TV_OK;  // never the tensor-core kernel
+  if (dtype != TV_BF16) return TV_OK;  // never the tensor-core kernel
   int ctas = 0;
   if (int rc = grid_of(num_ctas, &ctas)) return rc;
   *bytes += tv::chunk_tc_workspace(head_dim, ctas);
@@ -355,7 +355,8 @@ extern "C" int tv_chunk_attn(const void* q, int64_t q_stride, const void* k_cach
       if (int rc = grid_of(num_ctas, &p.ctas)) return rc;
       p.arrive = static_cast<uint32_t*>(workspace);
       p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-      p.part_ml = p.part_o + (int64_t)p.ctas * 2 * 256 * head_dim;
+      p.m_tiles = tv::chunk_tc_m_tiles(head_dim);
+      p.part_ml = p.part_o + (int64_t)p.ctas * 2 * 128 * p.m_tiles * head_dim;
       if (!(flags & TV_ATTN_WORKSPACE_ZEROED)) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
       return tv::launch_chunk_tc(p, head_dim, st);
     }

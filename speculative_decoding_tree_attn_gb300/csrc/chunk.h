@@ -28,6 +28,7 @@ struct ChunkParams {
   float* lse;
   int32_t* status;
   uint32_t* arrive;  // tcgen05 kernel: arrivals of split units, by their first CTA
+  int m_tiles;       // ... 128-row M tiles of a unit
   float* part_o;     // [CTAs][2][rows][D]
   float* part_ml;    // [CTAs][2][rows][2]
   int ctas;
@@ -61,6 +62,7 @@ __device__ __forceinline__ bool chunk_of(const ChunkParams& p, int b, ChunkOf& c
 
 // The tcgen05 kernel: why it cannot run a shape (nullptr: it can), its workspace, its launch.
 const char* chunk_tc_unsupported(const DeviceInfo& dev, const ChunkParams& p, int dtype, int head_dim);
+int chunk_tc_m_tiles(int head_dim);
 size_t chunk_tc_workspace(int head_dim, int ctas);
 int launch_chunk_tc(const ChunkParams& p, int head_dim, cudaStream_t stream);
 

@@ -14,7 +14,9 @@
 //   tile has two S buffers, so the products of the next tile and of the other M
 //   tile run while a tile's softmax does.  (One S buffer, freed once it is in
 //   registers, and two for P: 6.0 against 5.7 ms.)
-//   S_0 2 x 64 | S_1 2 x 64 | O_0 128 | O_1 128 columns fill the TMEM.
+//   S_0 2 x 64 | S_1 2 x 64 | O_0 128 | O_1 128 columns fill the TMEM; with heads
+//   of 256 a unit is one M tile, S 2 x 64 | O 256 (4 x 512 tokens, 16/4 heads: 59
+//   us, 516 on CUDA cores).
 // * Softmax: a thread per row, against a reference that is the first tile's
 //   maximum and moves, with O rescaled in TMEM, only when weights pass 2^20; so
 //   later tiles need no maximum at all (it took a third of a tile's time).  Weights are rounded to bf16 for
@@ -26,6 +28,12 @@
 //   run from lengths and offsets alone.  A unit cut by a run's end leaves
 //   (max, sum, output) of each piece in the workspace and the CTA whose piece
 //   arrives last joins them in order, so results do not depend on timing.
+//
+// Bound by shared memory and the chain of a tile (scores, softmax, outputs, next
+// scores: 1630 cycles, of which the operands' 160 KB take 1250): 8192 tokens
+// behind 24576, 64/8 heads of 128, 5.5-5.7 ms, 0.71-0.73 of the measured bf16
+// rate; by what a unit costs beside its tiles (about four of them) for prompts of
+// a few hundred tokens (32 of 1-1023 tokens: 179 us, 0.29).
 //
 // Every mbarrier wait is bounded (2 s); past it the CTA sets TV_DEV_TIMEOUT, lets
 // its products and loads finish, frees its TMEM and returns.
@@ -52,15 +60,18 @@ constexpr float kMost = 0x1p20f;   // sum of a row's weights in a tile before it
 
 template <int D>
 struct Cfg {
+  static constexpr int kM = D == 256 ? 1 : 2;      // M tiles of a unit: two of 256 columns do not fit the TMEM
   static constexpr int kQTile = D / 64 * kQHalf;
   static constexpr int kTile = D / 64 * kHalf;     // bytes of a K or V tile
-  static constexpr int kSlots = D == 128 ? 4 : 8;  // of K, and of V
-  static constexpr int kOffK = 2 * kQTile;         // behind Q_0, Q_1
+  static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 4 : 2;  // of K, and of V
+  static constexpr int kOffK = kM * kQTile;        // behind Q_0, Q_1
   static constexpr int kOffV = kOffK + kSlots * kTile;
   static constexpr int kOffOut = kOffV + kSlots * kTile;  // 4 KB a softmax warp: 32 rows of 64 output columns
   static constexpr int kSmem = kOffOut + 8 * 4096 + 1024;
 };
-static_assert(Cfg<128>::kSmem <= 227 * 1024 - 1024 && Cfg<64>::kSmem <= 227 * 1024 - 1024, "fits beside the barriers");
+static_assert(Cfg<64>::kSmem <= 227 * 1024 - 1024 && Cfg<128>::kSmem <= 227 * 1024 - 1024 &&
+                  Cfg<256>::kSmem <= 227 * 1024 - 1024,
+              "fits beside the barriers");
 
 __host__ __device__ constexpr uint32_t kColS(int m, uint32_t tile) { return m * 128 + (tile & 1) * 64; }
 constexpr uint32_t kColO(int m) { return 256 + m * 128; }
@@ -145,7 +156,7 @@ struct Request {
   int window, sinks;  // sinks: tiles of kept first keys
 
   __device__ __forceinline__ void set(const ChunkParams& p, int b) {
-    step = 2 * (128 / p.G);
+    step = p.m_tiles * (128 / p.G);
     chunk_of(p, b, c);
     units = (c.n + step - 1) / step;
     window = p.window;
@@ -288,7 +299,7 @@ struct Walk {
   __device__ __forceinline__ bool next(Piece& s) {
     while (at < plan.x1) {
       if (fresh) {
-        const int j0 = i * r.step, n = min(r.step, r.c.n - j0), half = r.step / 2;
+        const int j0 = i * r.step, n = min(r.step, r.c.n - j0), half = 128 / p.G;
         s.b = b;
         s.s0 = r.c.s0 + j0;
         s.tokens[0] = min(n, half);
@@ -526,26 +537,29 @@ __device__ __forceinline__ uint32_t count_arrival(uint32_t* counter) {
 // outputs, the next piece on its way meanwhile.  (A row at a time, every trip to memory waited for: 45 us for 256 rows.)
 template <int D>
 __device__ __noinline__ void join(const ChunkParams& p, const Plan& plan, const Piece& s, int warp, int lane) {
-  constexpr int kE = D / 32, kRows = 8;
+  constexpr int kW = D == 64 ? 64 : 128, kCols = D / kW, kE = kW / 32, kRows = 8;  // columns at a time
+  constexpr int kSlot = 128 * Cfg<D>::kM, kWarps = 4 * Cfg<D>::kM;
   using Part = typename std::conditional<kE == 4, float4, float2>::type;
   const int c0 = (int)run_of(s.real, plan.total, plan.ctas), c1 = (int)run_of(s.real + s.tiles - 1, plan.total, plan.ctas);
   const int n = c1 - c0 + 1, per = 128 / p.G;
   const int blocks0 = (s.tokens[0] * p.G + kRows - 1) / kRows, blocks = blocks0 + (s.tokens[1] * p.G + kRows - 1) / kRows;
   // piece 0 lies in its CTA's second slot, the others in the first
-  const int64_t first = ((int64_t)c0 * 2 + 1) * 256, then = ((int64_t)c0 * 2 + 2) * 256;
-  auto load = [&](int blk, int i, float2& ml, Part (&v)[kRows]) {
+  const int64_t first = ((int64_t)c0 * 2 + 1) * kSlot, then = ((int64_t)c0 * 2 + 2) * kSlot;
+  auto load = [&](int q, int i, float2& ml, Part (&v)[kRows]) {
+    const int blk = q / kCols;
     const int at_row = blk < blocks0 ? blk * kRows : 128 + (blk - blocks0) * kRows;
-    const int64_t at = (i == 0 ? first : then + (int64_t)(i - 1) * 512) + at_row;
+    const int64_t at = (i == 0 ? first : then + (int64_t)(i - 1) * (2 * kSlot)) + at_row;
     ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + lane % kRows);
-    const Part* src = reinterpret_cast<const Part*>(p.part_o + at * D) + lane;
+    const Part* src = reinterpret_cast<const Part*>(p.part_o + at * D + q % kCols * kW) + lane;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) v[r] = __ldcg(src + r * 32);
+    for (int r = 0; r < kRows; ++r) v[r] = __ldcg(src + r * (D / kE));
   };
   float2 ml;
   Part v[kRows];
-  if (warp < blocks) load(warp, 0, ml, v);
+  if (warp < blocks * kCols) load(warp, 0, ml, v);
 #pragma unroll 1
-  for (int blk = warp; blk < blocks; blk += 8) {
+  for (int q = warp; q < blocks * kCols; q += kWarps) {
+    const int blk = q / kCols;
     const int m = blk >= blocks0, row = (blk - (m ? blocks0 : 0)) * kRows;  // of the M tile
     float top = kNoScore, sum = 0.f, o[kRows][kE] = {};
 #pragma unroll 1
@@ -554,8 +568,8 @@ __device__ __noinline__ void join(const ChunkParams& p, const Plan& plan, const 
       Part v_next[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) v_next[r] = v[r];
-      if (i + 1 < n) load(blk, i + 1, ml_next, v_next);
-      else if (blk + 8 < blocks) load(blk + 8, 0, ml_next, v_next);
+      if (i + 1 < n) load(q, i + 1, ml_next, v_next);
+      else if (q + kWarps < blocks * kCols) load(q + kWarps, 0, ml_next, v_next);
       const float now = fmaxf(top, ml.x), keep = exp2_approx(top - now);
       const float w = ml.y == 0.f ? 0.f : exp2_approx(ml.x - now);
       sum = fmaf(sum, keep, w * ml.y);
@@ -575,12 +589,12 @@ __device__ __noinline__ void join(const ChunkParams& p, const Plan& plan, const 
     auto out_row = [&](int r) {
       return ((int64_t)s.s0 + m * per + (row + r) / p.G) * p.Hq + s.kvh * p.G + (row + r) % p.G;
     };
-    if (lane < min(rows, kRows) && p.lse) p.lse[out_row(lane)] = (top + log2f(sum)) * kLn2;
+    if (lane < min(rows, kRows) && p.lse && q % kCols == 0) p.lse[out_row(lane)] = (top + log2f(sum)) * kLn2;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const float fr = __shfl_sync(0xffffffffu, f, r);
       if (r >= rows) continue;
-      char* dst = p.out + (out_row(r) * D + lane * kE) * 2;
+      char* dst = p.out + (out_row(r) * D + q % kCols * kW + lane * kE) * 2;
       if constexpr (kE == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[r][0] * fr, o[r][1] * fr), pack_bf16(o[r][2] * fr, o[r][3] * fr));
       else
@@ -685,11 +699,13 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
         ok = mbar_wait_warp(&bars.v_seen[m], cleared & 1, &bars.abort, p.status, limit_ns());
         if (!ok) break;
         ++cleared;
-        const int t = t0 + rl % kBlk, h = rl / kBlk;
-        if (h < D / 64 && (t > s.last || (t < s.lo && t >= s.sink))) {
-          uint4* row = reinterpret_cast<uint4*>(sV + slot * C::kTile + h * kHalf + rl % kBlk * 128);
+        const int t = t0 + rl % kBlk;
+        if (t > s.last || (t < s.lo && t >= s.sink)) {
+          for (int h = rl / kBlk; h < D / 64; h += 2) {
+            uint4* row = reinterpret_cast<uint4*>(sV + slot * C::kTile + h * kHalf + rl % kBlk * 128);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) row[y] = make_uint4(0, 0, 0, 0);
+            for (int y = 0; y < 8; ++y) row[y] = make_uint4(0, 0, 0, 0);
+          }
         }
         fence_proxy_async();
         __syncwarp();
@@ -816,7 +832,7 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
     // a piece: its rows to the workspace; the unit's last arrival joins them
     {
       const int64_t slot = (int64_t)blockIdx.x * 2 + (s.a == 0);
-      const int64_t row = slot * 256 + m * 128 + rl;
+      const int64_t row = slot * (128 * C::kM) + m * 128 + rl;
       if (valid) {
         reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(top, sum);
         if (n_mine == 0) {
@@ -892,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) {
       for (int v = 0; v < 2; ++v) {
         mbar_init(&bars.full[v][i], 1);
-        mbar_init(&bars.empty[v][i], 2);
+        mbar_init(&bars.empty[v][i], C::kM);
       }
     }
     for (int m = 0; m < 2; ++m) {
@@ -907,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.drain[m], 1);
       mbar_init(&bars.drain[2 + m], 1);
     }
-    mbar_init(&bars.posted, 256);
+    mbar_init(&bars.posted, 128 * C::kM);
     mbar_init(&bars.decided, 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -927,14 +943,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
       run_producer<D>(p, plan, cost, maps, bars, base, warp, lane);
     } else if (warp < 6) {
-      if (lane == 0) issue_scores<D>(p, plan, cost, maps, bars, base, tmem, warp - 4);
+      if (lane == 0 && warp - 4 < C::kM) issue_scores<D>(p, plan, cost, maps, bars, base, tmem, warp - 4);
     } else {
-      if (lane == 0) issue_outputs<D>(p, plan, cost, bars, base, tmem, warp - 6);
+      if (lane == 0 && warp - 6 < C::kM) issue_outputs<D>(p, plan, cost, bars, base, tmem, warp - 6);
     }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    run_softmax<D, kAny>(p, plan, cost, maps, bars, sV, base + C::kOffOut, tmem, (warp - 8) / 4, warp, lane);
+    if (warp < 8 + 4 * C::kM)
+      run_softmax<D, kAny>(p, plan, cost, maps, bars, sV, base + C::kOffOut, tmem, (warp - 8) / 4, warp, lane);
   }
   fence_before();
   __syncthreads();
@@ -995,7 +1012,7 @@ int launch(const ChunkParams& p, const Maps& maps, cudaStream_t stream) {
       cudaFuncSetAttribute(chunk_tc_kernel<D, kAny>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(chunk_tc_kernel)");
   // join of one piece in tiles, over the number of units (about): 1500 cycles of 1900 for 64 rows
-  const int step = 2 * (128 / p.G);
+  const int step = Cfg<D>::kM * (128 / p.G);
   const int64_t units = (int64_t)p.Hkv * std::max<int64_t>(ceil_div(p.T, step), std::min(p.T, p.B));
   const int64_t rows = std::min<int64_t>(step, ceil_div(p.T, p.B)) * p.G;
   const float join_cost = 0.8f * (float)ceil_div(rows, 64) / (float)units;
@@ -1009,7 +1026,6 @@ int launch(const ChunkParams& p, const Maps& maps, cudaStream_t stream) {
 const char* chunk_tc_unsupported(const DeviceInfo& dev, const ChunkParams& p, int dtype, int head_dim) {
   if (dev.cc_major != 10) return "device is not sm_10x";
   if (dtype != TV_BF16) return "dtype is not bf16";
-  if (head_dim != 64 && head_dim != 128) return "head_dim is not 64 or 128";
   if (p.G > 128) return "more than 128 query heads per KV head";
   if (p.block_size % 8) return "block_size is not a multiple of 8";
   if (p.num_blocks >= INT32_MAX / ((int64_t)p.Hkv * p.block_size)) return "the cache has 2^31 rows";
@@ -1019,7 +1035,11 @@ const char* chunk_tc_unsupported(const DeviceInfo& dev, const ChunkParams& p, in
   return nullptr;
 }
 
-size_t chunk_tc_workspace(int head_dim, int ctas) { return (size_t)ctas * 2 * 256 * (head_dim + 2) * 4; }
+int chunk_tc_m_tiles(int head_dim) { return head_dim == 256 ? Cfg<256>::kM : Cfg<128>::kM; }
+
+size_t chunk_tc_workspace(int head_dim, int ctas) {
+  return (size_t)ctas * 2 * 128 * chunk_tc_m_tiles(head_dim) * (head_dim + 2) * 4;
+}
 
 int launch_chunk_tc(const ChunkParams& p, int D, cudaStream_t stream) {
   EncodeTiled fn;
@@ -1042,6 +1062,7 @@ int launch_chunk_tc(const ChunkParams& p, int D, cudaStream_t stream) {
   if (int rc = encode_out(fn, &maps, p, D)) return rc;
   // the plain form masks before it scales: its factor has to keep -inf what it is
   const bool any = p.softcap > 0.f || p.slopes || !(p.scale * kLog2e >= FLT_MIN);
+  if (D == 256) return any ? launch<256, true>(p, maps, stream) : launch<256, false>(p, maps, stream);
   if (D == 64) return any ? launch<64, true>(p, maps, stream) : launch<64, false>(p, maps, stream);
   return any ? launch<128, true>(p, maps, stream) : launch<128, false>(p, maps, stream);
 }

@@ -147,7 +147,7 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,dtype,bs,stride", [(4, 1, 256, "bf16", 16, 1), (4, 1, 128, "f32", 16, 1), (4, 1, 64, "bf16", 12, 1),
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,bs,stride", [(4, 1, 256, "f32", 16, 1), (4, 1, 128, "f32", 16, 1), (4, 1, 64, "bf16", 12, 1),
                                                      (130, 1, 64, "bf16", 16, 1), (4, 1, 128, "bf16", 16, 0)])
 def test_shapes_without_a_tcgen05_kernel(Hq, Hkv, D, dtype, bs, stride):
     """Refused by name, and computed by the other kernel (the last: one query row for every token)."""
@@ -199,7 +199,7 @@ def test_the_oracle_agrees():
     assert np.abs(to_np(out) - ro).max() < 1e-5 and np.abs(to_np(lse) - rl).max() < 1e-5
 
 
-@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("bf16", 256), ("f32", 64)])
 def test_rows_that_see_nothing(dtype, D):
     """A chunk longer than its sequence: its first tokens sit below 0; a sequence of length 0 and below."""
     c = _case([0, 0, 0, 0], [40, 9, 300, 20], 4, 1, D, dtype, 16)
@@ -296,15 +296,16 @@ def test_chunks_in_turn_are_the_whole_prompt():
             at += n
 
 
+@pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("ctas", [1, 2, 3, 7, 40, 152, 333, 4096])
-def test_any_grid(ctas):
-    c = _case([900, 0, 2000, 40], [100, 300, 5, 1], 8, 2, 128, "bf16", 16, seed=4)
+def test_any_grid(ctas, D):
+    c = _case([900, 0, 2000, 40], [100, 300, 5, 1], 8, 2, D, "bf16", 16, seed=4)
     out, lse, status = _run(c, num_ctas=ctas)
     assert status == 0
     _check(c, out, lse, True)
 
 
-@pytest.mark.parametrize("D,G,bs", [(128, 4, 16), (64, 4, 64), (128, 16, 8)])
+@pytest.mark.parametrize("D,G,bs", [(128, 4, 16), (64, 4, 64), (128, 16, 8), (256, 4, 16)])
 def test_long_runs_of_a_cta(D, G, bs):
     """Few CTAs: hundreds of tiles each, half of an M tile pair idle for whole requests, and then not."""
     rng = np.random.default_rng(D + G)
@@ -315,7 +316,7 @@ def test_long_runs_of_a_cta(D, G, bs):
         _check(c, out, lse, True)
 
 
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_an_output_on_a_16_byte_boundary(D):
     c = _case([30, 200], [40, 70], 8, 2, D, "bf16", 16)
     want, _, _ = _run(c)
