@@ -386,6 +386,21 @@ def test_captured_replayed_with_other_lengths_and_on_another_stream():
         _check(c, out, lse, True)
 
 
+def test_two_calls_at_once():
+    """Two streams, a workspace each, many times over."""
+    cs = [_case([900, 40, 2000], [100, 300, 70], 8, 2, D, "bf16", 16, seed=D) for D in (128, 64)]
+    want = [_run(c)[0] for c in cs]
+    ws = [capi.alloc_workspace(capi.tv_chunk_attn_workspace_size(8, 2, c["q"].shape[2], torch.bfloat16)) for c in cs]
+    outs, streams = [torch.zeros_like(w) for w in want], [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, w, o, st in zip(cs, ws, outs, streams):
+            capi.tv_chunk_attn(c["q"], c["kc"], c["vc"], c["table"], c["lens"], cu_new=c["cu"], out=o, workspace=w,
+                               flags=capi.TV_ATTN_WORKSPACE_ZEROED, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
 def test_offsets_past_32_bits():
     """Blocks at the far end of a cache of more than 2^31 elements."""
     D, bs, Hkv = 128, 16, 8
