@@ -11,11 +11,13 @@
 // walks their keys in tiles of 32 with the running maximum and sum of a
 // softmax; a thread holds 8 rows x 2 scores and 8 rows x D / 16 outputs in
 // registers, so 10 16-byte reads of shared memory feed 64 products.  Everything
-// is float32.  Keys that no row of the tile sees are not read.  Bound by the
+// is float32.  Keys that no row of the tile sees are not read.  Few tiles of rows
+// share their keys among CTAs, whose parts the last to arrive joins in order.  Bound by the
 // latency of its own steps (load, scores, weights, outputs) at 8-16 warps an SM:
-// 17-26 TFLOP/s of the FP32 pipe's 80.
+// 20-28 TFLOP/s of the FP32 pipe's 80.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -31,6 +33,9 @@ constexpr int kThreads = 128;
 constexpr int kKeys = 32;      // of a tile
 constexpr int kMaxCtas = 4096;
 constexpr size_t kCounterBytes = 4 * kMaxCtas;  // first in the workspace
+constexpr int kPieces = 64;       // of a CUDA-core tile's keys at most
+constexpr int kSlots = 1216;      // pieces of all tiles at most: about eight CTAs an SM
+constexpr size_t kSlotFloats = 64 * (128 + 2);  // a piece's rows with their maxima and sums, enough for 32 rows of 256 too
 
 template <int D>
 struct Simt {
@@ -44,6 +49,17 @@ struct Simt {
   static constexpr int kPitchP = kKeys + 4;
   static constexpr int kBytes = 4 * (kRows * kPitch + kKeys * kPitch + kKeys * D + kRows * kPitchP);
 };
+
+__device__ __forceinline__ void cp_async16(float* dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(read ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ float4 as_floats(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 as_floats(const __nv_bfloat16* p) {
@@ -83,7 +99,7 @@ __device__ __forceinline__ bool find_tile(const ChunkParams& p, int unit, int to
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_constant__ ChunkParams p, int split) {
   using S = Simt<D>;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;
@@ -93,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
   __shared__ int64_t row_at[kKeys];  // cache row (of KV head 0) of a key, -1: zeros
 
   const int kvh = blockIdx.y;
-  const int h0 = blockIdx.z * S::kRows, heads = min(p.G - h0, S::kRows);  // query heads of the KV head
+  const int h0 = blockIdx.z / split * S::kRows, heads = min(p.G - h0, S::kRows);  // query heads of the KV head
   const int tokens = S::kRows / min(p.G, S::kRows);
   int b, i;
   ChunkOf c;
@@ -133,7 +149,11 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
 
   const int lead = min((sink + kKeys - 1) / kKeys, lo / kKeys);  // tiles of kept first keys before the window's
   const int tiles = last >= 0 ? lead + last / kKeys + 1 - lo / kKeys : 0;
-  for (int tile = 0; tile < tiles; ++tile) {
+  // few tiles of rows over many keys: several CTAs share one's keys, 128 each at least, and the last to arrive joins
+  const int pieces = min(split, max(1, tiles / 4)), piece = blockIdx.z % split;
+  if (piece >= pieces) return;
+  const int tile1 = (int)((int64_t)tiles * (piece + 1) / pieces);
+  for (int tile = (int)((int64_t)tiles * piece / pieces); tile < tile1; ++tile) {
     const int t0 = (tile < lead ? tile : lo / kKeys + tile - lead) * kKeys;
     __syncthreads();
     if (tid < kKeys) {
@@ -147,18 +167,34 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
       row_at[tid] = at;
     }
     __syncthreads();
-    for (int x = tid; x < kKeys * (D / 4); x += kThreads) {
-      const int key = x / (D / 4), d = x % (D / 4) * 4;
-      const int64_t at = row_at[key];
-      float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-      if (at >= 0) {
-        const int64_t off = (at + (int64_t)kvh * p.block_size) * D + d;
-        k = as_floats(reinterpret_cast<const T*>(p.k_cache) + off);
-        v = as_floats(reinterpret_cast<const T*>(p.v_cache) + off);
+    // float32 straight into shared memory, all of K on its way and V behind it while the scores are computed (load by load
+    // through registers 1305 against 974 us: 175 tokens over 4648, 32/4 heads of 256)
+    if constexpr (std::is_same<T, float>::value) {
+      auto load = [&](const char* cache, float* dst, int pitch) {
+        for (int x = tid; x < kKeys * (D / 4); x += kThreads) {
+          const int key = x / (D / 4), d = x % (D / 4) * 4;
+          const int64_t at = row_at[key], from = at < 0 ? 0 : (at + (int64_t)kvh * p.block_size) * D + d;
+          cp_async16(dst + key * pitch + d, reinterpret_cast<const float*>(cache) + from, at >= 0);
+        }
+        cp_async_commit();
+      };
+      load(p.k_cache, sk, S::kPitch);
+      load(p.v_cache, sv, D);
+    } else {
+      for (int x = tid; x < kKeys * (D / 4); x += kThreads) {
+        const int key = x / (D / 4), d = x % (D / 4) * 4;
+        const int64_t at = row_at[key];
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+        if (at >= 0) {
+          const int64_t off = (at + (int64_t)kvh * p.block_size) * D + d;
+          k = as_floats(reinterpret_cast<const T*>(p.k_cache) + off);
+          v = as_floats(reinterpret_cast<const T*>(p.v_cache) + off);
+        }
+        *reinterpret_cast<float4*>(sk + key * S::kPitch + d) = k;
+        *reinterpret_cast<float4*>(sv + key * D + d) = v;
       }
-      *reinterpret_cast<float4*>(sk + key * S::kPitch + d) = k;
-      *reinterpret_cast<float4*>(sv + key * D + d) = v;
     }
+    cp_async_wait<1>();
     __syncthreads();
     float s[S::kMine * 2] = {};
 #pragma unroll S::kUnroll
@@ -196,7 +232,8 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
       sp[(ty + 8 * r) * S::kPitchP + tx] = e0;
       sp[(ty + 8 * r) * S::kPitchP + tx + 16] = e1;
     }
-    __syncwarp();  // a row's weights are its own half warp's
+    cp_async_wait<0>();
+    __syncthreads();  // V; a row's weights are its own half warp's
 #pragma unroll S::kUnroll
     for (int key = 0; key < kKeys; key += 4) {
       float4 w[S::kMine];
@@ -220,9 +257,61 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
     }
   }
 #pragma unroll
-  for (int r = 0; r < S::kMine; ++r) {
+  for (int r = 0; r < S::kMine; ++r)
 #pragma unroll
     for (int w = 1; w < 16; w *= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+  if (pieces > 1) {
+    const int unit = (blockIdx.z / split * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    float* slot = p.part_o + (int64_t)unit * split * kSlotFloats;  // [piece][rows][D + 2]: outputs, maximum, sum
+    float* here = slot + piece * kSlotFloats;
+#pragma unroll
+    for (int r = 0; r < S::kMine; ++r) {
+      float* dst = here + (ty + 8 * r) * (D + 2);
+#pragma unroll
+      for (int k = 0; k < S::kCols * 4; k += 2)
+        *reinterpret_cast<float2*>(dst + k / 4 * 64 + tx * 4 + k % 4) = make_float2(o[r][k], o[r][k + 1]);
+      if (tx == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(m[r], l[r]);
+    }
+    __shared__ bool joins;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t before;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(p.arrive + unit), "r"(1u) : "memory");
+      joins = before == (uint32_t)pieces - 1;
+      if (joins) p.arrive[unit] = 0;
+    }
+    __syncthreads();
+    if (!joins) return;
+    __threadfence();
+#pragma unroll
+    for (int r = 0; r < S::kMine; ++r) {
+      m[r] = kNoScore;
+      l[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < S::kCols * 4; ++k) o[r][k] = 0.f;
+    }
+#pragma unroll 1
+    for (int i = 0; i < pieces; ++i) {
+#pragma unroll
+      for (int r = 0; r < S::kMine; ++r) {
+        const float* src = slot + i * kSlotFloats + (ty + 8 * r) * (D + 2);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + D));
+        const float top = fmaxf(m[r], ml.x), keep = exp2_approx(m[r] - top);
+        const float w = ml.y == 0.f ? 0.f : exp2_approx(ml.x - top);
+        l[r] = fmaf(l[r], keep, w * ml.y);
+        m[r] = top;
+#pragma unroll
+        for (int k = 0; k < S::kCols * 4; k += 2) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src + k / 4 * 64 + tx * 4 + k % 4));
+          o[r][k] = fmaf(o[r][k], keep, w * x.x);
+          o[r][k + 1] = fmaf(o[r][k + 1], keep, w * x.y);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < S::kMine; ++r) {
     const int row = ty + 8 * r;
     if (row >= rows) continue;
     const int64_t at = (int64_t)(c.s0 + j0 + row / heads) * p.Hq + kvh * p.G + h0 + row % heads;
@@ -236,22 +325,28 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
 }
 
 template <typename T, int D>
-int launch_simt(const ChunkParams& p, cudaStream_t stream) {
+int launch_simt(const ChunkParams& p, bool zeroed, cudaStream_t stream) {
   using S = Simt<D>;
   const int64_t tokens = S::kRows / std::min(p.G, S::kRows);
   const int64_t units = p.cu ? p.T / tokens + p.B : tv::ceil_div(p.T / p.B, tokens) * p.B;
   const cudaError_t e =
       cudaFuncSetAttribute(chunk_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return tv::cuda_fail(e, "cudaFuncSetAttribute(chunk_simt_kernel)");
-  const dim3 grid((unsigned)units, (unsigned)p.Hkv, (unsigned)tv::ceil_div(p.G, S::kRows));
-  chunk_simt_kernel<T, D><<<grid, kThreads, S::kBytes, stream>>>(p);
+  const int64_t groups = tv::ceil_div(p.G, S::kRows), ctas = units * p.Hkv * groups;
+  const int split = (int)std::max<int64_t>(1, std::min<int64_t>(kPieces, kSlots / ctas));
+  static_assert((size_t)S::kRows * (D + 2) <= kSlotFloats, "a piece fits its slot");
+  if (split > 1 && !zeroed) TV_CUDA_TRY(cudaMemsetAsync(p.arrive, 0, kCounterBytes, stream));
+  const dim3 grid((unsigned)units, (unsigned)p.Hkv, (unsigned)(groups * split));
+  chunk_simt_kernel<T, D><<<grid, kThreads, S::kBytes, stream>>>(p, split);
   TV_LAUNCH_CHECK("chunk_simt_kernel");
   return TV_OK;
 }
 
 template <typename T>
-int dispatch_simt(const ChunkParams& p, int D, cudaStream_t stream) {
-  return D == 64 ? launch_simt<T, 64>(p, stream) : D == 128 ? launch_simt<T, 128>(p, stream) : launch_simt<T, 256>(p, stream);
+int dispatch_simt(const ChunkParams& p, int D, bool zeroed, cudaStream_t stream) {
+  return D == 64    ? launch_simt<T, 64>(p, zeroed, stream)
+         : D == 128 ? launch_simt<T, 128>(p, zeroed, stream)
+                    : launch_simt<T, 256>(p, zeroed, stream);
 }
 
 int check_shape(const char* fn, int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t dtype, int32_t num_ctas) {
@@ -282,11 +377,11 @@ extern "C" int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t hea
   tv::clear_error();
   if (!bytes) return tv::fail(TV_ERR_INVALID_ARG, "tv_chunk_attn_workspace_size: null pointer");
   if (int rc = check_shape("tv_chunk_attn_workspace_size", Hq, Hkv, head_dim, dtype, num_ctas)) return rc;
-  *bytes = kCounterBytes;
+  *bytes = kCounterBytes + kSlots * kSlotFloats * sizeof(float);
   if (dtype != TV_BF16) return TV_OK;  // never the tensor-core kernel
   int ctas = 0;
   if (int rc = grid_of(num_ctas, &ctas)) return rc;
-  *bytes += tv::chunk_tc_workspace(head_dim, ctas);
+  *bytes = std::max(*bytes, kCounterBytes + tv::chunk_tc_workspace(head_dim, ctas));
   return TV_OK;
 }
 
@@ -347,20 +442,21 @@ extern "C" int tv_chunk_attn(const void* q, int64_t q_stride, const void* k_cach
   p.out = static_cast<char*>(out);
   p.lse = lse;
   p.status = status;
+  p.arrive = static_cast<uint32_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
+  const bool zeroed = flags & TV_ATTN_WORKSPACE_ZEROED;
   if ((flags & 3) != TV_ATTN_SIMT) {
     tv::DeviceInfo dev;
     if (int rc = tv::current_device_info(&dev)) return rc;
     const char* why = tv::chunk_tc_unsupported(dev, p, dtype, head_dim);
     if (!why) {
       if (int rc = grid_of(num_ctas, &p.ctas)) return rc;
-      p.arrive = static_cast<uint32_t*>(workspace);
-      p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
       p.m_tiles = tv::chunk_tc_m_tiles(head_dim);
       p.part_ml = p.part_o + (int64_t)p.ctas * 2 * 128 * p.m_tiles * head_dim;
-      if (!(flags & TV_ATTN_WORKSPACE_ZEROED)) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
+      if (!zeroed) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
       return tv::launch_chunk_tc(p, head_dim, st);
     }
     if ((flags & 3) == TV_ATTN_TCGEN05) return tv::fail(TV_ERR_UNSUPPORTED, "tv_chunk_attn: no tcgen05 kernel: %s", why);
   }
-  return dtype == TV_BF16 ? dispatch_simt<__nv_bfloat16>(p, head_dim, st) : dispatch_simt<float>(p, head_dim, st);
+  return dtype == TV_BF16 ? dispatch_simt<__nv_bfloat16>(p, head_dim, zeroed, st) : dispatch_simt<float>(p, head_dim, zeroed, st);
 }
