@@ -353,6 +353,25 @@ def test_same_bits_again_and_counters_left_zero():
     assert torch.equal(out, first[0]) and not ws[:16384].any()
 
 
+@pytest.mark.parametrize("D,dtype,bs", [(64, "f32", 16), (128, "f32", 64), (256, "f32", 16), (128, "bf16", 20)])
+def test_keys_shared_by_ctas_without_tcgen05(D, dtype, bs):
+    """Few rows over many keys: right, the same bits again, counters left zero, also behind a call on tcgen05."""
+    c = _case([5000, 0, 700], [3, 1, 40], 8, 2, D, dtype, bs, seed=D)
+    other = _case([2000, 10], [30, 300], 8, 2, 128, "bf16", 16, seed=5)
+    ws = capi.alloc_workspace(max(capi.tv_chunk_attn_workspace_size(8, 2, x["q"].shape[2], x["q"].dtype)
+                                  for x in (c, other)))
+    want, want_lse, status = _run(c)
+    assert status == 0
+    _check(c, want, want_lse, False)
+    want_other = _run(other)[0]
+    for _ in range(10):
+        out, lse, status = _run(c, capi.TV_ATTN_WORKSPACE_ZEROED, workspace=ws)
+        assert status == 0 and not ws[:16384].any()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        out, _, status = _run(other, capi.TV_ATTN_WORKSPACE_ZEROED, workspace=ws)
+        assert status == 0 and torch.equal(out, want_other) and not ws[:16384].any()
+
+
 def test_one_workspace_for_different_calls():
     ws = capi.alloc_workspace(capi.tv_chunk_attn_workspace_size(16, 2, 128, torch.bfloat16))
     for seed, shape in enumerate((([5000], [3], 8, 1, 128, "bf16", 16), ([0], [700], 16, 2, 128, "bf16", 16),
