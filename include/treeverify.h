@@ -722,8 +722,9 @@ int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int3
  * workspace  device buffer of at least tv_chunk_attn_workspace_size bytes, 256-byte
  *            aligned; its counters (the first 16 KiB) as in tv_decode_attn: cleared
  *            first, or taken as zero with TV_ATTN_WORKSPACE_ZEROED and left zero
- *            by a call that completes (not by one that reports TV_DEV_TIMEOUT).
- *            Calls that overlap on the GPU need their own.
+ *            by a call that completes, on either kernel (not by one that reports
+ *            TV_DEV_TIMEOUT).  A call of no tokens or requests does nothing, to the
+ *            workspace either.  Calls that overlap on the GPU need their own.
  * num_ctas   persistent grid of the tensor-core kernel (0 = one CTA per SM); at most
  *            4096, the value given to tv_chunk_attn_workspace_size.
  * flags      TV_ATTN_AUTO, TV_ATTN_SIMT (float32 on CUDA cores, every shape) or

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(const __grid_const
 }
 
 template <typename T, int D>
-int launch_simt(const ChunkParams& p, bool zeroed, cudaStream_t stream) {
+int launch_simt(const ChunkParams& p, cudaStream_t stream) {
   using S = Simt<D>;
   const int64_t tokens = S::kRows / std::min(p.G, S::kRows);
   const int64_t units = p.cu ? p.T / tokens + p.B : tv::ceil_div(p.T / p.B, tokens) * p.B;
@@ -335,7 +335,6 @@ int launch_simt(const ChunkParams& p, bool zeroed, cudaStream_t stream) {
   const int64_t groups = tv::ceil_div(p.G, S::kRows), ctas = units * p.Hkv * groups;
   const int split = (int)std::max<int64_t>(1, std::min<int64_t>(kPieces, kSlots / ctas));
   static_assert((size_t)S::kRows * (D + 2) <= kSlotFloats, "a piece fits its slot");
-  if (split > 1 && !zeroed) TV_CUDA_TRY(cudaMemsetAsync(p.arrive, 0, kCounterBytes, stream));
   const dim3 grid((unsigned)units, (unsigned)p.Hkv, (unsigned)(groups * split));
   chunk_simt_kernel<T, D><<<grid, kThreads, S::kBytes, stream>>>(p, split);
   TV_LAUNCH_CHECK("chunk_simt_kernel");
@@ -343,10 +342,10 @@ int launch_simt(const ChunkParams& p, bool zeroed, cudaStream_t stream) {
 }
 
 template <typename T>
-int dispatch_simt(const ChunkParams& p, int D, bool zeroed, cudaStream_t stream) {
-  return D == 64    ? launch_simt<T, 64>(p, zeroed, stream)
-         : D == 128 ? launch_simt<T, 128>(p, zeroed, stream)
-                    : launch_simt<T, 256>(p, zeroed, stream);
+int dispatch_simt(const ChunkParams& p, int D, cudaStream_t stream) {
+  return D == 64    ? launch_simt<T, 64>(p, stream)
+         : D == 128 ? launch_simt<T, 128>(p, stream)
+                    : launch_simt<T, 256>(p, stream);
 }
 
 int check_shape(const char* fn, int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t dtype, int32_t num_ctas) {
@@ -444,19 +443,21 @@ extern "C" int tv_chunk_attn(const void* q, int64_t q_stride, const void* k_cach
   p.status = status;
   p.arrive = static_cast<uint32_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
-  const bool zeroed = flags & TV_ATTN_WORKSPACE_ZEROED;
+  const char* why = "TV_ATTN_SIMT";
   if ((flags & 3) != TV_ATTN_SIMT) {
     tv::DeviceInfo dev;
     if (int rc = tv::current_device_info(&dev)) return rc;
-    const char* why = tv::chunk_tc_unsupported(dev, p, dtype, head_dim);
-    if (!why) {
-      if (int rc = grid_of(num_ctas, &p.ctas)) return rc;
-      p.m_tiles = tv::chunk_tc_m_tiles(head_dim);
-      p.part_ml = p.part_o + (int64_t)p.ctas * 2 * 128 * p.m_tiles * head_dim;
-      if (!zeroed) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
-      return tv::launch_chunk_tc(p, head_dim, st);
-    }
-    if ((flags & 3) == TV_ATTN_TCGEN05) return tv::fail(TV_ERR_UNSUPPORTED, "tv_chunk_attn: no tcgen05 kernel: %s", why);
+    why = tv::chunk_tc_unsupported(dev, p, dtype, head_dim);
+    if (why && (flags & 3) == TV_ATTN_TCGEN05)
+      return tv::fail(TV_ERR_UNSUPPORTED, "tv_chunk_attn: no tcgen05 kernel: %s", why);
   }
-  return dtype == TV_BF16 ? dispatch_simt<__nv_bfloat16>(p, head_dim, zeroed, st) : dispatch_simt<float>(p, head_dim, zeroed, st);
+  // also where this call cuts no unit and counts nothing: the next one may take the counters as zero
+  if (!(flags & TV_ATTN_WORKSPACE_ZEROED)) TV_CUDA_TRY(cudaMemsetAsync(workspace, 0, kCounterBytes, st));
+  if (!why) {
+    if (int rc = grid_of(num_ctas, &p.ctas)) return rc;
+    p.m_tiles = tv::chunk_tc_m_tiles(head_dim);
+    p.part_ml = p.part_o + (int64_t)p.ctas * 2 * 128 * p.m_tiles * head_dim;
+    return tv::launch_chunk_tc(p, head_dim, st);
+  }
+  return dtype == TV_BF16 ? dispatch_simt<__nv_bfloat16>(p, head_dim, st) : dispatch_simt<float>(p, head_dim, st);
 }

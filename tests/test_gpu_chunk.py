@@ -372,6 +372,24 @@ def test_keys_shared_by_ctas_without_tcgen05(D, dtype, bs):
         assert status == 0 and torch.equal(out, want_other) and not ws[:16384].any()
 
 
+@pytest.mark.parametrize("dtype,D,bs", [("f32", 64, 16), ("bf16", 64, 12)])
+def test_counters_are_cleared_by_calls_that_cut_nothing(dtype, D, bs):
+    """A workspace of garbage, then a call without the flag whose rows are many enough to share no keys: the calls behind
+    it, which cut their units, take the counters as zero."""
+    big = _case([0] * 40, [500] * 40, 8, 2, D, dtype, bs, seed=3, poison=False)
+    cut = [_case([5000, 700], [3, 40], 8, 2, 64, "f32", 16, seed=4), _case([4000, 900], [60, 3], 8, 2, 128, "bf16", 16, seed=5)]
+    want = [_run(c)[0] for c in cut]
+    ws = capi.alloc_workspace(max(capi.tv_chunk_attn_workspace_size(8, 2, d, t) for d, t in
+                                  ((D, DT[dtype]), (64, torch.float32), (128, torch.bfloat16))))
+    ws.fill_(255)
+    out, _, status = _run(big, workspace=ws)
+    assert status == 0 and not ws[:16384].any()
+    assert torch.equal(out, _run(big)[0])
+    for c, w in zip(cut, want):
+        out, _, status = _run(c, capi.TV_ATTN_WORKSPACE_ZEROED, workspace=ws)
+        assert status == 0 and torch.equal(out, w) and not ws[:16384].any()
+
+
 def test_one_workspace_for_different_calls():
     ws = capi.alloc_workspace(capi.tv_chunk_attn_workspace_size(16, 2, 128, torch.bfloat16))
     for seed, shape in enumerate((([5000], [3], 8, 1, 128, "bf16", 16), ([0], [700], 16, 2, 128, "bf16", 16),
