@@ -100,6 +100,7 @@ __device__ __forceinline__ uint64_t place(float x, int i) {
 
 struct Scale {
   float m, c1, c2;  // log2 e / T in two floats
+  float floor_y;    // a weight whose log2w() lies below is less than min_p, one 2^-8 above is not
 
   // (x - m) log2 e / T; the first float alone falls with x
   __device__ __forceinline__ float log2w(float x) const { return (x - m) * c1; }
@@ -152,7 +153,28 @@ struct Shared {
   unsigned long long limit, total;
   unsigned long long table[2][kTableSize];  // weights of bf16 logits, by sign and magnitude
   int bin;
+  int least_s;
+  unsigned long long least;
 };
+
+// min_p as least 2^(-43 - least_s), least within [2^43, 2^44).  Below 2^-126 there is no limit: the weights that it would
+// take away have a probability of 0 anyway.  By one thread, before the CTA's next barrier.
+__device__ __forceinline__ void set_least(Shared& sh, float min_p) {
+  int e;
+  sh.least = (unsigned long long)(frexpf(fmaxf(fminf(min_p, 1.f), 0.f), &e) * 0x1p24f) << 20;
+  sh.least_s = 1 - e;
+}
+// log2w() is off by 3 2^-24 of itself, 2^-15 at most here, log2f by less.
+__device__ __forceinline__ float floor_of(float min_p) { return min_p >= FLT_MIN ? log2f(fminf(min_p, 1.f)) - 0x1p-9f : -FLT_MAX; }
+// Whether min_p leaves x, whose log2w() is y.  All passes ask here: what one counts the others find.
+__device__ __forceinline__ bool min_p_leaves(const Scale& sc, const Shared& sh, float x, float y) {
+  if (!(y >= sc.floor_y)) return false;
+  if (y >= sc.floor_y + 0x1p-8f) return true;
+  int s;
+  const unsigned long long w = sc.mantissa(x, sh.powers, s);  // within [2^42.99, 2^43.993)
+  const int d = sh.least_s - s;
+  return d >= 0 && (d > 1 || w << d >= sh.least);
+}
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
 #pragma unroll
@@ -504,10 +526,8 @@ __device__ unsigned long long scan_weights(Shared& sh, int n, unsigned long long
 // A row whose limits leave at most kList candidates: those with a bin up to `bar` and of at least min_p.  They are sorted
 // in the cluster's first CTA, which cuts and draws.  False where there are more.
 template <typename T>
-__device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, float top_p, float least, float floor_y,
-                              float u, int32_t* token) {
+__device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, float top_p, float u, int32_t* token) {
   Shared& sh = r.sh;
-  const unsigned long long least_w = (unsigned long long)__float2ull_ru(least * 0x1p43f);
   __syncthreads();
   if (threadIdx.x == 0) sh.gathered = 0;
   r.cluster.sync();
@@ -516,11 +536,9 @@ __device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, fl
   unsigned long long* weights = r.cluster.map_shared_rank(sh.all_weight, 0);
   r.each([&](float x, int i) {
     const float y = sc.log2w(x);
-    if (!(y >= floor_y) || bin_of(y) > bar) return;
-    const unsigned long long w = sc.weight(x, sh.powers);
-    if (w < least_w) return;
+    if (!(y >= sc.floor_y) || bin_of(y) > bar || !min_p_leaves(sc, sh, x, y)) return;
     const uint32_t k = atomicAdd(count, 1u);
-    if (k < kList) places[k] = place(x, i), weights[k] = w;
+    if (k < kList) places[k] = place(x, i), weights[k] = sc.weight(x, sh.powers);
   });
   r.cluster.sync();
   const uint32_t n_all = *count;
@@ -557,14 +575,12 @@ __device__ bool sample_sorted(Row<T>& r, const Scale& sc, int bar, int top_k, fl
 // Where the kept elements end: the place of the last of them.  True where the chunks' kept masses, and this thread's in
 // kept_here, are known with it.
 template <typename T>
-__device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, float least, float floor_y,
-                            unsigned long long& limit, unsigned long long& kept_here) {
+__device__ bool find_limits(Row<T>& r, const Scale& sc, int top_k, float top_p, unsigned long long& limit,
+                            unsigned long long& kept_here) {
   Shared& sh = r.sh;
   for (int b = threadIdx.x; b < kBins; b += kThreads) sh.count[b] = 0, sh.mass[b] = 0;
   __syncthreads();
-  const unsigned long long least_w = (unsigned long long)__float2ull_ru(least * 0x1p43f);
-  // elements that min_p leaves: by their exact weight, which is looked at near the border alone
-  auto kept = [&](float x, float y) { return y >= floor_y && (y >= floor_y + 0x1p-8f || sc.weight(x, sh.powers) >= least_w); };
+  auto kept = [&](float x, float y) { return min_p_leaves(sc, sh, x, y); };
   r.each([&](float x, int) {
     const float y = sc.log2w(x);
     if (!kept(x, y)) return;
@@ -718,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
   r.v1 = min(p.V, (rank + 1) * p.slice);
   r.wide = (uint64_t)p.V * sizeof(T) % 16 == 0;
   if (threadIdx.x < 64) sh.powers[threadIdx.x] = kPowers[threadIdx.x];
+  if (threadIdx.x == 64) set_least(sh, p.min_p ? p.min_p[at] : 0.f);
 
   float temp = p.temperature ? p.temperature[at] : 1.f;
   int top_k = p.top_k ? p.top_k[at] : 0;
@@ -726,7 +743,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
   float u = p.u[at];
   const bool bad_temp = !(temp >= 0.f && temp < INFINITY);
   if (!(top_p > 0.f)) top_p = top_p <= 0.f ? 0.f : 1.f;  // NaN: no limit
-  const float least = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
 
   // the largest logit, and whether the row has a distribution
   float mine = -INFINITY;  // this thread's largest
@@ -766,10 +782,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
     sc.m = m;
     sc.c1 = (float)c;
     sc.c2 = (float)(c - (double)sc.c1);
+    sc.floor_y = floor_of(min_p);
     if (top_k < 0 || top_k >= p.V) top_k = 0;
-    const float floor_y = least > 0.f ? log2f(least) - 0x1p-9f : -FLT_MAX;
     unsigned long long limit = 0;
-    const unsigned long long least_w = (unsigned long long)__float2ull_ru(least * 0x1p43f);
     // Few candidates: those above a bar that top_k of the threads' largest elements reach.
     int bar = kBins - 1;
     if (top_k > 0 && top_k <= 128 * C) {
@@ -780,14 +795,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
       const int b = r.template find_bin<false>(top_k, kBins - 1, 0);
       if (b >= 0) bar = b;
     }
-    if (bar < kBins - 1 && sample_sorted(r, sc, bar, top_k, top_p, least, floor_y, u, p.tokens + at)) {
+    if (bar < kBins - 1 && sample_sorted(r, sc, bar, top_k, top_p, u, p.tokens + at)) {
       cluster.sync();
       if (probs) {
         limit = *cluster.map_shared_rank(&sh.limit, 0);
         const float inv = (float)(0x1p43 / (double)*cluster.map_shared_rank(&sh.total, 0));
         r.each([&](float x, int i) {
           const float y = sc.log2w(x);
-          const bool in = y >= floor_y && place(x, i) >= limit && (least_w == 0 || sc.weight(x, sh.powers) >= least_w);
+          const bool in = y >= sc.floor_y && place(x, i) >= limit && min_p_leaves(sc, sh, x, y);
           if (i < r.v1) probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
         });
       }
@@ -797,13 +812,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
     r.fill_table(sc);
     bool known = false;
     unsigned long long total = 0, none = 0, before = 0;
-    if (top_k > 0 || top_p < 1.f) known = find_limits(r, sc, top_k, top_p, least, floor_y, limit, total);
+    if (top_k > 0 || top_p < 1.f) known = find_limits(r, sc, top_k, top_p, limit, total);
 
     // kept mass of every 256 elements
     auto kept_weight = [&](float x, int i) -> unsigned long long {
-      if (!(sc.log2w(x) >= floor_y) || place(x, i) < limit) return 0;
-      const unsigned long long w = r.weight(sc, x);
-      return w >= least_w ? w : 0;
+      const float y = sc.log2w(x);
+      return y >= sc.floor_y && place(x, i) >= limit && min_p_leaves(sc, sh, x, y) ? r.weight(sc, x) : 0;
     };
     const int lane = threadIdx.x % 32;
     if (!known) total = 0;
@@ -870,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const __grid_
       const float inv = (float)(0x1p43 / (double)total);
       r.each([&](float x, int i) {
         const float y = sc.log2w(x);
-        const bool in = y >= floor_y && place(x, i) >= limit && (least_w == 0 || sc.weight(x, sh.powers) >= least_w);
+        const bool in = y >= sc.floor_y && place(x, i) >= limit && min_p_leaves(sc, sh, x, y);
         if (i < r.v1) probs[i] = in ? sc.probability(x, sh.powers) * inv : 0.f;
       });
     }

@@ -76,6 +76,35 @@ def test_limits_that_are_off_and_at_their_ends():
     assert torch.equal(a, capi.tv_token_sample(x[:2], torch.tensor([0.3, 0.6]).cuda()))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("least", [1e-40, 1e-30, 1e-20, 1e-13, 1e-12, 1e-11, 1e-9])
+def test_limits_below_a_unit_of_the_sums(least, dtype):
+    """min_p below 2^-43 and just above it, on logits down to -100: sorted (top_k 9), by bins, without other limits."""
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(np.stack([rng.permutation(np.linspace(0.0, -100.0, 1000)) for _ in range(4)])).to(DT[dtype]).cuda()
+    u = rng.uniform(size=4)
+    for kw in (dict(), dict(top_k=[9, 99, 300, 999]), dict(top_p=[0.3, 0.9999, 1.0, 1.0 - 2.0 ** -24]),
+               dict(top_k=[300, 999, 9, 40], top_p=[1.0 - 2.0 ** -24] * 4), dict(temperature=[0.7, 3.0, 1.5, 1e-3])):
+        _check(x, u, min_p=[least] * 4, **kw)
+    two = torch.tensor([[0.0, -32.0]], device="cuda", dtype=DT[dtype])
+    _, probs = _check(two, [0.5], min_p=[least])
+    assert bool(probs[0, 1] > 0) == (np.exp(-32.0) >= least)
+
+
+@pytest.mark.parametrize("u", [1.0 - 2.0 ** -24, 1.0 - 2.0 ** -23, 1.0])
+def test_a_draw_among_weights_of_a_few_units(u):
+    """200,000 tokens of 5.3 2^-43 behind one of 1, min_p between 5 and 5.3 of these units, a draw among them: a kept token
+    (which one is beyond the sums' resolution)."""
+    x = torch.full((3, 200000), -28.14, device="cuda")
+    x[:, 0] = 0.0
+    tokens, probs = torch.full((3,), -7, dtype=torch.int32, device="cuda"), torch.zeros_like(x)
+    col = lambda *v: torch.tensor(v, device="cuda")
+    capi.tv_token_sample(x, col(u, u, u), top_p=col(1.0 - 2.0 ** -24, 1.0, 1.0 - 2.0 ** -24),
+                         min_p=col(5.2 * 2.0 ** -43, 5.2 * 2.0 ** -43, 0.0), tokens=tokens, probs=probs)
+    assert ((tokens >= 0) & (tokens < 200000)).all()
+    assert (probs.gather(1, tokens.long()[:, None]) > 0).all()
+
+
 def test_uniforms_at_the_ends():
     x = _logits(6, 5000, "f32", 6)
     u = [0.0, 1.0 - 2.0 ** -24, 1.0, 1.5, -0.5, 2.0 ** -149]
