@@ -792,8 +792,9 @@ int tv_token_logprobs(const void* logits, const int32_t* tokens, const int32_t* 
  * min_p; of these, in descending order, the shortest run whose sum reaches top_p of
  * theirs (at least one).  The token is the first index whose running sum over the
  * kept w exceeds u times their total.  Sums are exact over weights that are good
- * to 2^-39 of themselves or 2^-44 of the largest, so a token is the one of the
- * definition in float64 unless u falls on the border of two.
+ * to 2^-36 of themselves or 2^-44 of the largest, so a token is the one of the
+ * definition in float64 unless u falls on the border of two, or an element on that
+ * of a limit.
  *
  * logits    device [R, V] (dtype), contiguous; -inf: an excluded token.
  * temperature device float32 [R] (nullable: 1): 0 (or anything below 2^-60): the
@@ -807,8 +808,8 @@ int tv_token_logprobs(const void* logits, const int32_t* tokens, const int32_t* 
  * u         device float32 [R] in [0, 1): 1 or more gives the last kept token with any
  *           weight, less than 0 or NaN the first.
  * tokens    device int32 [R] out.
- * probs     device float32 [R, V] out (nullable): w_i / their total, 0 for a token that
- *           is not kept.
+ * probs     device float32 [R, V] out (nullable): w_i / their total, within three
+ *           roundings, 0 for a token that is not kept or of w_i < 2^-126.
  * A row that holds a NaN or +inf, or nothing above -inf, has no distribution: its
  * token is -1, its probabilities are NaN.
  * logits and probs 16-byte aligned; V <= 1,048,576 (else TV_ERR_UNSUPPORTED).

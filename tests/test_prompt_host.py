@@ -4,6 +4,7 @@ launched, and the oracle's definitions agree with independent ones."""
 
 import ctypes
 import os
+import re
 
 import numpy as np
 import pytest
@@ -122,6 +123,60 @@ def test_sample_refuses_on_the_host(change, code, text):
 
 def test_sample_of_nothing():
     assert _call("tv_token_sample", SAMPLE, R=0) == 0
+
+
+def _weight_mantissa(x, m, temperature):
+    """The arithmetic of the sampling kernel's weights, float32 operation by operation: w as (mantissa, s), w = mantissa
+    2^(-43 - s).  A fused product and sum goes through float64, which holds the product exactly."""
+    f = np.float32
+    fma = lambda a, b, c: (np.float64(a) * np.float64(b) + np.float64(c)).astype(f)
+    c = 1.4426950408889634074 / float(f(temperature))
+    c1 = f(c)
+    c2 = f(c - float(c1))
+    dh = x - m
+    back = dh - x
+    dl = (x - (dh - back)) - (m + back)
+    yh = dh * c1
+    yl = fma(dh, c1, -yh) + fma(dh, c2, dl * c1)
+    n = np.rint(yh * f(64))
+    rh = fma(n, f(-2.0 ** -6), yh)
+    hi, lo = f(0.693147182464599609375), f(-1.904654323148236e-09)
+    th = rh * hi
+    tl = fma(rh, hi, -th) + fma(rh, lo, yl * hi)
+    t = th + tl
+    q = t * t * fma(t, fma(t, fma(t, f(1 / 120), f(1 / 24)), f(1 / 6)), f(0.5))
+    e = np.rint(th * f(2.0 ** 38)).astype(np.int64) + np.rint((tl + q) * f(2.0 ** 38)).astype(np.int64)
+    powers = np.array([round(np.exp2(np.longdouble(j) / 64) * 2 ** 43) for j in range(64)], dtype=np.int64)
+    ni = n.astype(np.int64)
+    p = powers[ni & 63]
+    return p + ((p >> 12) * e >> 26), -(ni >> 6), powers
+
+
+def test_sampling_weights_bound():
+    """A weight is good to 2^-36 of itself.  In units of 2^-39: q, below 2^-16.05, takes five float32 roundings (2.41) and
+    its sum with tl a sixth (0.25); the two roundings to units of 2^-38 are one each (2); p >> 12 cuts 2^-31 of a factor of
+    |e^t - 1| < 2^-7.5 (1.39); what tl gathers is 0.9 for weights down to 2^-126; the table and the last cut 0.1; all of it
+    over e^-|t|, 7.1.  The table is the one in the source."""
+    assert re.sub(r"\s", "", ",".join(f"{v}ull" for v in _weight_mantissa(np.zeros(1, np.float32), np.float32(0), 1.0)[2])) in \
+        re.sub(r"\s", "", open(os.path.join(B.CSRC, "sample.cu")).read())
+    rng = np.random.default_rng(5)
+    worst = 0.0
+    for temperature in (1.0, 0.6, 1.2, 1e-3, 0.013, 50.0, 1e9, 2.0 ** -30):
+        for most in (0.02, 1.0, 20.0, 44.0, 126.0):  # log2 w down to
+            for top in (0.0, 9.7, -3.3, 180.25):
+                m = np.float32(top * temperature)
+                t = float(np.float32(temperature))
+                x = (m - rng.uniform(0.0, most * np.log(2.0) * t, size=20000)).astype(np.float32)
+                x = np.concatenate((x, [m])).astype(np.float32)
+                exact = (x.astype(np.longdouble) - np.longdouble(m)) / np.longdouble(t)
+                with np.errstate(under="ignore"):
+                    got, s, _ = _weight_mantissa(x, m, temperature)
+                live = exact / np.log(np.longdouble(2)) > -126
+                w = got.astype(np.longdouble) * np.exp2(np.longdouble(-43) - s)
+                worst = max(worst, float((np.abs(w / np.exp(exact) - 1))[live].max()))
+                assert w[-1] == 1
+                assert ((got >= 2.0 ** 42.99) & (got < 2.0 ** 43.993)).all()
+    assert 2.0 ** -39 < worst <= 2.0 ** -36, worst * 2.0 ** 39
 
 
 def test_binding_names_what_it_refuses():
