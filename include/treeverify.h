@@ -700,6 +700,12 @@ int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int3
  * A score of -inf has no weight; a row without any weight (no visible key: its
  * position is below 0, n being larger than L_b; or every score -inf) is zero with
  * lse = -inf.  Visible values are finite.
+ * Scores, maxima, sums and lse are float32.  The tensor-core kernel (bf16) rounds
+ * each weight to bf16 before it multiplies V, by 2^-8 of itself at most, where
+ * tv_decode_attn and the CUDA-core kernel hold more; its sum and lse take the
+ * weight as it was.  With a cap of up to 88 its scores are within 2^-21 of the cap,
+ * else, and in the others, within 2^-21 of themselves (and what a float32 sum of
+ * products adds).
  * No page defines the call: it is the chain case of "Tree Verification", "Tree
  * Attention", with the chain's K/V in the cache.
  *

@@ -20,8 +20,9 @@
 // * Softmax: a thread per row, against a reference that is the first tile's
 //   maximum and moves, with O rescaled in TMEM, only when weights pass 2^20; so
 //   later tiles need no maximum at all (it took a third of a tile's time).  Weights are rounded to bf16 for
-//   P V (an operand of kind::f16 holds no more; half a step, 2^-9 of a weight on
-//   average, against the 2^-9 that rounding the output takes), their sum is not.
+//   P V (an operand of kind::f16 holds no more; half a step, 2^-8 of a weight at
+//   most, as much as rounding the output takes), their sum is not.  A second bf16
+//   part, as tv_decode_attn has it, would double P V and its reads of V.
 // * Work: the units' tiles (with a few virtual ones for a unit's fixed cost) lie
 //   end to end and each CTA of a persistent grid takes an equal run.  The sums
 //   over a request's units have a closed form (floor sums), so a CTA finds its
@@ -666,7 +667,10 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
       }
       if constexpr (kAny) {
         if (cap_in > 0.f || cap_in < 0.f) {
-          // tanh y = 1 - 2 / (1 + e^2y): off by 2^-22 of the cap at most, which is 3e-5 here
+          // tanh y = 1 - 2 / (1 + e^2y): off by 2^-21 of the cap at most, 4e-5 here, small scores as much as large ones.  In
+          // units of 2^-24 around y = -0.8, where the sum is largest: the argument's factors and product 1.5, the exponential
+          // (2^-22) 1.2, 1 + e^2y 1.4, the reciprocal (a step) 2, the cap's factor and the last product 1.7.  (Scorer's form
+          // keeps small scores' bits: 16 windows of 1024 with a cap of 30 take 1070 us with it, 620 this way.)
 #pragma unroll
           for (int c = 0; c < 64; ++c) sv[c] = fmaf(rcp_approx(1.f + exp2_approx(sv[c] * cap_in)), -2.f * score.cap2, score.cap2);
         } else {

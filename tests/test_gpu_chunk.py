@@ -191,6 +191,27 @@ def test_masks_caps_and_biases(mask, dtype, D, bs, kernel):
     _check(c, out, lse, kernel == "auto" and dtype == "bf16")
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", [88.0, 50.0, 30.0, 5.0, 0.5])
+def test_caps_of_small_scores(cap, D):
+    """Scores far below the cap: the tcgen05 kernel's are within 2^-21 of the cap, however small they are, so lse is too and a
+    weight within twice that; the CUDA-core kernel's are within the bounds of _check, which go by the score."""
+    c = _case([40, 600], [200, 70], 8, 2, D, "bf16", 16, seed=11, gain=0.05, softcap=cap)
+    out, lse, status = _run(c, capi.TV_ATTN_TCGEN05)
+    assert status == 0
+    u = 2.0 ** -8
+    for first, ro, rl, pv, size, L in _dense(c):
+        n = ro.shape[0]
+        es = size * (D + 8) * 2.0 ** -24 + cap * 2.0 ** -21
+        sums = 2.0 ** -21 + (L / 32 + 64) * 2.0 ** -24
+        assert ((lse[first:first + n].double() - rl).abs() <= es + 2 * sums + rl.abs() * 2.0 ** -22).all()
+        bound = (2 * es + 2 * sums + u)[..., None] * pv
+        assert ((out[first:first + n].double() - ro).abs() <= bound + u * (ro.abs() + bound)).all()
+    out, lse, status = _run(c, capi.TV_ATTN_SIMT)
+    assert status == 0
+    _check(c, out, lse, False)
+
+
 def test_the_oracle_agrees():
     c = _case([3, 20], [5, 9], 4, 2, 64, "f32", 16, window=8, n_sink=2, softcap=4.0, alibi=True, poison=False)
     out, lse, _ = _run(c)
