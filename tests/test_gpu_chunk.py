@@ -173,6 +173,31 @@ def test_matches_float64(shape, kernel):
     assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()  # rows behind the last request
 
 
+@pytest.mark.parametrize("G,Hkv,D,bs", [(32, 3, 128, 16), (64, 2, 64, 32), (96, 2, 128, 16), (128, 2, 128, 64), (32, 2, 256, 16),
+                                        (96, 1, 64, 24), (128, 3, 256, 16)])
+@pytest.mark.parametrize("ctas", [0, 3, 40])
+def test_wide_groups_on_tcgen05(G, Hkv, D, bs, ctas):
+    """Groups of a multiple of 32 query heads: outputs in boxes of 32 heads of one token; 1 to 4 tokens an M tile, the last
+    units partly filled, cut by other grids."""
+    c = _case([700, 0, 13, 4000], [37, 70, 1, 5], G * Hkv, Hkv, D, "bf16", bs, seed=G, pad=2, fused=True, window=900, n_sink=3)
+    out, lse, status = _run(c, capi.TV_ATTN_TCGEN05, num_ctas=ctas)
+    assert status == 0
+    _check(c, out, lse, True)
+    assert (out[113:] == 7.0).all() and (lse[113:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_lengths_past_the_table_are_clamped(dtype, D):
+    """A length of more positions than the block table has counts as the table's."""
+    c = _case([100, 90, 5], [28, 38, 40], 4, 2, D, dtype, 16, poison=False)
+    assert c["table"].shape[1] == 8
+    want, wl, _ = _run(dict(c, lens=torch.tensor([128, 128, 45], dtype=torch.int32, device="cuda")))
+    for past in (129, 4000, 2 ** 31 - 1):
+        out, lse, status = _run(dict(c, lens=torch.tensor([past, 128, 45], dtype=torch.int32, device="cuda")))
+        assert status == 0 and torch.equal(out, want) and torch.equal(lse, wl)
+    _check(c, want, wl, dtype == "bf16")
+
+
 MASKS = [
     dict(window=1), dict(window=16), dict(window=100, n_sink=4), dict(window=129, n_sink=200), dict(window=5000, n_sink=3),
     dict(window=2 ** 31 - 1, n_sink=2 ** 31 - 1), dict(softcap=5.0), dict(softcap=0.01), dict(softcap=1e30),
