@@ -25,7 +25,7 @@
 //   part, as tv_decode_attn has it, would double P V and its reads of V.
 // * Work: the units' tiles (with a few virtual ones for a unit's fixed cost) lie
 //   end to end and each CTA of a persistent grid takes an equal run.  The sums
-//   over a request's units have a closed form (floor sums), so a CTA finds its
+//   over a request's units have a closed form (tiles_below), so a CTA finds its
 //   run from lengths and offsets alone.  A unit cut by a run's end leaves
 //   (max, sum, output) of each piece in the workspace and the CTA whose piece
 //   arrives last joins them in order, so results do not depend on timing.
@@ -105,31 +105,28 @@ __device__ __forceinline__ bool withhold(uint32_t) { return false; }
 
 // ---------------------------------------------------------------- the plan
 
-// sum over j < n of floor((b + a j) / m), b >= 0: whole parts are summed apart, what is left is counted along the other
-// axis (the steps of Euclid's algorithm on a and m).
-__device__ int64_t floor_sum(int64_t n, int64_t a, int64_t b, int64_t m) {
-  int64_t sum = 0;
-  while (true) {
-    if (a >= m) {
-      sum += n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
-    }
-    const int64_t top = a * n + b;
-    if (top < m) return sum;
-    n = top / m;
-    b = top % m;
-    const int64_t t = a;
-    a = m;
-    m = t;
+// The residues of a step's multiples: a k mod 64 repeats after 64 / gcd(a, 64) turns, a power of two.
+struct Residues {
+  uint16_t sum[kBlk + 1];  // of the first i of them, up to a period
+  uint8_t log_gcd, log_period;
+  uint8_t inverse;         // of a / gcd(a, 64) modulo the period
+};
+
+Residues residues_of(int a) {
+  Residues r{};
+  while (r.log_gcd < 6 && a % (2 << r.log_gcd) == 0) ++r.log_gcd;
+  r.log_period = 6 - r.log_gcd;
+  const int period = 1 << r.log_period;
+  for (int k = 0; k < period; ++k) {
+    r.sum[k + 1] = r.sum[k] + a * k % kBlk;
+    if ((a >> r.log_gcd) * k % period == 1 % period) r.inverse = k;
   }
+  return r;
 }
 
-// sum over j < n of max(0, floor((b + a j) / 64)), a >= 1
-__device__ int64_t tiles_below(int64_t n, int a, int64_t b) {
+// sum over j < n of max(0, floor((b + a j) / 64)), a >= 1: the terms' own sum without their residues'.  With b = 64 .. + g i
+// + rest, g = gcd(a, 64), the residues are rest + (a (k + j) mod 64), k = i times the inverse: a run of the table.
+__device__ int64_t tiles_below(int64_t n, int a, int64_t b, const Residues& r) {
   if (n <= 0) return 0;
   if (b < 0) {
     const int64_t skip = (-b + a - 1) / a;
@@ -137,16 +134,11 @@ __device__ int64_t tiles_below(int64_t n, int a, int64_t b) {
     n -= skip;
     b += skip * a;
   }
-  if ((a & (a - 1)) == 0 && a <= kBlk) {  // steps of a power of two: runs of r equal terms
-    const int r_log = 6 - (31 - __clz(a));
-    auto upto = [&](int64_t x) {  // sum over i < x of floor(i / r)
-      const int64_t q = x >> r_log;
-      return (q * (q - 1) / 2 << r_log) + q * (x - (q << r_log));
-    };
-    const int64_t c = b >> (31 - __clz(a));
-    return upto(c + n) - upto(c);
-  }
-  return floor_sum(n, a, b, kBlk);
+  const int period = 1 << r.log_period, first = (int)(b % kBlk);
+  const int k = (first >> r.log_gcd) * r.inverse & (period - 1), end = k + (int)(n & (period - 1));
+  const int run = r.sum[min(end, period)] + r.sum[max(0, end - period)] - r.sum[k];
+  const int64_t residues = n * (first & ((1 << r.log_gcd) - 1)) + (n >> r.log_period) * r.sum[period] + run;
+  return (n * b + n * (n - 1) / 2 * a - residues) / kBlk;
 }
 
 // One request's units.
@@ -170,13 +162,13 @@ struct Request {
     return 1 + max(0, last) / kBlk - skipped;
   }
   // Tiles (and virtual ones) of the units before i, i < units
-  __device__ __forceinline__ int64_t before(int i, int cost) const {
-    int64_t n = (int64_t)i * (1 + cost) + tiles_below(i, step, (int64_t)c.first + step - 1);
-    if (window > 0) n -= tiles_below(i, step, (int64_t)c.first + 1 - window - (int64_t)sinks * kBlk);
+  __device__ __forceinline__ int64_t before(int i, int cost, const Residues& r) const {
+    int64_t n = (int64_t)i * (1 + cost) + tiles_below(i, step, (int64_t)c.first + step - 1, r);
+    if (window > 0) n -= tiles_below(i, step, (int64_t)c.first + 1 - window - (int64_t)sinks * kBlk, r);
     return n;
   }
-  __device__ __forceinline__ int64_t all(int cost) const {
-    return units ? before(units - 1, cost) + tiles(units - 1) + cost : 0;
+  __device__ __forceinline__ int64_t all(int cost, const Residues& r) const {
+    return units ? before(units - 1, cost, r) + tiles(units - 1) + cost : 0;
   }
 };
 
@@ -196,7 +188,7 @@ __device__ __forceinline__ int64_t run_start(int64_t c, int64_t total, int64_t c
 __device__ __forceinline__ int64_t run_of(int64_t x, int64_t total, int64_t ctas) { return divide((x + 1) * ctas - 1, total); }
 
 // All threads of the CTA.
-__device__ void make_plan(const ChunkParams& p, int cost, int least, float join_cost, Plan& plan) {
+__device__ void make_plan(const ChunkParams& p, const Residues& res, int cost, int least, float join_cost, Plan& plan) {
   __shared__ int64_t sums[kThreads / 32 + 1];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -205,7 +197,7 @@ __device__ void make_plan(const ChunkParams& p, int cost, int least, float join_
   for (int b = b0; b < b1; ++b) {
     Request r;
     r.set(p, b);
-    mine += r.all(cost);
+    mine += r.all(cost, res);
   }
   mine *= p.Hkv;
   int64_t run = mine;
@@ -235,16 +227,16 @@ __device__ void make_plan(const ChunkParams& p, int cost, int least, float join_
     int64_t at = start;
     for (;; ++b) {
       r.set(p, b);
-      const int64_t n = r.all(cost) * p.Hkv;
+      const int64_t n = r.all(cost, res) * p.Hkv;
       if (x0 < at + n) break;
       at += n;
     }
     int lo = 0;  // the last unit that starts at or before x0
     for (int hi = r.units; hi - lo > 1;) {
       const int mid = lo + (hi - lo) / 2;
-      if (at + r.before(mid, cost) * p.Hkv <= x0) lo = mid; else hi = mid;
+      if (at + r.before(mid, cost, res) * p.Hkv <= x0) lo = mid; else hi = mid;
     }
-    at += r.before(lo, cost) * p.Hkv;
+    at += r.before(lo, cost, res) * p.Hkv;
     const int one = r.tiles(lo) + cost;
     plan.kvh = (int)divide(x0 - at, one);
     plan.at = at + (int64_t)plan.kvh * one;
@@ -892,8 +884,8 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
 
 template <int D, bool kAny>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps, int cost, int least,
-                    float join_cost) {
+    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ Maps maps,
+                    const __grid_constant__ Residues res, int cost, int least, float join_cost) {
   using C = Cfg<D>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
@@ -906,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = threadIdx.x; b < p.B; b += kThreads)
       if (!chunk_of(p, b, c)) atomicOr(p.status, TV_DEV_BAD_OFFSETS);
   }
-  make_plan(p, cost, least, join_cost, plan);
+  make_plan(p, res, cost, least, join_cost, plan);
   if (plan.x0 >= plan.x1) return;  // all threads, before anything is set up
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -1020,7 +1012,7 @@ int launch(const ChunkParams& p, const Maps& maps, cudaStream_t stream) {
   const int64_t units = (int64_t)p.Hkv * std::max<int64_t>(ceil_div(p.T, step), std::min(p.T, p.B));
   const int64_t rows = std::min<int64_t>(step, ceil_div(p.T, p.B)) * p.G;
   const float join_cost = 0.8f * (float)ceil_div(rows, 64) / (float)units;
-  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, 4, 8, join_cost);
+  chunk_tc_kernel<D, kAny><<<p.ctas, kThreads, smem, stream>>>(p, maps, residues_of(step), 4, 8, join_cost);
   TV_LAUNCH_CHECK("chunk_tc_kernel");
   return TV_OK;
 }

@@ -351,6 +351,17 @@ def test_any_grid(ctas, D):
     _check(c, out, lse, True)
 
 
+@pytest.mark.parametrize("G", [1, 3, 5, 6, 7, 12, 20, 43])
+@pytest.mark.parametrize("D,window", [(128, 0), (64, 700), (256, 0)])
+def test_any_group_cut_anywhere(G, D, window):
+    """Steps of 256 down to 2 tokens a unit, most of them no power of two: the runs of many grids meet without a gap."""
+    c = _case([900, 0, 2000, 40], [100, 300, 5, 1], 2 * G, 2, D, "bf16", 16, seed=G, window=window, n_sink=70)
+    for ctas in (1, 13, 152, 1000):
+        out, lse, status = _run(c, num_ctas=ctas)
+        assert status == 0
+        _check(c, out, lse, True)
+
+
 @pytest.mark.parametrize("D,G,bs", [(128, 4, 16), (64, 4, 64), (128, 16, 8), (256, 4, 16)])
 def test_long_runs_of_a_cta(D, G, bs):
     """Few CTAs: hundreds of tiles each, half of an M tile pair idle for whole requests, and then not."""
