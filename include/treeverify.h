@@ -591,7 +591,9 @@ int tv_kv_append(const void* q, int64_t q_stride, void* q_out, int64_t q_out_str
  *   y = x * weight / sqrt(mean(x^2) + eps), its leading rot_dim elements turned
  * by the position's angles.  Sums, factors and rotation are float32 and a row is
  * rounded once; a row whose squares leave float32 follows float32's rules.  Without
- * weights, interleaving and with rot_dim = head_dim it gives tv_kv_append's bits.
+ * weights, interleaving and with rot_dim = head_dim it gives tv_kv_append's bits;
+ * elements that are neither normalised nor rotated keep theirs, but a bf16 NaN of
+ * queries and keys becomes 7fff.
  *
  * q_weight  device [head_dim] (dtype), nullable: queries are not normalised.
  * k_weight  device [head_dim] (dtype), nullable: keys are not normalised.

@@ -102,6 +102,25 @@ def test_without_norm_the_bits_of_kv_append(dtype, D, T):
         assert torch.equal(a, b)
 
 
+def test_without_norm_and_rotation_the_bits_of_every_value():
+    """All 65536 bf16 values as queries, keys and values: what is neither normalised nor rotated keeps its bits, as in
+    tv_kv_append, but for the NaNs of queries and keys, which become one."""
+    c = _case([3], [1024], 2, 1, 64, "bf16", 16, 14, rot=0)
+    as_bits = lambda x: x.contiguous().view(torch.int16)
+    one_nan = lambda x: torch.where(torch.isnan(x), torch.full_like(as_bits(x), 0x7fff), as_bits(x))
+    bits = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(1024, 1, 64)
+    rows = bits.expand(1024, 4, 64).contiguous().view(torch.bfloat16)
+    c["q"], c["k"], c["v"] = rows[:, :2], rows[:, 2:3], rows[:, 3:]
+    kc, vc, lens, q = _append(c, norm=(False, False))
+    kc2, vc2 = c["k_cache"].clone(), c["v_cache"].clone()
+    capi.tv_kv_append(c["k"], c["v"], kc2, vc2, c["table"], c["lens"], cu_new=c["cu"])
+    assert torch.equal(as_bits(kc), one_nan(kc2)) and torch.equal(as_bits(vc), as_bits(vc2))
+    assert torch.equal(as_bits(q), one_nan(c["q"]))
+    c["cs"] = capi.tv_rope_table(1028, 32)  # the second half of a head is not rotated
+    kc, vc, lens, q = _append(c, norm=(False, False))
+    assert torch.equal(as_bits(q[..., 32:]), one_nan(c["q"][..., 32:]))
+
+
 def test_rows_of_zeros_and_of_large_and_small_values():
     c = _case([0], [4], 2, 2, 64, "f32", 16, 12)
     rows = torch.empty(4, 6, 64, device="cuda").normal_()
