@@ -741,7 +741,8 @@ int tv_chunk_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t head_dim, int3
  * status     device int32 (nullable): TV_DEV_BAD_OFFSETS; TV_DEV_BAD_BLOCK (a visible
  *            position's block is outside [0, num_blocks): its key and value count
  *            as zeros); TV_DEV_TIMEOUT.
- * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, any Hq / Hkv, Hkv <= 65535;
+ * Supported: head_dim in {64, 128, 256}, Hq % Hkv == 0, Hq / Hkv <= 2,097,120,
+ * Hkv <= 65535;
  * q, out and the caches 16-byte aligned, q_stride a multiple of 16 bytes (unused
  * for one token).
  */

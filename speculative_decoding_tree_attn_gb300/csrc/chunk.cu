@@ -356,6 +356,8 @@ int check_shape(const char* fn, int32_t Hq, int32_t Hkv, int32_t head_dim, int32
     return tv::fail(TV_ERR_UNSUPPORTED, "%s: head_dim %d not in {64, 128, 256}", fn, head_dim);
   if (Hkv > 65535 || (int64_t)Hq * head_dim >= INT32_MAX / 4)
     return tv::fail(TV_ERR_UNSUPPORTED, "%s: more than 65535 KV heads, or a token's heads exceed 2^29 elements", fn);
+  if (Hq / Hkv > 65535 * 32)  // the CUDA-core kernel's grid: a CTA has 32 or 64 rows
+    return tv::fail(TV_ERR_UNSUPPORTED, "%s: more than %d query heads per KV head", fn, 65535 * 32);
   return TV_OK;
 }
 

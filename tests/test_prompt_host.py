@@ -85,6 +85,14 @@ def test_chunk_refuses_on_the_host(change, code, text):
     assert text in capi.lib().tv_last_error()
 
 
+def test_chunk_refuses_groups_past_its_grid():
+    for change in (dict(Hq=1 << 22, Hkv=1), dict(Hq=65535 * 32 + 1, Hkv=1), dict(Hq=3 << 21, Hkv=2)):
+        assert _call("tv_chunk_attn", CHUNK, q_stride=1 << 29, **change) == -4
+        assert b"query heads per KV head" in capi.lib().tv_last_error()
+    with pytest.raises(capi.TVError, match="query heads"):
+        capi.tv_chunk_attn_workspace_size(1 << 22, 1, 64, torch.float32)
+
+
 def test_chunk_of_nothing():
     assert _call("tv_chunk_attn", CHUNK, B=0) == 0
     assert _call("tv_chunk_attn", CHUNK, T=0) == 0
