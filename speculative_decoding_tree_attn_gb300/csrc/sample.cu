@@ -26,7 +26,8 @@
 //
 // A row is read again for each pass, from L2: bound by the instructions of the
 // exact pass (45 an element of float32, 15 of bf16) where there is no top_k, by
-// the passes' exchanges where there are few rows.
+// the passes' exchanges where there are few rows.  64 registers (two CTAs an SM)
+// spill 12 to 32 bytes.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -167,14 +168,17 @@ __device__ __forceinline__ void set_least(Shared& sh, float min_p) {
 }
 // log2w() is off by 3 2^-24 of itself, 2^-15 at most here, log2f by less.
 __device__ __forceinline__ float floor_of(float min_p) { return min_p >= FLT_MIN ? log2f(fminf(min_p, 1.f)) - 0x1p-9f : -FLT_MAX; }
-// Whether min_p leaves x, whose log2w() is y.  All passes ask here: what one counts the others find.
-__device__ __forceinline__ bool min_p_leaves(const Scale& sc, const Shared& sh, float x, float y) {
-  if (!(y >= sc.floor_y)) return false;
-  if (y >= sc.floor_y + 0x1p-8f) return true;
+// Whether a weight near the border reaches min_p.  A call of its own: inlined into every pass it took 3-10 % of short rows.
+__device__ __noinline__ bool reaches(float m, float c1, float c2, const Shared& sh, float x) {
+  const Scale sc{m, c1, c2, 0.f};
   int s;
   const unsigned long long w = sc.mantissa(x, sh.powers, s);  // within [2^42.99, 2^43.993)
   const int d = sh.least_s - s;
   return d >= 0 && (d > 1 || w << d >= sh.least);
+}
+// Whether min_p leaves x, whose log2w() is y.  All passes ask here: what one counts the others find.
+__device__ __forceinline__ bool min_p_leaves(const Scale& sc, const Shared& sh, float x, float y) {
+  return y >= sc.floor_y && (y >= sc.floor_y + 0x1p-8f || reaches(sc.m, sc.c1, sc.c2, sh, x));
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
@@ -248,7 +252,8 @@ struct Row {
   }
 
   // bf16 has few values: the weights of nearly all that logits take fit a table, and a weight costs a lookup instead of
-  // some 45 instructions (64 rows of 128,000 without limits 45 -> 36 us).
+  // some 45 instructions.  Filled for every row, as it costs little: 64 rows of 128,000 without limits 42 -> 32 us, with
+  // top-p 64 of some 50,000 57.5 -> 54.5, 200 of 32,000 98 -> 95, 200 of 8000 66 -> 67.5, 200 of 500 27 -> 27.5.
   __device__ void fill_table(const Scale& sc) {
     if constexpr (sizeof(T) == 2) {
       for (uint32_t i = threadIdx.x; i < 2 * kTableSize; i += kThreads) {
