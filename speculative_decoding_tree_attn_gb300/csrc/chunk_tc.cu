@@ -15,8 +15,8 @@
 //   tile run while a tile's softmax does.  (One S buffer, freed once it is in
 //   registers, and two for P: 6.0 against 5.7 ms.)
 //   S_0 2 x 64 | S_1 2 x 64 | O_0 128 | O_1 128 columns fill the TMEM; with heads
-//   of 256 a unit is one M tile, S 2 x 64 | O 256 (4 x 512 tokens, 16/4 heads: 59
-//   us, 516 on CUDA cores).
+//   of 256 a unit is one M tile, S 2 x 64 | O 256 (4 x 512 tokens, 16/4 heads: 58
+//   us, 516 on CUDA cores; the softmax warps spill 44-66 bytes there).
 // * Softmax: a thread per row, against a reference that is the first tile's
 //   maximum and moves, with O rescaled in TMEM, only when weights pass 2^20; so
 //   later tiles need no maximum at all (it took a third of a tile's time).  Weights are rounded to bf16 for
@@ -32,7 +32,7 @@
 //
 // Bound by shared memory and the chain of a tile (scores, softmax, outputs, next
 // scores: 1630 cycles, of which the operands' 160 KB take 1250): 8192 tokens
-// behind 24576, 64/8 heads of 128, 5.5-5.7 ms, 0.71-0.73 of the measured bf16
+// behind 24576, 64/8 heads of 128, 5.5-5.6 ms, 0.73-0.75 of the measured bf16
 // rate; by what a unit costs beside its tiles (about four of them) for prompts of
 // a few hundred tokens (32 of 1-1023 tokens: 179 us, 0.29).
 //
@@ -248,8 +248,9 @@ __device__ void make_plan(const ChunkParams& p, const Residues& res, int cost, i
     plan.x1 = x1;
     plan.total = total;
     plan.ctas = ctas;
-    // A cut costs about 15 tiles (the pieces written and read back, the wait for the last), an uneven run up to one unit:
-    // 32 prompts of 1-1023 tokens 202 -> 180 us.
+    // A cut costs about 15 tiles (the pieces written and read back, the wait for the last), an uneven run up to one unit, a
+    // quarter of a run at most.  With units up to 0 | 12 | 24 | 48 tiles whole: 32 prompts of 1-1023 tokens 207 | 192 | 180 |
+    // 180 us, 64 x 256 tokens with heads of 64 104 | 85 | 85 | 85, 8 x 1000 tokens 116 | 116 | 95 | 95.
     plan.whole = (int)min((int64_t)24, divide(total, ctas) / 4);
   }
   __syncthreads();
@@ -623,7 +624,8 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
     const float slope = kAny && p.slopes && valid ? slope_of(p.slopes, head) : 0.f;
     float top = kNoScore, sum = 0.f;
     // The M tiles' softmaxes share the issue slots, their products the tensor pipe: out of step with each other they
-    // share better (a long prompt piece 5.30 -> 5.21 ms; 32 prompts of 512 tokens, with few tiles a unit, 170 -> 174 us).
+    // share better where the tiles are many.  Not at all | from 16 tiles on | from 4: 8192 tokens behind 24576 5.51 | 5.48 |
+    // 5.48 ms, 64 turns 740 | 739 | 738 us, 32 prompts of 512 tokens 119 | 118 | 128 us.
     if (m == 1 && n_mine >= 16) {
       const long long from = clock64();
       while (clock64() - from < 600) {
@@ -708,6 +710,8 @@ __device__ __forceinline__ void run_softmax(const ChunkParams& p, const Plan& pl
       }
       // Weights against the reference as it is.  It may lie below the maximum as long as their sum stays below 2^20:
       // floats do not mind.  Past that, and in a unit's first tile, it becomes the maximum and the weights are taken again.
+      // (Without a bias it seldom moves.  A slope above 0.22 moves it in every tile, as the far keys come first: 8 x 1000
+      // tokens, 32/8 heads of 128, 195 us with the usual slopes, 95 without.)
       const float f = kAny ? 1.f : mul;
       const uint64_t sc2 = pack_f32x2(f, f);
       uint32_t pk[32];

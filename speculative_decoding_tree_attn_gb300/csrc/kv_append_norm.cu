@@ -78,7 +78,9 @@ __device__ __forceinline__ void finish_row(const NormParams& p, const char* w_at
   }
 }
 
-// One warp per (token, slice of its heads), as in kv_append.cu; the warps behind the tokens' count the new lengths.
+// One warp per (token, slice of its heads), as in kv_append.cu; the warps behind the tokens' count the new lengths.  5 CTAs
+// an SM leave 96 registers, of which bf16 spills 24 bytes.  With 4 | 5 | 6: 17k tokens of 32/8 heads of 128 in bf16 109 | 72 |
+// 73 us, 256 such tokens 5.6 | 5.0 | 5.7, 32 float32 prompts of up to 600 88 | 85 | 81.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 5) kv_append_norm_kernel(const __grid_constant__ NormParams np) {
   const AppendParams& p = np.a;
